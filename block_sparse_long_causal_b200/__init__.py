@@ -21,6 +21,8 @@ Entry points mirror the C ABI in include/fp.h:
     paged_cache(...)        -> PagedCache (fp_paged_cache_init: chunked prefill onto a paged K/V cache)
     paged_block_pool / paged_block_search / paged_block_sparse_attn / paged_dense_attn /
     paged_validate_lists    -> the fp_paged_* calls
+    kv_cache(...)           -> KVCache (fp_kv_cache_init: serving from a paged K/V cache)
+    cache_append / cache_attn / cache_select / cache_compact -> the fp_cache_* calls
 and SparsePrefill bundles the three steps with caller-side buffers.
 """
 from __future__ import annotations
@@ -45,7 +47,8 @@ EXPORTED = ("fp_problem_init", "fp_block_pool", "fp_block_search", "fp_block_poo
             "fp_paged_block_pool", "fp_paged_block_search", "fp_paged_block_sparse_attn", "fp_paged_dense_attn",
             "fp_paged_validate_lists", "fp_block_search_topp", "fp_block_sparse_attn_fp8", "fp_dense_attn_fp8",
             "fp_index_buffer_elems", "fp_check_device_status", "fp_key_split_bytes", "fp_block_sparse_attn_fp8_blockscaled",
-            "fp_dense_attn_fp8_blockscaled")
+            "fp_dense_attn_fp8_blockscaled", "fp_kv_cache_init", "fp_cache_append", "fp_cache_attn_workspace",
+            "fp_cache_attn", "fp_cache_select", "fp_cache_compact")
 
 
 class FpError(RuntimeError):
@@ -68,6 +71,12 @@ class fp_paged_cache(C.Structure):
                 ("index_elems", C.c_int64)]
 
 
+class fp_kv_cache(C.Structure):
+    _fields_ = [("k", C.c_void_p), ("v", C.c_void_p), ("weights", C.c_void_p), ("positions", C.c_void_p),
+                ("lens", C.c_void_p), ("block_table", C.c_void_p), ("max_pages", C.c_int32),
+                ("page_size", C.c_int32), ("num_pages", C.c_int32), ("max_len", C.c_int32), ("max_new", C.c_int32)]
+
+
 def _load():
     if not os.path.exists(LIB_PATH):
         raise ImportError(f"libfp.so is not built ({LIB_PATH}); run python block_sparse_long_causal_b200/build.py")
@@ -75,6 +84,8 @@ def _load():
     vp, i32, f32 = C.c_void_p, C.c_int32, C.c_float
     P = C.POINTER(fp_problem)
     PC = C.POINTER(fp_paged_cache)
+    KV = C.POINTER(fp_kv_cache)
+    i64 = C.c_int64
     sig = {
         "fp_paged_cache_init": [PC, P, vp, vp, vp, vp, i32, i32, i32],
         "fp_block_search_topp": [P, vp, vp, f32, vp, vp, vp, vp, vp],
@@ -101,6 +112,12 @@ def _load():
         "fp_index_buffer_elems": [vp, i32, i32, i32, C.POINTER(C.c_int64)],
         "fp_check_device_status": [i32],
         "fp_key_split_bytes": [P, vp, C.POINTER(C.c_int64)],
+        "fp_kv_cache_init": [KV, P, vp, vp, vp, vp, vp, i32, i32, i32, i32],
+        "fp_cache_append": [P, KV, vp, i64, vp, i64, vp, vp, vp],
+        "fp_cache_attn_workspace": [P, KV, C.POINTER(C.c_int64)],
+        "fp_cache_attn": [P, KV, vp, i64, f32, vp, i64, vp, vp, f32, vp, vp],
+        "fp_cache_select": [P, KV, i32, i32, i32, vp, vp, vp, vp, vp, vp],
+        "fp_cache_compact": [P, KV, i32, vp, vp, vp, vp, vp],
     }
     for name, args in sig.items():
         fn = getattr(lib, name)
@@ -374,6 +391,153 @@ def paged_dense_attn(p: Problem, c: PagedCache, q, k_cache, v_cache, softmax_sca
 def paged_validate_lists(p: Problem, c: PagedCache, counts, indices, dev_status, stream=None):
     _check(_lib.fp_paged_validate_lists(p.ref, c.ref, _ptr(counts), _ptr(indices), _ptr(dev_status),
                                         _stream(stream)))
+
+
+def _rows_of(t, name: str, tokens: int, heads: int, d: int, device):
+    """Pointer and token-row stride of a bf16 [tokens, heads, head_dim] tensor whose rows may lie apart (a
+    slice of a fused projection)."""
+    _want(t, name, torch.bfloat16, device)
+    if tuple(t.shape) != (tokens, heads, d):
+        raise ValueError(f"{name} must be [{tokens}, {heads}, {d}], got {list(t.shape)}")
+    if tokens == 0:
+        return None, 0
+    if t.stride(2) != 1 or (heads > 1 and t.stride(1) != d):
+        raise ValueError(f"{name}: the heads of a token must be contiguous")
+    return C.c_void_p(t.data_ptr()), int(t.stride(0)) if tokens > 1 else 0
+
+
+def _want(t, name: str, dtype, device, numel=None):
+    if not isinstance(t, torch.Tensor):
+        raise ValueError(f"{name} must be a tensor")
+    if t.dtype != dtype:
+        raise ValueError(f"{name} must be {dtype}, got {t.dtype}")
+    if t.device != device:
+        raise ValueError(f"{name} is on {t.device}, the cache on {device}")
+    if numel is not None and (t.numel() != numel or not t.is_contiguous()):
+        raise ValueError(f"{name} must be contiguous with {numel} elements")
+    return t
+
+
+class KVCache:
+    """fp_kv_cache for the new tokens of problem p, plus the device tensors that it points to: k_cache
+    and v_cache bf16 [num_pages * page_size, Hkv, d] (or [num_pages, page_size, Hkv, d]), lens int32
+    [num_seqs], block_table int32 [num_seqs, max_pages], optional weights float32 and positions int32
+    [num_pages, Hkv, page_size]. The tensors are used in place: a serving loop keeps one KVCache per
+    problem shape over the same tensors."""
+
+    def __init__(self, p: Problem, k_cache, v_cache, lens, block_table, page_size: int, weights=None, positions=None,
+                 max_len: int = 0):
+        page_size, hkv, d = int(page_size), int(p.num_kv_heads), int(p.head_dim)
+        dev = k_cache.device
+        for name, t in (("k_cache", k_cache), ("v_cache", v_cache)):
+            _want(t, name, torch.bfloat16, dev, k_cache.numel())
+            if t.dim() not in (3, 4) or tuple(t.shape[-2:]) != (hkv, d):
+                raise ValueError(f"{name} must be [num_pages * page_size, {hkv}, {d}]")
+        if page_size < 1 or k_cache.numel() == 0 or k_cache.numel() % (page_size * hkv * d):
+            raise ValueError(f"k_cache must hold whole pages of {page_size} slots")
+        num_pages = k_cache.numel() // (page_size * hkv * d)
+        _want(lens, "lens", torch.int32, dev, p.num_seqs)
+        _want(block_table, "block_table", torch.int32, dev)
+        if block_table.dim() != 2 or block_table.shape[0] != p.num_seqs or not block_table.is_contiguous():
+            raise ValueError("block_table must be contiguous [num_seqs, max_pages]")
+        if p.cu_dev.device != dev:
+            raise ValueError(f"the problem is on {p.cu_dev.device}, the cache on {dev}")
+        for name, t, dt in (("weights", weights, torch.float32), ("positions", positions, torch.int32)):
+            if t is not None:
+                _want(t, name, dt, dev, num_pages * hkv * page_size)
+        self.p, self.device = p, dev
+        self.k, self.v, self.lens, self.table = k_cache, v_cache, lens, block_table
+        self.weights, self.positions = weights, positions
+        self.c = fp_kv_cache()
+        _check(_lib.fp_kv_cache_init(C.byref(self.c), p.ref, p.cu_host.ctypes.data_as(C.c_void_p), _ptr(k_cache),
+                                     _ptr(v_cache), _ptr(lens), _ptr(block_table), int(block_table.shape[1]),
+                                     page_size, num_pages, int(max_len)))
+        if weights is not None:
+            self.c.weights = weights.data_ptr()
+        if positions is not None:
+            self.c.positions = positions.data_ptr()
+
+    def __getattr__(self, name):
+        return getattr(self.__dict__["c"], name)
+
+    @property
+    def ref(self):
+        return C.byref(self.c)
+
+
+def kv_cache(p: Problem, k_cache, v_cache, lens, block_table, page_size: int, weights=None, positions=None,
+             max_len: int = 0) -> KVCache:
+    return KVCache(p, k_cache, v_cache, lens, block_table, page_size, weights, positions, max_len)
+
+
+def _cache_args(p: Problem, c: KVCache, next_pos, dev_status):
+    if p is not c.p:
+        raise ValueError("the cache was described for another problem (kv_cache(p, ...))")
+    for name, t, n in (("next_pos", next_pos, p.num_seqs), ("dev_status", dev_status, 1)):
+        if t is not None:
+            _want(t, name, torch.int32, c.device, n)
+
+
+def _call(c: KVCache, fn, *args, stream):
+    """fn on the cache's device, on `stream` or that device's current one."""
+    with torch.cuda.device(c.device):
+        _check(fn(*args, _stream(stream)))
+
+
+def cache_append(p: Problem, c: KVCache, k, v, next_pos=None, dev_status=None, stream=None):
+    """fp_cache_append: the new tokens' K and V rows into their slots."""
+    _cache_args(p, c, next_pos, dev_status)
+    kp, ks = _rows_of(k, "k", p.total_tokens, p.num_kv_heads, p.head_dim, c.device)
+    vp, vs = _rows_of(v, "v", p.total_tokens, p.num_kv_heads, p.head_dim, c.device)
+    _call(c, _lib.fp_cache_append, p.ref, c.ref, kp, ks, vp, vs, _ptr(next_pos), _ptr(dev_status), stream=stream)
+
+
+def cache_attn_workspace(p: Problem, c: KVCache) -> int:
+    n = C.c_int64(0)
+    with torch.cuda.device(c.device):
+        _check(_lib.fp_cache_attn_workspace(p.ref, c.ref, C.byref(n)))
+    return int(n.value)
+
+
+def cache_attn(p: Problem, c: KVCache, q, softmax_scale: float, workspace, out, lse=None, decay=None, dev_status=None,
+               stream=None):
+    """fp_cache_attn; decay None leaves the cache's weights alone."""
+    _cache_args(p, c, None, dev_status)
+    qp, qs = _rows_of(q, "q", p.total_tokens, p.num_q_heads, p.head_dim, c.device)
+    _want(out, "out", torch.bfloat16, c.device, p.total_tokens * p.num_q_heads * p.head_dim)
+    if lse is not None:
+        _want(lse, "lse", torch.float32, c.device, p.total_tokens * p.num_q_heads)
+    if workspace.device != c.device:
+        raise ValueError(f"workspace is on {workspace.device}, the cache on {c.device}")
+    if decay is not None and not 0.0 <= decay <= 1.0:
+        raise ValueError("decay must be in [0, 1]")
+    _call(c, _lib.fp_cache_attn, p.ref, c.ref, qp, qs, float(softmax_scale), _ptr(workspace),
+          workspace.numel() * workspace.element_size(), _ptr(out), _ptr(lse), -1.0 if decay is None else float(decay),
+          _ptr(dev_status), stream=stream)
+
+
+def _move_args(p: Problem, c: KVCache, budget: int, moves, move_counts, new_lens):
+    n = p.num_seqs * p.num_kv_heads
+    _want(moves, "moves", torch.int32, c.device, 2 * n * budget)
+    _want(move_counts, "move_counts", torch.int32, c.device, n)
+    _want(new_lens, "new_lens", torch.int32, c.device, p.num_seqs)
+
+
+def cache_select(p: Problem, c: KVCache, budget: int, sinks: int, recent: int, next_pos, moves, move_counts, new_lens,
+                 dev_status=None, stream=None):
+    """fp_cache_select: the slots that stay, as moves int32 [num_seqs, Hkv, budget, 2]."""
+    _cache_args(p, c, next_pos, dev_status)
+    _move_args(p, c, int(budget), moves, move_counts, new_lens)
+    _call(c, _lib.fp_cache_select, p.ref, c.ref, int(budget), int(sinks), int(recent), _ptr(next_pos), _ptr(moves),
+          _ptr(move_counts), _ptr(new_lens), _ptr(dev_status), stream=stream)
+
+
+def cache_compact(p: Problem, c: KVCache, budget: int, moves, move_counts, new_lens, dev_status=None, stream=None):
+    """fp_cache_compact: apply the moves of cache_select and set lens."""
+    _cache_args(p, c, None, dev_status)
+    _move_args(p, c, int(budget), moves, move_counts, new_lens)
+    _call(c, _lib.fp_cache_compact, p.ref, c.ref, int(budget), _ptr(moves), _ptr(move_counts), _ptr(new_lens),
+          _ptr(dev_status), stream=stream)
 
 
 class SparsePrefill:

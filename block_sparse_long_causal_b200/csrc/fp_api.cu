@@ -644,6 +644,215 @@ fp_status fp_paged_validate_lists(const fp_problem* p, const fp_paged_cache* c, 
   return validate_impl(p, c, counts, indices, dev_status, stream);
 }
 
+// ---- serving from a paged key/value cache
+namespace {
+fp_status check_kv(const fp_problem* p, const fp_kv_cache* c) {
+  fp_status st = check_problem(p);
+  if (st != FP_OK) return st;
+  if (!c) return fail(FP_ERR_INVALID_ARG, "cache is NULL");
+  if (!c->k || !c->v || !c->lens || !c->block_table)
+    return fail(FP_ERR_INVALID_ARG, "cache.k, v, lens and block_table must be non-NULL (use fp_kv_cache_init)");
+  if (!aligned16(c->k) || !aligned16(c->v) || !aligned16(c->weights) || !aligned16(c->positions))
+    return fail(FP_ERR_INVALID_ARG, "cache.k, v, weights and positions must be 16-byte aligned");
+  if (c->page_size < 16 || c->page_size % 16 || c->max_pages < 1 || c->num_pages < 1 || c->max_new < 0 ||
+      c->max_len < c->max_new || (int64_t)c->max_pages * c->page_size < c->max_len ||
+      (int64_t)c->num_pages * c->page_size > (int64_t)INT32_MAX)
+    return fail(FP_ERR_INVALID_ARG, "inconsistent key/value cache (use fp_kv_cache_init)");
+  return FP_OK;
+}
+
+fp::CacheInfo cache_info(const fp_problem* p, const fp_kv_cache* c) {
+  fp::CacheInfo a;
+  memset(&a, 0, sizeof a);
+  a.cu_seqlens = p->cu_seqlens;
+  a.lens = c->lens;
+  a.block_table = c->block_table;
+  a.num_seqs = p->num_seqs;
+  a.total_tokens = p->total_tokens;
+  a.max_pages = c->max_pages;
+  a.page_size = c->page_size;
+  a.num_pages = c->num_pages;
+  a.max_len = c->max_len;
+  a.max_new = c->max_new;
+  a.hq = p->num_q_heads;
+  a.hkv = p->num_kv_heads;
+  a.group = p->num_q_heads / p->num_kv_heads;
+  a.k = static_cast<uint16_t*>(c->k);
+  a.v = static_cast<uint16_t*>(c->v);
+  a.weights = c->weights;
+  a.positions = c->positions;
+  return a;
+}
+
+// 0 selects the packed row; otherwise rows must not overlap and must stay 16-byte aligned
+fp_status row_stride(const char* name, int64_t given, int64_t packed, int64_t* out) {
+  if (given != 0 && (given < packed || given % 8))
+    return fail(FP_ERR_INVALID_ARG, "%s=%lld must be 0 or a multiple of 8 of at least %lld elements", name,
+                (long long)given, (long long)packed);
+  *out = given ? given : packed;
+  return FP_OK;
+}
+
+fp_status check_budget(int32_t budget, const int32_t* moves, const int32_t* counts, const int32_t* new_lens) {
+  if (budget < 1) return fail(FP_ERR_INVALID_ARG, "budget=%d must be >= 1", budget);
+  if (!moves || !counts || !new_lens)
+    return fail(FP_ERR_INVALID_ARG, "moves, move_counts and new_lens must be non-NULL");
+  if ((reinterpret_cast<uintptr_t>(moves) & 7u) != 0)
+    return fail(FP_ERR_INVALID_ARG, "moves must be 8-byte aligned");
+  return FP_OK;
+}
+}  // namespace
+
+fp_status fp_kv_cache_init(fp_kv_cache* c, const fp_problem* p, const int32_t* host_cu_seqlens, void* k, void* v,
+                           int32_t* dev_lens, const int32_t* dev_block_table, int32_t max_pages, int32_t page_size,
+                           int32_t num_pages, int32_t max_len) {
+  fp_status st = check_problem(p);
+  if (st != FP_OK) return st;
+  if (!c || !host_cu_seqlens || !k || !v || !dev_lens || !dev_block_table)
+    return fail(FP_ERR_INVALID_ARG, "NULL argument to fp_kv_cache_init");
+  if (page_size <= 0 || page_size % 16)
+    return fail(FP_ERR_UNSUPPORTED, "page_size=%d must be a positive multiple of 16", page_size);
+  if (max_pages < 1 || num_pages < 1) return fail(FP_ERR_INVALID_ARG, "max_pages and num_pages must be >= 1");
+  if ((int64_t)num_pages * page_size > (int64_t)INT32_MAX)
+    return fail(FP_ERR_INVALID_ARG, "num_pages * page_size exceeds 2^31 - 1 rows");
+  const int64_t room = (int64_t)max_pages * page_size;
+  if (max_len < 0 || max_len > room)
+    return fail(FP_ERR_INVALID_ARG, "max_len=%d outside [0, max_pages * page_size = %lld]", max_len, (long long)room);
+  if (host_cu_seqlens[p->num_seqs] != p->total_tokens)
+    return fail(FP_ERR_INVALID_ARG, "host_cu_seqlens does not match the problem");
+  int64_t max_new = 0;
+  for (int s = 0; s < p->num_seqs; ++s) {
+    const int64_t L = (int64_t)host_cu_seqlens[s + 1] - host_cu_seqlens[s];
+    if (L < 0) return fail(FP_ERR_INVALID_ARG, "cu_seqlens must be non-decreasing (sequence %d)", s);
+    if (L > max_new) max_new = L;
+  }
+  // rooms past 2^30 slots are never filled (num_pages bounds the rows), and key positions stay in int32
+  const int64_t bound = max_len ? max_len : (room < (1 << 30) ? room : (1 << 30));
+  if (max_new > bound)
+    return fail(FP_ERR_INVALID_ARG, "%lld new tokens exceed max_len=%lld", (long long)max_new, (long long)bound);
+  fp_kv_cache n;
+  memset(&n, 0, sizeof n);
+  n.k = k;
+  n.v = v;
+  n.lens = dev_lens;
+  n.block_table = dev_block_table;
+  n.max_pages = max_pages;
+  n.page_size = page_size;
+  n.num_pages = num_pages;
+  n.max_len = (int32_t)bound;
+  n.max_new = (int32_t)max_new;
+  if ((st = check_kv(p, &n)) != FP_OK) return st;
+  *c = n;
+  return FP_OK;
+}
+
+fp_status fp_cache_append(const fp_problem* p, const fp_kv_cache* c, const void* k, int64_t k_stride, const void* v,
+                          int64_t v_stride, const int32_t* next_pos, int32_t* dev_status, void* stream) {
+  fp_status st = check_kv(p, c);
+  if (st != FP_OK) return st;
+  fp::AppendParams a;
+  memset(&a, 0, sizeof a);
+  const int64_t packed = (int64_t)p->num_kv_heads * p->head_dim;
+  if ((st = row_stride("k_stride", k_stride, packed, &a.k_stride)) != FP_OK) return st;
+  if ((st = row_stride("v_stride", v_stride, packed, &a.v_stride)) != FP_OK) return st;
+  if (p->total_tokens == 0) return FP_OK;
+  if (!k || !v) return fail(FP_ERR_INVALID_ARG, "k and v must be non-NULL");
+  if (!aligned16(k) || !aligned16(v)) return fail(FP_ERR_INVALID_ARG, "k and v must be 16-byte aligned");
+  a.c = cache_info(p, c);
+  a.k = static_cast<const uint16_t*>(k);
+  a.v = static_cast<const uint16_t*>(v);
+  a.next_pos = next_pos;
+  a.dev_status = dev_status;
+  return cuda_status(fp::launch_append(a, static_cast<cudaStream_t>(stream)), "append launch");
+}
+
+fp_status fp_cache_attn_workspace(const fp_problem* p, const fp_kv_cache* c, int64_t* bytes) {
+  fp_status st = check_kv(p, c);
+  if (st != FP_OK) return st;
+  if (!bytes) return fail(FP_ERR_INVALID_ARG, "bytes must be non-NULL");
+  *bytes = fp::cache_attn_layout(sm_count(), p->num_q_heads, p->total_tokens).total;
+  return FP_OK;
+}
+
+fp_status fp_cache_attn(const fp_problem* p, const fp_kv_cache* c, const void* q, int64_t q_stride, float softmax_scale,
+                        void* workspace, int64_t workspace_bytes, void* out, float* lse, float decay,
+                        int32_t* dev_status, void* stream) {
+  fp_status st = check_kv(p, c);
+  if (st != FP_OK) return st;
+  fp::CacheAttnParams a;
+  memset(&a, 0, sizeof a);
+  if ((st = row_stride("q_stride", q_stride, (int64_t)p->num_q_heads * p->head_dim, &a.q_stride)) != FP_OK) return st;
+  if (!std::isfinite(softmax_scale)) return fail(FP_ERR_INVALID_ARG, "softmax_scale is not finite");
+  if (!(decay <= 1.f)) return fail(FP_ERR_INVALID_ARG, "decay must be at most 1 (negative: no weights)");
+  if (decay >= 0.f && !c->weights) return fail(FP_ERR_INVALID_ARG, "decay >= 0 needs cache.weights");
+  if (p->total_tokens == 0) return FP_OK;
+  if (!q || !out) return fail(FP_ERR_INVALID_ARG, "q and out must be non-NULL");
+  if (!aligned16(q) || !aligned16(out)) return fail(FP_ERR_INVALID_ARG, "q and out must be 16-byte aligned");
+  const int sms = sm_count();
+  const fp::CacheAttnLayout w = fp::cache_attn_layout(sms, p->num_q_heads, p->total_tokens);
+  if (!workspace) return fail(FP_ERR_INVALID_ARG, "workspace must be non-NULL");
+  if ((reinterpret_cast<uintptr_t>(workspace) & 255u) != 0)
+    return fail(FP_ERR_INVALID_ARG, "workspace must be 256-byte aligned");
+  if (workspace_bytes < w.total)
+    return fail(FP_ERR_INVALID_ARG, "workspace of %lld bytes is smaller than the %lld bytes needed",
+                (long long)workspace_bytes, (long long)w.total);
+  char* base = static_cast<char*>(workspace);
+  const float scale = softmax_scale > 0.f ? softmax_scale : 1.0f / std::sqrt((float)p->head_dim);
+  a.c = cache_info(p, c);
+  a.q = static_cast<const uint16_t*>(q);
+  a.scale_log2 = scale * 1.4426950408889634f;
+  a.out = static_cast<uint16_t*>(out);
+  a.lse = lse;
+  a.lse2 = reinterpret_cast<float*>(base + w.lse2);
+  a.part_o = reinterpret_cast<float*>(base + w.part_o);
+  a.part_ml = reinterpret_cast<float*>(base + w.part_ml);
+  a.meta = reinterpret_cast<int32_t*>(base + w.meta);
+  a.decay = decay;
+  a.dev_status = dev_status;
+  a.wait_limit_ns = wait_limit_ns();
+  return cuda_status(fp::launch_cache_attn(a, sms, static_cast<cudaStream_t>(stream)), "cache attention launch");
+}
+
+fp_status fp_cache_select(const fp_problem* p, const fp_kv_cache* c, int32_t budget, int32_t sinks, int32_t recent,
+                          const int32_t* next_pos, int32_t* moves, int32_t* move_counts, int32_t* new_lens,
+                          int32_t* dev_status, void* stream) {
+  fp_status st = check_kv(p, c);
+  if (st != FP_OK) return st;
+  if ((st = check_budget(budget, moves, move_counts, new_lens)) != FP_OK) return st;
+  if (sinks < 0 || recent < 0 || (int64_t)sinks + recent > budget)
+    return fail(FP_ERR_INVALID_ARG, "sinks=%d and recent=%d must be non-negative with a sum of at most budget=%d",
+                sinks, recent, budget);
+  if (!c->weights) return fail(FP_ERR_INVALID_ARG, "selection needs cache.weights");
+  fp::SelectParams a;
+  memset(&a, 0, sizeof a);
+  a.c = cache_info(p, c);
+  a.budget = budget;
+  a.sinks = sinks;
+  a.recent = recent;
+  a.next_pos = next_pos;
+  a.moves = moves;
+  a.move_counts = move_counts;
+  a.new_lens = new_lens;
+  a.dev_status = dev_status;
+  return cuda_status(fp::launch_select(a, static_cast<cudaStream_t>(stream)), "selection launch");
+}
+
+fp_status fp_cache_compact(const fp_problem* p, const fp_kv_cache* c, int32_t budget, const int32_t* moves,
+                           const int32_t* move_counts, const int32_t* new_lens, int32_t* dev_status, void* stream) {
+  fp_status st = check_kv(p, c);
+  if (st != FP_OK) return st;
+  if ((st = check_budget(budget, moves, move_counts, new_lens)) != FP_OK) return st;
+  fp::CompactParams a;
+  memset(&a, 0, sizeof a);
+  a.c = cache_info(p, c);
+  a.budget = budget;
+  a.moves = moves;
+  a.move_counts = move_counts;
+  a.new_lens = new_lens;
+  a.dev_status = dev_status;
+  return cuda_status(fp::launch_compact(a, static_cast<cudaStream_t>(stream)), "compaction launch");
+}
+
 fp_status fp_selftest_exp2(const float* x, float* y_poly, float* y_mufu, int64_t n, void* stream) {
   if (n < 0 || (n > 0 && (!x || !y_poly || !y_mufu)))
     return fail(FP_ERR_INVALID_ARG, "x, y_poly and y_mufu must be non-NULL for n > 0");
@@ -653,6 +862,6 @@ fp_status fp_selftest_exp2(const float* x, float* y_poly, float* y_mufu, int64_t
 
 const char* fp_last_error(void) { return g_err; }
 
-int32_t fp_version(void) { return 500; }
+int32_t fp_version(void) { return 600; }
 
 }  // extern "C"

@@ -109,6 +109,67 @@ struct __align__(64) AttnParams {
   const int8_t* k_exp;            // and key-block scale 2^k_exp[global block * hkv + g]
 };
 
+// A key/value cache and the chunk of new tokens that a call works on (fp_kv_cache with fp_problem).
+struct CacheInfo {
+  const int32_t* cu_seqlens;  // device [S+1], the new tokens
+  int32_t* lens;              // device [S], slots in use before the new tokens
+  const int32_t* block_table; // device [S, max_pages]
+  int32_t num_seqs, total_tokens;
+  int32_t max_pages, page_size, num_pages;
+  int32_t max_len;            // bound of lens[s] + L_s
+  int32_t max_new;            // bound of L_s
+  int32_t hq, hkv, group;
+  uint16_t* k;                // [num_pages * page_size, Hkv, d] bf16 bits
+  uint16_t* v;
+  float* weights;             // [num_pages, Hkv, page_size] or null
+  int32_t* positions;         // likewise
+};
+
+struct AppendParams {
+  CacheInfo c;
+  const uint16_t* k;          // [T, Hkv, d], rows k_stride elements apart
+  const uint16_t* v;
+  int64_t k_stride, v_stride;
+  const int32_t* next_pos;    // device [S] or null (the slot is the position)
+  int32_t* dev_status;
+};
+
+struct CacheAttnParams {
+  CacheInfo c;
+  const uint16_t* q;          // [T, Hq, d], rows q_stride elements apart
+  int64_t q_stride;
+  float scale_log2;           // softmax_scale * log2(e)
+  uint16_t* out;              // [T, Hq, d] bf16 bits
+  float* lse;                 // [Hq, T] or null (natural log)
+  float* lse2;                // [Hq, T] workspace, log2 units (for the weights)
+  float* part_o;              // workspace: partial outputs [2 * grid][rows][128], not normalised
+  float* part_ml;             // workspace: their running max (log2 units) and row sum [2 * grid][2][rows]
+  int32_t* meta;              // workspace: the unit that each CTA's range begins inside of [grid][kMetaWords]
+  float decay;                // weights = decay * weights + this call's; < 0: weights are left alone
+  int32_t* dev_status;
+  uint64_t wait_limit_ns;
+};
+
+struct SelectParams {
+  CacheInfo c;
+  int32_t budget, sinks, recent;
+  const int32_t* next_pos;    // device [S] or null
+  int32_t* moves;             // [S, Hkv, budget, 2]
+  int32_t* move_counts;       // [S, Hkv]
+  int32_t* new_lens;          // [S]
+  int32_t* dev_status;
+};
+
+struct CompactParams {
+  CacheInfo c;
+  int32_t budget;
+  const int32_t* moves;
+  const int32_t* move_counts;
+  const int32_t* new_lens;
+  int32_t parts;              // CTAs per (sequence, kv-head), set by the launcher
+  int32_t* dev_status;
+};
+
 constexpr int kMaxSeqs = FP_MAX_SEQS;
 constexpr int kHeadDim = 128;
 constexpr int kTileM = 128;   // query rows per attention tile
@@ -134,6 +195,16 @@ cudaError_t launch_validate(const ValidateParams& p, cudaStream_t st);
 // Cumulative top-p selection (comparison selector): scores scratch [index_elems] floats.
 cudaError_t launch_topp(const SearchParams& p, float gamma, float* scores, cudaStream_t st);
 cudaError_t launch_attn(const AttnParams& p, int grid, cudaStream_t st);
+// Key/value cache (fp_cache.cu, fp_cache_attn.cu).
+cudaError_t launch_append(const AppendParams& p, cudaStream_t st);
+cudaError_t launch_select(const SelectParams& p, cudaStream_t st);
+cudaError_t launch_compact(const CompactParams& p, cudaStream_t st);
+int cache_attn_grid(int sms);               // CTAs of the attention launch on a device of sms SMs
+struct CacheAttnLayout {                    // byte offsets of its workspace
+  int64_t part_o, part_ml, meta, lse2, total;
+};
+CacheAttnLayout cache_attn_layout(int sms, int64_t hq, int64_t total_tokens);
+cudaError_t launch_cache_attn(const CacheAttnParams& p, int sms, cudaStream_t st);
 cudaError_t launch_exp2_selftest(const float* x, float* y_poly, float* y_mufu, long long n, cudaStream_t st);
 
 }  // namespace fp

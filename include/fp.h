@@ -318,6 +318,100 @@ FP_API fp_status fp_paged_dense_attn(const fp_problem* p, const fp_paged_cache* 
 FP_API fp_status fp_paged_validate_lists(const fp_problem* p, const fp_paged_cache* c, const int32_t* counts,
                                          const int32_t* indices, int32_t* dev_status, void* stream);
 
+/* ---------------------------------------------------------------------------------------------
+ * Serving from a paged key/value cache: after the prompt, new tokens are appended, attended over the
+ * whole cache, and the cache is kept within a budget by the attention weight that its slots collect.
+ * The cache arrays and the block table are those of the chunked prefill above (k and v bf16
+ * [num_pages * page_size, Hkv, d]), so a prompt prefilled there is served from here, but nothing is tied
+ * to blocks: the slots in use may be any number, and page_size any positive multiple of 16.
+ *   - fp_problem describes the new tokens of a call (cu_seqlens over L_s of them for sequence s; 0 is
+ *     allowed; its block_size, sched and key_split are not used).
+ *   - lens[s] (device) is the number of slots that sequence s uses before the new tokens: new token t
+ *     sits in slot lens[s] + t and sees the slots 0 .. lens[s] + t. Slot u lives in page
+ *     block_table[s * max_pages + u / page_size] at row u % page_size. The slots of a sequence hold any
+ *     subset of its past tokens in any order (softmax attention has no order); a sequence's pages
+ *     must not be another's when a call writes to them (append, weights, compaction).
+ *   - weights (optional, device float32 [num_pages, Hkv, page_size]): attention weight that a slot has
+ *     collected in a kv-head. positions (optional, device int32, same layout): the token's position in
+ *     its sequence, which eviction uses to tell sinks and recent tokens once slots were compacted.
+ *     next_pos[s] (device, optional) is the position of the sequence's first new token; NULL: slot and
+ *     position are the same.
+ *   - lens lives on the device so that a captured graph can be replayed as the sequences grow; the host
+ *     promises max_len >= lens[s] + L_s (0 in fp_kv_cache_init: max_pages * page_size).
+ * A step is: fp_cache_append, fp_cache_attn, then either fp_cache_select + fp_cache_compact (which sets
+ * lens) or lens[s] += L_s by the caller; next_pos[s] += L_s by the caller.
+ * Device arrays that disagree with this description (lens[s] + L_s > max_len, cu_seqlens other than
+ * the host's) set FP_DEV_BAD_PROBLEM: fp_cache_attn then does no work, the others skip that sequence.
+ * A block-table entry outside [0, num_pages) sets it too; attention reads that page as zeros, and the
+ * calls that write skip its slots (selection ranks them lowest). Slots past a sequence's last one may
+ * hold anything, NaN included; the slots in use are read as numbers, so a non-finite value of one
+ * reaches every row that attends it, and a non-finite V also the rows before it in its chunk. */
+typedef struct fp_kv_cache {
+  void* k;                    /* device bf16 [num_pages * page_size, Hkv, d], 16-byte aligned */
+  void* v;
+  float* weights;             /* see above; NULL after init */
+  int32_t* positions;         /* see above; NULL after init */
+  int32_t* lens;              /* device [num_seqs] */
+  const int32_t* block_table; /* device [num_seqs, max_pages] */
+  int32_t max_pages;          /* row length of block_table */
+  int32_t page_size;          /* slots per page; a positive multiple of 16 */
+  int32_t num_pages;          /* pages in k / v */
+  int32_t max_len;            /* upper bound of lens[s] + L_s */
+  int32_t max_new;            /* max_s L_s */
+} fp_kv_cache;
+
+/* Fill *c for problem p (the new tokens) from a HOST copy of cu_seqlens (read only during the call) and
+ * the device arrays. page_size that is no multiple of 16: FP_ERR_UNSUPPORTED. */
+FP_API fp_status fp_kv_cache_init(fp_kv_cache* c, const fp_problem* p, const int32_t* host_cu_seqlens, void* k,
+                                  void* v, int32_t* dev_lens, const int32_t* dev_block_table, int32_t max_pages,
+                                  int32_t page_size, int32_t num_pages, int32_t max_len);
+
+/* Write the new tokens' keys and values into the cache: k and v are device bf16 [total_tokens, Hkv, d]
+ * whose token rows lie k_stride / v_stride elements apart (0: Hkv * d; otherwise at least that and a
+ * multiple of 8, so a slice of a fused projection needs no copy). Their slots' weights become 0 and
+ * their positions next_pos[s] + t (each where the cache has the array). lens is left alone. */
+FP_API fp_status fp_cache_append(const fp_problem* p, const fp_kv_cache* c, const void* k, int64_t k_stride,
+                                 const void* v, int64_t v_stride, const int32_t* next_pos, int32_t* dev_status,
+                                 void* stream);
+
+/* Bytes of workspace that fp_cache_attn needs (for the current device). */
+FP_API fp_status fp_cache_attn_workspace(const fp_problem* p, const fp_kv_cache* c, int64_t* bytes);
+
+/* Attention of the new tokens over the cache (dense: every slot 0 .. lens[s] + t), for one token per
+ * sequence up to whole prompts, the new tokens' own keys and values among the slots (fp_cache_append
+ * first). q: device bf16 [total_tokens, Hq, d] with token rows q_stride elements apart (0: Hq * d;
+ * otherwise at least that and a multiple of 8). out / lse / softmax_scale as for fp_block_sparse_attn.
+ * decay < 0: the cache's weights are left alone. decay in [0, 1]: for every slot u in use of every
+ * sequence with new tokens and every kv-head g,
+ *   weights[u, g] = decay * weights[u, g] + sum over the new tokens t and q-heads h of g that see u of
+ *                   exp(softmax_scale * q_th . k_u - lse_th)
+ * (1: the weight collected so far; 0: that of this call alone, the old value is not read).
+ * workspace: device, 256-byte aligned, scratch (calls that may run at the same time must not share it).
+ * The result of a call does not depend on timing: the work's split is a function of the lengths. */
+FP_API fp_status fp_cache_attn(const fp_problem* p, const fp_kv_cache* c, const void* q, int64_t q_stride,
+                               float softmax_scale, void* workspace, int64_t workspace_bytes, void* out, float* lse,
+                               float decay, int32_t* dev_status, void* stream);
+
+/* Choose the `budget` slots of every (sequence, kv-head) that stay, of the lens[s] + L_s in use after the
+ * new tokens. Slots whose position is below `sinks`, or among the last `recent` positions (at or past
+ * next_pos[s] + L_s - recent), rank first; then the larger weight; equal ones by the lower slot (-0
+ * counts as 0, NaN ranks below every number). 0 <= sinks, 0 <= recent, sinks + recent <= budget.
+ * The result is a list of moves that makes the slots 0 .. budget - 1 the ones that stay: the i-th kept
+ * slot at or past the budget goes to the i-th evicted slot below it (both ascending).
+ * moves: device int32 [num_seqs, Hkv, budget, 2], (source, destination), entries past the count are -1;
+ * move_counts: device int32 [num_seqs, Hkv]; new_lens: device int32 [num_seqs], min(lens + L, budget).
+ * Reads the cache's weights (required) and positions (if any); changes nothing of the cache. */
+FP_API fp_status fp_cache_select(const fp_problem* p, const fp_kv_cache* c, int32_t budget, int32_t sinks,
+                                 int32_t recent, const int32_t* next_pos, int32_t* moves, int32_t* move_counts,
+                                 int32_t* new_lens, int32_t* dev_status, void* stream);
+
+/* Apply the moves of fp_cache_select (same budget) to K, V, weights and positions, and set
+ * lens[s] = new_lens[s]. Moves that are not from [budget, max_len) to [0, budget) are skipped and set
+ * FP_DEV_BAD_LIST; sources are left as they were. */
+FP_API fp_status fp_cache_compact(const fp_problem* p, const fp_kv_cache* c, int32_t budget, const int32_t* moves,
+                                  const int32_t* move_counts, const int32_t* new_lens, int32_t* dev_status,
+                                  void* stream);
+
 /* Largest intermediate size (bytes) fp_sparse_prefill_noalloc handles: 64 MiB. */
 #define FP_NOALLOC_MAX_BYTES (64ll << 20)
 
