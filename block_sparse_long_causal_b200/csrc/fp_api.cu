@@ -693,6 +693,21 @@ fp_status row_stride(const char* name, int64_t given, int64_t packed, int64_t* o
   return FP_OK;
 }
 
+// q as [tokens][heads][128], boxes of 64 columns x `group` heads x `tile_tokens` tokens (128-byte swizzle)
+fp_status make_q_tmap(CUtensorMap* m, const void* base, int64_t tokens, int64_t heads, int64_t stride, int group,
+                      int tile_tokens) {
+  EncodeTiledFn fn = encode_fn();
+  if (!fn) return fail(FP_ERR_CUDA, "cuTensorMapEncodeTiled is unavailable");
+  cuuint64_t dims[3] = {128, (cuuint64_t)heads, (cuuint64_t)tokens};
+  cuuint64_t strides[2] = {256, (cuuint64_t)stride * 2};
+  cuuint32_t box[3] = {64, (cuuint32_t)group, (cuuint32_t)tile_tokens}, estr[3] = {1, 1, 1};
+  CUresult r = fn(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void*>(base), dims, strides, box, estr,
+                  CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                  CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  if (r != CUDA_SUCCESS) return fail(FP_ERR_CUDA, "cuTensorMapEncodeTiled failed (%d)", (int)r);
+  return FP_OK;
+}
+
 fp_status check_budget(int32_t budget, const int32_t* moves, const int32_t* counts, const int32_t* new_lens) {
   if (budget < 1) return fail(FP_ERR_INVALID_ARG, "budget=%d must be >= 1", budget);
   if (!moves || !counts || !new_lens)
@@ -770,7 +785,8 @@ fp_status fp_cache_attn_workspace(const fp_problem* p, const fp_kv_cache* c, int
   fp_status st = check_kv(p, c);
   if (st != FP_OK) return st;
   if (!bytes) return fail(FP_ERR_INVALID_ARG, "bytes must be non-NULL");
-  *bytes = fp::cache_attn_layout(sm_count(), p->num_q_heads, p->total_tokens).total;
+  const bool tiled = fp::cache_attn_tiled(c->max_new, p->num_q_heads / p->num_kv_heads);
+  *bytes = fp::cache_attn_layout(sm_count(), tiled, p->num_q_heads, p->total_tokens).total;
   return FP_OK;
 }
 
@@ -789,7 +805,9 @@ fp_status fp_cache_attn(const fp_problem* p, const fp_kv_cache* c, const void* q
   if (!q || !out) return fail(FP_ERR_INVALID_ARG, "q and out must be non-NULL");
   if (!aligned16(q) || !aligned16(out)) return fail(FP_ERR_INVALID_ARG, "q and out must be 16-byte aligned");
   const int sms = sm_count();
-  const fp::CacheAttnLayout w = fp::cache_attn_layout(sms, p->num_q_heads, p->total_tokens);
+  const int group = p->num_q_heads / p->num_kv_heads;
+  const bool tiled = fp::cache_attn_tiled(c->max_new, group);
+  const fp::CacheAttnLayout w = fp::cache_attn_layout(sms, tiled, p->num_q_heads, p->total_tokens);
   if (!workspace) return fail(FP_ERR_INVALID_ARG, "workspace must be non-NULL");
   if ((reinterpret_cast<uintptr_t>(workspace) & 255u) != 0)
     return fail(FP_ERR_INVALID_ARG, "workspace must be 256-byte aligned");
@@ -803,14 +821,25 @@ fp_status fp_cache_attn(const fp_problem* p, const fp_kv_cache* c, const void* q
   a.scale_log2 = scale * 1.4426950408889634f;
   a.out = static_cast<uint16_t*>(out);
   a.lse = lse;
-  a.lse2 = reinterpret_cast<float*>(base + w.lse2);
+  a.lse2 = decay >= 0.f ? reinterpret_cast<float*>(base + w.lse2) : nullptr;
   a.part_o = reinterpret_cast<float*>(base + w.part_o);
   a.part_ml = reinterpret_cast<float*>(base + w.part_ml);
   a.meta = reinterpret_cast<int32_t*>(base + w.meta);
   a.decay = decay;
   a.dev_status = dev_status;
   a.wait_limit_ns = wait_limit_ns();
-  return cuda_status(fp::launch_cache_attn(a, sms, static_cast<cudaStream_t>(stream)), "cache attention launch");
+  if (tiled) {
+    a.tile_tokens = 128 / group;
+    a.box_rows = 128;
+    while (c->page_size % a.box_rows) a.box_rows /= 2;
+    const int64_t rows = (int64_t)c->num_pages * c->page_size, cols = (int64_t)p->num_kv_heads * p->head_dim;
+    if ((st = make_tmap(&a.tm_k, c->k, rows, cols, a.box_rows)) != FP_OK) return st;
+    if ((st = make_tmap(&a.tm_v, c->v, rows, cols, a.box_rows)) != FP_OK) return st;
+    if ((st = make_q_tmap(&a.tm_q, q, p->total_tokens, p->num_q_heads, a.q_stride, group, a.tile_tokens)) != FP_OK)
+      return st;
+  }
+  return cuda_status(fp::launch_cache_attn(a, tiled, sms, static_cast<cudaStream_t>(stream)),
+                     "cache attention launch");
 }
 
 fp_status fp_cache_select(const fp_problem* p, const fp_kv_cache* c, int32_t budget, int32_t sinks, int32_t recent,

@@ -1,11 +1,34 @@
 // fp_cache.cuh -- what the key/value cache kernels share: the launch description of a cache, page
 // look-up and the per-launch tables that turn a work index into (sequence, unit).
 #pragma once
+#include <type_traits>
+
 #include "fp_dev.cuh"
 #include "fp_internal.h"
 #include "fp_seq.cuh"
 
 namespace fp {
+
+// Programmatic dependent launch: a kernel that was launched with launch_pdl may start while the one before
+// it on the stream still runs; pdl_wait returns once that one has ended and its writes are visible.
+// pdl_trigger, in the earlier kernel, allows the start (at its end without it).
+__device__ __forceinline__ void pdl_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+__device__ __forceinline__ void pdl_trigger() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
+template <typename P>
+cudaError_t launch_pdl(void (*kernel)(P), dim3 grid, int threads, int smem, cudaStream_t st,
+                       const std::remove_const_t<P>& p) {
+  cudaLaunchAttribute at[1];
+  at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  at[0].val.programmaticStreamSerializationAllowed = 1;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = grid;
+  cfg.blockDim = dim3(threads);
+  cfg.dynamicSmemBytes = (size_t)smem;
+  cfg.stream = st;
+  cfg.attrs = at;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, kernel, p);
+}
 
 // Row of the cache that holds slot u of sequence s, or -1 when the block table points outside the
 // cache (callers flag FP_DEV_BAD_PROBLEM and treat the slot as not there). u < max_pages * page_size

@@ -30,7 +30,6 @@ constexpr int kOffJoin = kWarps * kStages * kStageBytes;
 constexpr int kOffMl = kOffJoin + kWarps * kRowsT * kJoinCols * 4;  // float m[warp][16], l[warp][16]
 constexpr int kOffTabR = kOffMl + 2 * kWarps * kRowsT * 4 + 64;
 constexpr int row_smem(int S) { return kOffTabR + 8 * (S + 1); }
-constexpr int kMetaWords = 8;
 
 __device__ __forceinline__ void cp_async16(uint32_t dst, const void* src, bool valid) {
   asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(valid ? 16 : 0) : "memory");
@@ -94,7 +93,7 @@ __device__ __forceinline__ void cursor_next(Cursor& u, const CacheInfo& c, const
   load_seq(u, c, find_seq64(tab, c.num_seqs, u.unit0));
 }
 
-__global__ void __launch_bounds__(kRowThreads, 2) cache_rows_kernel(const CacheAttnParams p) {
+__global__ void __launch_bounds__(kRowThreads, 2) cache_rows_kernel(const __grid_constant__ CacheAttnParams p) {
   extern __shared__ __align__(128) unsigned char smem[];
   const CacheInfo& c = p.c;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
@@ -104,6 +103,7 @@ __global__ void __launch_bounds__(kRowThreads, 2) cache_rows_kernel(const CacheA
   const bool ok = cache_table<kRowThreads>(c, tab, s_scan, s_bad, p.dev_status, [&](int, int L, int n) -> long long {
     return (long long)c.hkv * ((L * c.group + kRowsT - 1) / kRowsT) * ((n + kKeysT - 1) / kKeysT);
   });
+  pdl_trigger();
   const long long total = ok ? tab[c.num_seqs] : 0;
   const int ctas = (int)min((long long)gridDim.x, total);  // CTAs with work: every one has a tile
   const int me = blockIdx.x;
@@ -303,7 +303,7 @@ __global__ void __launch_bounds__(kRowThreads, 2) cache_rows_kernel(const CacheA
             const long long at =
                 (long long)(cur.g * c.group + pr % c.group) * c.total_tokens + cur.seq0 + pr / c.group;
             const float v = lt > 0.f || lt != lt ? mu + log2f(lt) : -INFINITY;
-            p.lse2[at] = v;
+            if (p.lse2) p.lse2[at] = v;
             if (p.lse) p.lse[at] = v * 0.6931471805599453f;
           }
         }
@@ -347,7 +347,8 @@ __global__ void __launch_bounds__(kRowThreads, 2) cache_rows_kernel(const CacheA
 // Joins the pieces of a unit that several CTAs share. Block b looks at the unit inside of which the
 // range of CTA b + 1 begins (meta), and works when that CTA is the first such of its unit: the pieces
 // are the last one of CTA b (slot 1) and the first one (slot 0) of every CTA up to meta[1].
-__global__ void __launch_bounds__(256) cache_join_kernel(const CacheAttnParams p) {
+__global__ void __launch_bounds__(256) cache_join_kernel(const __grid_constant__ CacheAttnParams p) {
+  pdl_wait();
   const int b = blockIdx.x + 1;
   const int32_t* meta = p.meta + (long long)b * kMetaWords;
   if (meta[0] == 0) return;
@@ -383,7 +384,7 @@ __global__ void __launch_bounds__(256) cache_join_kernel(const CacheAttnParams p
   *reinterpret_cast<uint4*>(p.out + ((long long)t * c.hq + h) * kHeadDim + cc) = o;
   if ((threadIdx.x & 15) == 0) {
     const float v = any ? mu + log2f(l) : -INFINITY;
-    p.lse2[(long long)h * c.total_tokens + t] = v;
+    if (p.lse2) p.lse2[(long long)h * c.total_tokens + t] = v;
     if (p.lse) p.lse[(long long)h * c.total_tokens + t] = v * 0.6931471805599453f;
   }
 }
@@ -392,7 +393,7 @@ __global__ void __launch_bounds__(256) cache_join_kernel(const CacheAttnParams p
 // Every warp takes 16 keys of one (sequence, kv-head) and walks the rows of its new tokens, 16 at a
 // time: S again from Q and K, then p = 2^(S - lse2) summed over the rows. No two warps touch one
 // weight, so the sum's order is fixed.
-__global__ void __launch_bounds__(kRowThreads) cache_weights_kernel(const CacheAttnParams p) {
+__global__ void __launch_bounds__(kRowThreads) cache_weights_kernel(const __grid_constant__ CacheAttnParams p) {
   extern __shared__ __align__(128) unsigned char smem[];
   const CacheInfo& c = p.c;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
@@ -486,29 +487,34 @@ constexpr int weights_smem(int S) { return kWarps * kKeysW * 256 + 128 + 8 * (S 
 
 }  // namespace
 
-int cache_attn_grid(int sms) { return 2 * sms; }
+bool cache_attn_tiled(int32_t max_new, int32_t group) { return (int64_t)max_new * group > kRowsT; }
 
-CacheAttnLayout cache_attn_layout(int sms, int64_t hq, int64_t total_tokens) {
+CacheAttnLayout cache_attn_layout(int sms, bool tiled, int64_t hq, int64_t total_tokens) {
   auto up = [](int64_t x) { return (x + 255) & ~(int64_t)255; };
-  const int64_t grid = cache_attn_grid(sms);
+  const int64_t grid = tiled ? sms : 2 * sms, rows = 2 * grid * (tiled ? 2 * kTileM : kRowsT);
   CacheAttnLayout w;
   w.part_o = 0;
-  w.part_ml = up(w.part_o + 2 * grid * kRowsT * kHeadDim * 4);
-  w.meta = up(w.part_ml + 2 * grid * 2 * kRowsT * 4);
+  w.part_ml = up(w.part_o + rows * kHeadDim * 4);
+  w.meta = up(w.part_ml + rows * 2 * 4);
   w.lse2 = up(w.meta + grid * kMetaWords * 4);
   w.total = up(w.lse2 + hq * total_tokens * 4);
   return w;
 }
 
-cudaError_t launch_cache_attn(const CacheAttnParams& p, int sms, cudaStream_t st) {
+cudaError_t launch_cache_attn(const CacheAttnParams& p, bool tiled, int sms, cudaStream_t st) {
   static unsigned long long attr[kMaxCachedDevices] = {}, attr_w[kMaxCachedDevices] = {};
-  cudaError_t e = set_max_smem(reinterpret_cast<const void*>(cache_rows_kernel), row_smem(kMaxSeqs), attr);
-  if (e != cudaSuccess) return e;
-  const int grid = cache_attn_grid(sms);
-  cache_rows_kernel<<<grid, kRowThreads, row_smem(p.c.num_seqs), st>>>(p);
-  if ((e = cudaGetLastError()) != cudaSuccess) return e;
-  cache_join_kernel<<<grid - 1, 256, 0, st>>>(p);
-  if ((e = cudaGetLastError()) != cudaSuccess || !(p.decay >= 0.f)) return e;
+  cudaError_t e;
+  if (tiled) {
+    if ((e = launch_cache_tiles(p, sms, st)) != cudaSuccess) return e;
+  } else {
+    e = set_max_smem(reinterpret_cast<const void*>(cache_rows_kernel), row_smem(kMaxSeqs), attr);
+    if (e != cudaSuccess) return e;
+    const int grid = 2 * sms;
+    cache_rows_kernel<<<grid, kRowThreads, row_smem(p.c.num_seqs), st>>>(p);
+    if ((e = cudaGetLastError()) != cudaSuccess) return e;
+    if ((e = launch_pdl(cache_join_kernel, dim3(grid - 1), 256, 0, st, p)) != cudaSuccess) return e;
+  }
+  if (!(p.decay >= 0.f)) return cudaSuccess;
   if ((e = set_max_smem(reinterpret_cast<const void*>(cache_weights_kernel), weights_smem(kMaxSeqs), attr_w)) !=
       cudaSuccess)
     return e;

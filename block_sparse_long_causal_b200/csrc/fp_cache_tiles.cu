@@ -1,0 +1,735 @@
+// fp_cache_tiles.cu -- attention of new tokens over a paged key/value cache on the tcgen05 tensor cores:
+// the schedule for calls whose sequences bring more packed rows than the 16-row kernel's tile holds.
+//
+// A row tile is 128 / G whole tokens with the G q-heads of one kv-head (row r: token r / G, head r % G),
+// so that a K/V tile is read once for all heads of its group. A unit is two neighbouring row tiles of one
+// (sequence, kv-head), one per softmax warpgroup, over the same 128-key tiles; a unit with a single row
+// tile (few new tokens) gives its key tiles to the two warpgroups in turn and joins the two results
+// when it ends, so that one warpgroup's softmax overlaps the other's matrix products either way.
+//
+// The key tiles of all units form one line that is cut into equal parts, one per CTA, whatever the
+// lengths; a part may begin or end inside a unit, and the pieces of such a unit are joined from the
+// workspace by the join kernel. The line visits the units in an order (unit_at) that lets CTAs which
+// run at the same time work on the same kv-heads, whose K/V then stay in the L2.
+#include "fp_cache.cuh"
+
+namespace fp {
+
+namespace tiles {
+
+constexpr int kThreads = 384;
+constexpr unsigned kAll = 0xffffffffu;
+constexpr int kBK = 128;                  // keys of a tile
+constexpr int kStages = 2;                // K ring and V ring
+constexpr int kUnitRing = 4;
+constexpr int kUnitReaders = 9;           // the MMA warp and the 8 softmax warps
+constexpr int kRegsCtl = 104, kRegsSoftmax = 200;
+static_assert(128 * kRegsCtl + 256 * kRegsSoftmax == kThreads * 168, "register split must equal the launch allocation");
+constexpr uint64_t kDrainLimitNs = 1000000000ull;
+constexpr float kFastSumLimit = 65536.f;  // largest row sum that an item without a max pass may have
+constexpr uint32_t kTile = 128 * 128 * 2, kSlab = 128 * 128;
+constexpr uint32_t kOffQ = 0, kOffK = 2 * kTile, kOffV = kOffK + kStages * kTile, kOffBar = kOffV + kStages * kTile;
+// q_full, q_empty, k_full[], k_empty[], v_full[], v_empty[], s_full[2], p_full[2], o_final[2], x_full, x_done,
+// drain, unit_full[], unit_empty[]
+constexpr int kNumBars = 2 + 4 * kStages + 6 + 3 + 2 * kUnitRing;
+constexpr uint32_t kOffMisc = kOffBar + kNumBars * 8;                   // tmem base, abort flag, bad flag
+constexpr uint32_t kOffScan = (kOffMisc + 16 + 15) & ~15u;              // int64[12]; the line's start (5 int64)
+constexpr uint32_t kOffUnit = kOffScan + 8 * 12 + 8 * 6;                // unit descriptors
+constexpr uint32_t kUnitBytes = 48;
+constexpr uint32_t kOffX = kOffUnit + kUnitRing * kUnitBytes;           // float max[2][128], sum[2][128]
+constexpr uint32_t kOffTab = (kOffX + 2 * 2 * 128 * 4 + 15) & ~15u;
+constexpr uint32_t smem_bytes(int S) { return kOffTab + 8 * (S + 1) + 1024; }
+static_assert(smem_bytes(kMaxSeqs) <= 227 * 1024, "shared memory per CTA");
+constexpr uint32_t kIdescQK = idesc_bf16_f32(128, kBK, 0, 0), kIdescPV = idesc_bf16_f32(128, kHeadDim, 0, 1);
+
+// What the roles need of a piece of a unit: key tiles [kt0, kt1) of its kts.
+struct Piece {
+  int seq0, L, len;   // first new token, new tokens, slots before them; -1 in seq0: the CTA's part is done
+  int g, tok0;        // kv-head, first token of row tile 0
+  int nslot;          // row tiles
+  int kt0, kt1, kts;
+  int kts0;           // key tiles that row tile 0 needs (kts: row tile 1)
+  int slot;           // partial result's place, or -1: the whole unit
+};
+static_assert(sizeof(Piece) <= kUnitBytes, "unit ring entry");
+
+struct Unit {
+  int s, g, m;
+  int seq0, L, len;
+};
+__device__ __forceinline__ int key_tiles(const Unit& u, int tokens) {
+  return (u.len + min(u.L, tokens) + kBK - 1) / kBK;
+}
+// Unit x in kv-head order: per sequence kv-head outermost, then the row-tile pairs from the last (longest)
+// to the first.
+__device__ __forceinline__ Unit decode(const CacheInfo& c, const long long* tab, int TT, long long x) {
+  Unit u;
+  u.s = find_seq64(tab, c.num_seqs, x);
+  u.seq0 = __ldg(c.cu_seqlens + u.s);
+  u.L = __ldg(c.cu_seqlens + u.s + 1) - u.seq0;
+  u.len = c.lens[u.s];
+  const int pairs = ((u.L + TT - 1) / TT + 1) / 2;
+  const int local = (int)(x - tab[u.s]);
+  u.g = local / pairs;
+  u.m = pairs - 1 - (local - u.g * pairs);
+  return u;
+}
+__device__ __forceinline__ long long gcd64(long long a, long long b) {
+  while (b) {
+    const long long t = a % b;
+    a = b;
+    b = t;
+  }
+  return a;
+}
+// The line's i-th unit. A CTA's part covers about N / ctas units in a row, so unit i is reached after the
+// fraction i * ctas / N (mod 1) of the run; ranking the units by that fraction gives the CTAs that
+// run at the same time neighbouring units of the kv-head order. d = gcd(ctas, N): i and i + N / d have
+// the same fraction and follow one another.
+__device__ __forceinline__ long long unit_at(long long i, long long N, int ctas, long long d) {
+  if (N <= ctas) return i;
+  return i * ctas % N + i / (N / d);
+}
+
+__device__ __forceinline__ void tma_load_3d(uint32_t dst, const void* tmap, uint32_t bar, int x, int y, int z) {
+  asm volatile(
+      "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%3, %4, %5}], [%2];"
+      ::"r"(dst), "l"(reinterpret_cast<uint64_t>(tmap)), "r"(bar), "r"(x), "r"(y), "r"(z)
+      : "memory");
+}
+
+__global__ void __launch_bounds__(kThreads, 1) cache_tiles_kernel(const __grid_constant__ CacheAttnParams p) {
+  extern __shared__ __align__(1024) unsigned char smem_raw[];
+  unsigned char* smem = (unsigned char*)(((uintptr_t)smem_raw + 1023) & ~(uintptr_t)1023);
+  const uint32_t sbase = smem_u32(smem);
+  const uint32_t sQ = sbase + kOffQ, sK = sbase + kOffK, sV = sbase + kOffV, bar0 = sbase + kOffBar;
+  const uint32_t b_q_full = bar0, b_q_empty = bar0 + 8;
+  auto b_k_full = [&](int i) { return bar0 + 16 + 8 * i; };
+  auto b_k_empty = [&](int i) { return bar0 + 16 + 8 * (kStages + i); };
+  auto b_v_full = [&](int i) { return bar0 + 16 + 8 * (2 * kStages + i); };
+  auto b_v_empty = [&](int i) { return bar0 + 16 + 8 * (3 * kStages + i); };
+  const uint32_t b_s_full0 = bar0 + 16 + 32 * kStages, b_p_full0 = b_s_full0 + 16, b_o_final0 = b_p_full0 + 16;
+  const uint32_t b_x_full = b_o_final0 + 16, b_x_done = b_x_full + 8, b_drain = b_x_done + 8;
+  auto b_u_full = [&](uint32_t i) { return b_drain + 8 + 8 * (i % kUnitRing); };
+  auto b_u_empty = [&](uint32_t i) { return b_drain + 8 + 8 * (kUnitRing + i % kUnitRing); };
+  uint32_t* s_tmem = reinterpret_cast<uint32_t*>(smem + kOffMisc);
+  volatile int* s_abort = reinterpret_cast<volatile int*>(smem + kOffMisc + 4);
+  int* s_bad = reinterpret_cast<int*>(smem + kOffMisc + 8);
+  long long* s_scan = reinterpret_cast<long long*>(smem + kOffScan);
+  long long* s_start = s_scan + 12;  // T, unit index, its tile, its line position
+  long long* tab = reinterpret_cast<long long*>(smem + kOffTab);
+  auto unit_entry = [&](uint32_t i) { return reinterpret_cast<Piece*>(smem + kOffUnit + (i % kUnitRing) * kUnitBytes); };
+
+  const CacheInfo& c = p.c;
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, wg = warp >> 2;
+  const int G = c.group, TT = p.tile_tokens;
+  if (tid == 0) {
+    mbar_init(b_q_full, 1);
+    mbar_init(b_q_empty, 1);
+    for (int i = 0; i < kStages; ++i) {
+      mbar_init(b_k_full(i), 1);
+      mbar_init(b_k_empty(i), 1);
+      mbar_init(b_v_full(i), 1);
+      mbar_init(b_v_empty(i), 1);
+    }
+    for (int k = 0; k < 2; ++k) {
+      mbar_init(b_s_full0 + 8 * k, 1);
+      mbar_init(b_p_full0 + 8 * k, 128);
+      mbar_init(b_o_final0 + 8 * k, 1);
+    }
+    mbar_init(b_x_full, 256);
+    mbar_init(b_x_done, 256);
+    mbar_init(b_drain, 1);
+    for (int i = 0; i < kUnitRing; ++i) {
+      mbar_init(b_u_full(i), 1);
+      mbar_init(b_u_empty(i), kUnitReaders);
+    }
+    *s_abort = 0;
+    fence_mbar_init();
+    tma_prefetch_desc(&p.tm_q);
+    tma_prefetch_desc(&p.tm_k);
+    tma_prefetch_desc(&p.tm_v);
+  }
+  if (warp == 1) {
+    tmem_alloc(smem_u32(s_tmem), 512);
+    tmem_relinquish();
+  }
+  const bool ok = cache_table<kThreads>(c, tab, s_scan, s_bad, p.dev_status, [&](int, int L, int) -> long long {
+    return (long long)c.hkv * (((L + TT - 1) / TT + 1) / 2);
+  });
+  const long long N = ok ? tab[c.num_seqs] : 0;
+  // ---- this CTA's part [x0, x1) of the line, and the unit that x0 falls into
+  const long long d = N > 0 ? gcd64(N, gridDim.x) : 1;
+  long long x0 = 0, x1 = 0;
+  int ctas = 0;
+  {
+    const long long per = (N + kThreads - 1) / kThreads, a = min(N, tid * per), b = min(N, a + per);
+    long long sum = 0;
+    for (long long i = a; i < b; ++i) {
+      const Unit u = decode(c, tab, TT, unit_at(i, N, gridDim.x, d));
+      sum += key_tiles(u, (2 * u.m + 2) * TT);
+    }
+    const long long incl = warp_incl_scan(sum);
+    __syncthreads();  // cache_table is done with the scratch
+    if (lane == 31) s_scan[warp] = incl;
+    __syncthreads();
+    long long base = incl - sum, T = 0;
+    for (int w = 0; w < kThreads / 32; ++w) {
+      if (w < warp) base += s_scan[w];
+      T += s_scan[w];
+    }
+    ctas = (int)min((long long)gridDim.x, T);
+    const int me = blockIdx.x;
+    if (me < ctas) {
+      x0 = T * me / ctas;
+      x1 = T * (me + 1) / ctas;
+      if (base <= x0 && x0 < base + sum) {
+        for (long long i = a; i < b; ++i) {
+          const Unit u = decode(c, tab, TT, unit_at(i, N, gridDim.x, d));
+          const int kts = key_tiles(u, (2 * u.m + 2) * TT);
+          if (x0 < base + kts) {
+            s_start[0] = i;
+            s_start[1] = x0 - base;
+            int32_t* meta = p.meta + (long long)me * kMetaWords;
+            // a part that begins inside a unit: the first such CTA of the unit has the pieces joined
+            const bool inside = x0 > base;
+            meta[0] = inside && T * (me - 1) / ctas <= base;
+            if (inside) {
+              int last = me;  // the last CTA whose part begins inside the unit
+              while (last + 1 < ctas && T * (last + 1) / ctas < base + kts) ++last;
+              meta[1] = last;
+              meta[2] = u.seq0;
+              meta[3] = u.g;
+              meta[4] = 2 * u.m * TT;
+              meta[5] = u.L;
+            }
+            break;
+          }
+          base += kts;
+        }
+      }
+    } else if (tid == 0) {
+      p.meta[(long long)me * kMetaWords] = 0;
+    }
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = *s_tmem;
+  pdl_trigger();
+  auto t_s = [&](int k) { return tmem + 128u * k; };
+  auto t_o = [&](int k) { return tmem + 256u + 128u * k; };
+
+  if (wg == 0) asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsCtl));
+  if (warp == 0) {
+    // =========================================================== loads
+    uint32_t kit = 0, vit = 0, uc = 0;
+    int q_issued = 0;
+    bool fail = false, bad_page = false;
+    const int bh = p.box_rows, lanes = kBK / bh;
+    const uint32_t q_bytes = (uint32_t)(G * TT) * 128u;
+    const int no_row = (int)min((long long)c.num_pages * c.page_size, 0x7fffffffll);  // loads from here read zeros
+    auto all_wait = [&](uint32_t bar, uint32_t parity) {
+      return __all_sync(kAll, mbar_wait(bar, parity, p.wait_limit_ns));
+    };
+    long long i = x0 < x1 ? s_start[0] : 0;
+    int kt = x0 < x1 ? (int)s_start[1] : 0;
+    for (long long x = x0; x < x1 && !fail; ++i, kt = 0) {
+      const Unit u = decode(c, tab, TT, unit_at(i, N, gridDim.x, d));
+      Piece pc;
+      pc.seq0 = u.seq0;
+      pc.L = u.L;
+      pc.len = u.len;
+      pc.g = u.g;
+      pc.tok0 = 2 * u.m * TT;
+      pc.nslot = pc.tok0 + TT < u.L ? 2 : 1;
+      pc.kts = key_tiles(u, (2 * u.m + 2) * TT);
+      pc.kts0 = key_tiles(u, (2 * u.m + 1) * TT);
+      pc.kt0 = kt;
+      pc.kt1 = (int)min((long long)pc.kts, kt + (x1 - x));
+      pc.slot = kt == 0 && pc.kt1 == pc.kts ? -1 : 2 * (int)blockIdx.x + (kt == 0 ? 1 : 0);
+      x += pc.kt1 - kt;
+      if (uc >= kUnitRing && !all_wait(b_u_empty(uc), ((uc / kUnitRing) - 1) & 1)) { fail = true; break; }
+      if (lane == 0) {
+        *unit_entry(uc) = pc;
+        mbar_arrive(b_u_full(uc));
+      }
+      if (!all_wait(b_q_empty, (uc & 1) ^ 1)) { fail = true; break; }
+      if (lane == 0) {
+        mbar_arrive_expect_tx(b_q_full, 2 * pc.nslot * q_bytes);
+        for (int k = 0; k < 2 * pc.nslot; ++k)
+          tma_load_3d(sQ + (k >> 1) * kTile + (k & 1) * kSlab, &p.tm_q, b_q_full, 64 * (k & 1), u.g * G,
+                      u.seq0 + pc.tok0 + (k >> 1) * TT);
+      }
+      ++q_issued;
+      ++uc;
+      const int n = u.len + u.L;
+      // one lane per group of box_rows slots, which lie in one page; a page outside the cache and groups
+      // past the sequence's end read as zeros
+      auto row_of = [&](int t) -> int {
+        const int key = t * kBK + lane * bh;
+        if (lane >= lanes || key >= n) return no_row;
+        const long long row = slot_row(c, u.s, key);
+        bad_page |= row < 0;
+        return row < 0 ? no_row : (int)row;
+      };
+      auto load = [&](uint32_t dst, const void* tm, uint32_t full, int row) {
+        if (lane == 0) mbar_arrive_expect_tx(full, kTile);
+        __syncwarp();
+        if (lane < lanes) {
+          tma_load_2d(dst + lane * bh * 128, tm, full, u.g * kHeadDim, row);
+          tma_load_2d(dst + kSlab + lane * bh * 128, tm, full, u.g * kHeadDim + 64, row);
+        }
+      };
+      auto load_v = [&](int row) -> bool {
+        const int vs = vit % kStages;
+        if (!all_wait(b_v_empty(vs), ((vit / kStages) & 1) ^ 1)) return false;
+        load(sV + vs * kTile, &p.tm_v, b_v_full(vs), row);
+        ++vit;
+        return true;
+      };
+      // V of a tile is loaded after K of the next one: its product comes later
+      int row = row_of(pc.kt0), vrow = -1;
+      for (int t = pc.kt0; t < pc.kt1; ++t) {
+        const int ks = kit % kStages;
+        const int next = t + 1 < pc.kt1 ? row_of(t + 1) : no_row;  // the table's answer arrives during the wait
+        if (!all_wait(b_k_empty(ks), ((kit / kStages) & 1) ^ 1)) { fail = true; break; }
+        load(sK + ks * kTile, &p.tm_k, b_k_full(ks), row);
+        ++kit;
+        if (t > pc.kt0 && !load_v(vrow)) { fail = true; break; }
+        vrow = row;
+        row = next;
+        if (*s_abort) { fail = true; break; }
+      }
+      if (!fail && !load_v(vrow)) fail = true;
+    }
+    if (!fail && uc >= kUnitRing && !all_wait(b_u_empty(uc), ((uc / kUnitRing) - 1) & 1)) fail = true;
+    if (!fail && lane == 0) {
+      unit_entry(uc)->seq0 = -1;
+      mbar_arrive(b_u_full(uc));
+    }
+    if (bad_page) dev_flag(p.dev_status, kDevBadProblem);
+    if (fail && lane == 0) {
+      *s_abort = 1;
+      dev_flag(p.dev_status, kDevTimeout);
+      for (int k = 0; k < kStages; ++k) {  // copies in flight land before the CTA ends
+        if (kit > (uint32_t)k) mbar_wait(b_k_full((kit - 1 - k) % kStages), ((kit - 1 - k) / kStages) & 1, kDrainLimitNs);
+        if (vit > (uint32_t)k) mbar_wait(b_v_full((vit - 1 - k) % kStages), ((vit - 1 - k) / kStages) & 1, kDrainLimitNs);
+      }
+      if (q_issued > 0) mbar_wait(b_q_full, (uint32_t)(q_issued - 1) & 1, kDrainLimitNs);
+    }
+    __syncwarp();
+  } else if (warp == 1) {
+    // =========================================================== tcgen05 issue (lane 0)
+    uint32_t kit = 0, vit = 0, cnt[2] = {0, 0};
+    bool fail = false;
+    auto all_wait = [&](uint32_t bar, uint32_t parity) {
+      return __all_sync(kAll, mbar_wait(bar, parity, p.wait_limit_ns));
+    };
+    for (uint32_t uc = 0; !fail; ++uc) {
+      if (!all_wait(b_u_full(uc), (uc / kUnitRing) & 1)) { fail = true; break; }
+      const Piece pc = *unit_entry(uc);
+      __syncwarp();
+      if (lane == 0) mbar_arrive(b_u_empty(uc));
+      if (pc.seq0 < 0) break;
+      if (!all_wait(b_q_full, uc & 1)) { fail = true; break; }
+      tc_fence_after();
+      const int n = pc.len + pc.L;
+      int prev_part = 0, prev_t = 0;
+      bool had_pv[2] = {false, false};
+      auto pv = [&](int k, bool fix) -> bool {  // O_k += P_k V of tile prev_t
+        if (!all_wait(b_p_full0 + 8 * k, (cnt[k] - 1) & 1)) return false;
+        const int vs = vit % kStages;
+        if (!all_wait(b_v_full(vs), (vit / kStages) & 1)) return false;
+        const int live = n - prev_t * kBK;
+        if (fix && live < kBK) {
+          // slots past the sequence's end may hold anything, and 0 * NaN is NaN: their V rows become zeros
+          for (int e = live * 8 + lane; e < kBK * 8; e += 32) {
+            *reinterpret_cast<uint4*>(smem + kOffV + vs * kTile + e * 16) = make_uint4(0, 0, 0, 0);
+            *reinterpret_cast<uint4*>(smem + kOffV + vs * kTile + kSlab + e * 16) = make_uint4(0, 0, 0, 0);
+          }
+          asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+          __syncwarp();
+        }
+        tc_fence_after();
+        if (lane == 0) {
+          const uint64_t vdesc = sdesc_sw128(sV + vs * kTile, kSlab, 1024);
+#pragma unroll
+          for (int kk = 0; kk < kBK / 16; ++kk)
+            mma_ts(t_o(k), t_s(k) + kk * 8, desc_advance(vdesc, kk * (2048 >> 4)), kIdescPV,
+                   had_pv[k] || kk > 0 ? 1u : 0u);
+        }
+        had_pv[k] = true;
+        return true;
+      };
+      auto qk = [&](int k, uint32_t kbase) {
+        if (lane == 0) {
+          const uint64_t qdesc = sdesc_sw128(sQ + (pc.nslot == 2 ? k : 0) * kTile, 16, 1024);
+          const uint64_t kdesc = sdesc_sw128(kbase, 16, 1024);
+#pragma unroll
+          for (int kk = 0; kk < kHeadDim / 16; ++kk) {
+            const uint32_t off = ((kk >> 2) * kSlab + (kk & 3) * 32) >> 4;
+            mma_ss(t_s(k), desc_advance(qdesc, off), desc_advance(kdesc, off), kIdescQK, kk > 0 ? 1u : 0u);
+          }
+          mma_commit(b_s_full0 + 8 * k);
+        }
+        ++cnt[k];
+      };
+      for (int t = pc.kt0; t < pc.kt1; ++t) {
+        const int part = pc.nslot == 2 ? (t < pc.kts0 ? 3 : 2) : 1 << ((t - pc.kt0) & 1);
+        const int ks = kit % kStages;
+        if (!all_wait(b_k_full(ks), (kit / kStages) & 1)) { fail = true; break; }
+        tc_fence_after();
+        const uint32_t kbase = sK + ks * kTile;
+        // a slot that took part in the previous tile issues that tile's PV before this one's QK (S overwrites
+        // P); the QK of one that did not goes first, so that its softmax overlaps the other's
+#pragma unroll
+        for (int k = 0; k < 2; ++k)
+          if (((part & ~prev_part) >> k) & 1) qk(k, kbase);
+#pragma unroll
+        for (int k = 0; k < 2; ++k)
+          if (!fail && ((prev_part >> k) & 1)) {
+            if (!pv(k, k == 0 || !(prev_part & 1))) { fail = true; break; }
+            if ((part >> k) & 1) qk(k, kbase);
+          }
+        if (fail) break;
+        if (t > pc.kt0) {
+          if (lane == 0) mma_commit(b_v_empty(vit % kStages));
+          ++vit;
+        }
+        if (lane == 0) {
+          mma_commit(b_k_empty(ks));
+          if (t + 1 == pc.kt1) mma_commit(b_q_empty);
+        }
+        ++kit;
+        prev_part = part;
+        prev_t = t;
+        if (*s_abort) { fail = true; break; }
+      }
+      if (fail) break;
+#pragma unroll
+      for (int k = 0; k < 2; ++k)
+        if (!fail && ((prev_part >> k) & 1))
+          if (!pv(k, k == 0 || !(prev_part & 1))) fail = true;
+      if (fail) break;
+      if (lane == 0) {
+        mma_commit(b_v_empty(vit % kStages));
+        if (had_pv[0]) mma_commit(b_o_final0);
+        if (had_pv[1]) mma_commit(b_o_final0 + 8);
+      }
+      ++vit;
+    }
+    if (lane == 0) {
+      if (fail) {
+        *s_abort = 1;
+        dev_flag(p.dev_status, kDevTimeout);
+      }
+      mma_commit(b_drain);  // every issued product completes before TMEM is released
+      mbar_wait(b_drain, 0, kDrainLimitNs);
+    }
+    __syncwarp();
+  } else if (wg >= 1) {
+    // =========================================================== softmax and epilogue
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kRegsSoftmax));
+    const int slot = wg - 1, r = (warp & 3) * 32 + lane;
+    const uint32_t lane_off = (uint32_t)((warp & 3) * 32) << 16;
+    const uint32_t s_col = t_s(slot) + lane_off, o_col = t_o(slot) + lane_off;
+    const uint32_t b_s_full = b_s_full0 + 8 * slot, b_p_full = b_p_full0 + 8 * slot;
+    float* s_xm = reinterpret_cast<float*>(smem + kOffX);
+    float* s_xl = s_xm + 256;
+    uint32_t cnt = 0, fc[2] = {0, 0}, xc = 0;
+    bool fail = false;
+    auto all_wait = [&](uint32_t bar, uint32_t parity) {
+      return __all_sync(kAll, mbar_wait(bar, parity, p.wait_limit_ns));
+    };
+    const uint64_t scale2 = f2_make(p.scale_log2, p.scale_log2);
+    for (uint32_t uc = 0; !fail; ++uc) {
+      if (!all_wait(b_u_full(uc), (uc / kUnitRing) & 1)) { fail = true; break; }
+      const Piece pc = *unit_entry(uc);
+      __syncwarp();
+      if (lane == 0) mbar_arrive(b_u_empty(uc));
+      if (pc.seq0 < 0) break;
+      const bool dual = pc.nslot == 1;  // both warpgroups share the row tile
+      const int tok = pc.tok0 + (dual ? 0 : slot) * TT + r / G;
+      // rows without a token (the tile's spare rows, tokens past the sequence's end) hold anything: they take no
+      // part in the votes and are not written
+      const bool pad = r >= TT * G || tok >= pc.L;
+      const int last = pad ? 0x7fffffff : pc.len + tok;  // the last key that the row sees
+      const int t1 = dual || slot == 1 ? pc.kt1 : min(pc.kt1, pc.kts0), step = dual ? 2 : 1;
+      float m_run = -INFINITY, l_run = 0.f;
+      int n = 0;
+      for (int t = pc.kt0 + (dual ? slot : 0); t < t1; t += step) {
+        if (!all_wait(b_s_full, cnt & 1)) { fail = true; break; }
+        tc_fence_after();
+        const int valid = last - t * kBK;  // keys 0 .. valid of the tile are seen
+        const bool masked = valid < kBK - 1;
+        uint32_t pk[kBK / 2];
+        bool done = false;
+        // without a max pass, against the row's reference so far; a sum of at most 2^16 bounds every term
+        if (__all_sync(kAll, pad || (!masked && m_run != -INFINITY))) {
+          const uint64_t negm2 = f2_make(-m_run, -m_run);
+          uint64_t acc[4] = {0ull, 0ull, 0ull, 0ull};
+          uint32_t cb[2][32];
+          tmem_ld32(s_col, cb[0]);
+#pragma unroll
+          for (int b = 0; b < kBK / 32; ++b) {
+            tmem_wait_ld();
+            reg_fence32(cb[b & 1]);
+            if (b + 1 < kBK / 32) tmem_ld32(s_col + 32 * (b + 1), cb[(b + 1) & 1]);
+#pragma unroll
+            for (int e = 0; e < 32; e += 2) {
+              const int pr = 16 * b + e / 2;
+              float v0, v1;
+              f2_split(ffma2(f2_bits(cb[b & 1][e], cb[b & 1][e + 1]), scale2, negm2), v0, v1);
+              v0 = ex2_approx(v0);
+              v1 = ex2_approx(v1);
+              acc[pr & 3] = fadd2(acc[pr & 3], f2_make(v0, v1));
+              pk[pr] = pack_bf16x2(v0, v1);  // P goes to the tensor cores in bf16 (half a step: 2^-9 of a term)
+            }
+          }
+          float a0, a1, b0, b1;
+          f2_split(fadd2(acc[0], acc[1]), a0, a1);
+          f2_split(fadd2(acc[2], acc[3]), b0, b1);
+          const float sum = (a0 + a1) + (b0 + b1);
+          done = __all_sync(kAll, pad || sum <= kFastSumLimit);
+          if (done) l_run += sum;
+        }
+        if (!done) {
+          uint32_t sr[kBK];
+#pragma unroll
+          for (int b = 0; b < kBK; b += 32) tmem_ld32(s_col + b, *reinterpret_cast<uint32_t(*)[32]>(&sr[b]));
+          tmem_wait_ld();
+#pragma unroll
+          for (int b = 0; b < kBK; b += 32) reg_fence32(*reinterpret_cast<uint32_t(*)[32]>(&sr[b]));
+          float m4[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+#pragma unroll
+          for (int e = 0; e < kBK; e += 8)
+#pragma unroll
+            for (int a = 0; a < 4; ++a) {
+              const float v0 = e + 2 * a <= valid ? __uint_as_float(sr[e + 2 * a]) : -INFINITY;
+              const float v1 = e + 2 * a + 1 <= valid ? __uint_as_float(sr[e + 2 * a + 1]) : -INFINITY;
+              sr[e + 2 * a] = __float_as_uint(v0);
+              sr[e + 2 * a + 1] = __float_as_uint(v1);
+              m4[a] = fmax3(m4[a], v0, v1);
+            }
+          const float m_new = fmaxf(m_run, fmax3(m4[0], m4[1], fmaxf(m4[2], m4[3])) * p.scale_log2);
+          // the reference follows only when a score passes it by 2^8: the quotient does not depend on it
+          const bool grow = m_new > m_run + 8.f;
+          float alpha = 1.f;
+          if (grow) {
+            alpha = ex2_approx(m_run - m_new);
+            m_run = m_new;
+          }
+          l_run *= alpha;
+          if (n > 0 && __any_sync(kAll, grow)) {
+            // this slot's earlier products are complete: S came after them. In a shared row tile they are those of
+            // the slot's own last tile, whose PV was issued before the QK of this one
+            const uint64_t a2 = f2_make(alpha, alpha);
+#pragma unroll 1
+            for (int b = 0; b < kHeadDim; b += 32) {
+              uint32_t o[32];
+              tmem_ld32(o_col + b, o);
+              tmem_wait_ld();
+              reg_fence32(o);
+#pragma unroll
+              for (int e = 0; e < 32; e += 2) {
+                float lo, hi;
+                f2_split(fmul2(f2_bits(o[e], o[e + 1]), a2), lo, hi);
+                o[e] = __float_as_uint(lo);
+                o[e + 1] = __float_as_uint(hi);
+              }
+              tmem_st32(o_col + b, o);
+            }
+          }
+          const float m_use = m_run == -INFINITY ? 0.f : m_run;
+          const uint64_t negm2 = f2_make(-m_use, -m_use);
+          uint64_t sum2[2] = {0ull, 0ull};
+#pragma unroll
+          for (int e = 0; e < kBK; e += 2) {
+            float v0, v1;
+            f2_split(ffma2(f2_bits(sr[e], sr[e + 1]), scale2, negm2), v0, v1);
+            v0 = ex2_approx(v0);
+            v1 = ex2_approx(v1);
+            sum2[(e >> 1) & 1] = fadd2(sum2[(e >> 1) & 1], f2_make(v0, v1));
+            pk[e / 2] = pack_bf16x2(v0, v1);
+          }
+          float a0, a1, b0, b1;
+          f2_split(sum2[0], a0, a1);
+          f2_split(sum2[1], b0, b1);
+          l_run += (a0 + a1) + (b0 + b1);
+        }
+#pragma unroll
+        for (int b = 0; b < kBK / 2; b += 32) tmem_st32(s_col + b, *reinterpret_cast<uint32_t(*)[32]>(&pk[b]));
+        tmem_wait_st();
+        tc_fence_before();
+        mbar_arrive(b_p_full);
+        ++cnt;
+        ++n;
+      }
+      if (__any_sync(kAll, fail || *s_abort)) { fail = true; break; }
+      // ---- the piece is complete
+      const int h = pc.g * G + r % G;
+      const long long token = (long long)pc.seq0 + tok;
+      float w0 = 1.f, w1 = 0.f;      // weights of O_0 and O_1 (of this slot's own O when not shared)
+      bool use[2] = {n > 0, false};  // which accumulators hold something (the same for every thread)
+      if (dual) {
+        const bool two = pc.kt1 - pc.kt0 > 1;
+        s_xm[slot * 128 + r] = m_run;
+        s_xl[slot * 128 + r] = l_run;
+        mbar_arrive(b_x_full);
+        if (!all_wait(b_x_full, xc & 1)) { fail = true; break; }
+        const float m0 = s_xm[r], l0 = s_xl[r], m1 = s_xm[128 + r], l1 = s_xl[128 + r];
+        m_run = fmaxf(m0, m1);
+        const float mu = m_run == -INFINITY ? 0.f : m_run;
+        w0 = ex2_approx(m0 - mu);
+        w1 = two ? ex2_approx(m1 - mu) : 0.f;
+        l_run = two ? w0 * l0 + w1 * l1 : w0 * l0;
+        use[0] = true;
+        use[1] = two;
+        if (!all_wait(b_o_final0, fc[0] & 1)) fail = true;
+        if (two && !all_wait(b_o_final0 + 8, fc[1] & 1)) fail = true;
+        fc[0] += 1;
+        fc[1] += two;
+      } else {
+        if (n > 0 && !all_wait(b_o_final0 + 8 * slot, fc[slot] & 1)) fail = true;
+        fc[0] += pc.kt0 < pc.kts0;  // both warpgroups count the phases of both barriers
+        fc[1] += 1;
+      }
+      if (fail) break;
+      tc_fence_after();
+      const bool any = l_run > 0.f || l_run != l_run;
+      if (pc.slot < 0) {
+        const float inv = any ? 1.f / l_run : 0.f;
+        w0 *= inv;
+        w1 *= inv;
+      }
+      const long long part = ((long long)pc.slot * 2 + (dual ? 0 : slot)) * 128 + r;  // row of the partial results
+      uint16_t* orow = p.out + (token * c.hq + h) * kHeadDim;
+      const uint32_t col0 = t_o(dual ? 0 : slot) + lane_off, col1 = t_o(1) + lane_off;
+      const int cb = dual ? 64 * slot : 0, ce = dual ? cb + 64 : kHeadDim;
+      if (use[0] || pc.slot < 0) {
+#pragma unroll 1
+        for (int b = cb; b < ce; b += 32) {
+          uint32_t o[32];
+          if (use[0]) {
+            tmem_ld32(col0 + b, o);
+            tmem_wait_ld();
+            reg_fence32(o);
+          }
+#pragma unroll
+          for (int e = 0; e < 32; ++e) o[e] = use[0] ? __float_as_uint(__uint_as_float(o[e]) * w0) : 0u;
+          if (use[1]) {
+            uint32_t o1[32];
+            tmem_ld32(col1 + b, o1);
+            tmem_wait_ld();
+            reg_fence32(o1);
+#pragma unroll
+            for (int e = 0; e < 32; ++e)
+              o[e] = __float_as_uint(fmaf(__uint_as_float(o1[e]), w1, __uint_as_float(o[e])));
+          }
+          if (!pad && pc.slot < 0) {
+            uint32_t w[16];
+#pragma unroll
+            for (int e = 0; e < 16; ++e) w[e] = pack_bf16x2(__uint_as_float(o[2 * e]), __uint_as_float(o[2 * e + 1]));
+            uint4* dst = reinterpret_cast<uint4*>(orow + b);
+#pragma unroll
+            for (int e = 0; e < 4; ++e) dst[e] = make_uint4(w[4 * e], w[4 * e + 1], w[4 * e + 2], w[4 * e + 3]);
+          } else if (!pad) {
+            float* dst = p.part_o + part * kHeadDim + b;
+#pragma unroll
+            for (int e = 0; e < 32; e += 8) st_global_v8(dst + e, o + e);
+          }
+          __syncwarp();
+        }
+      }
+      if (!pad && (!dual || slot == 0)) {
+        if (pc.slot < 0) {
+          const float mu = m_run == -INFINITY ? 0.f : m_run;
+          const float z = any ? mu + log2f(l_run) : -INFINITY;
+          const long long at = (long long)h * c.total_tokens + token;
+          if (p.lse2) p.lse2[at] = z;
+          if (p.lse) p.lse[at] = z * 0.6931471805599453f;
+        } else {  // a row tile without a key tile in this piece: sum 0, and its O is not read
+          *reinterpret_cast<float2*>(p.part_ml + 2 * part) = make_float2(n > 0 || dual ? m_run : -INFINITY, l_run);
+        }
+      }
+      tc_fence_before();
+      if (dual) {  // neither warpgroup goes on to overwrite an accumulator or the exchange that the other still reads
+        mbar_arrive(b_x_done);
+        if (!all_wait(b_x_done, xc & 1)) { fail = true; break; }
+        ++xc;
+        tc_fence_after();
+      }
+    }
+    if (fail) {
+      *s_abort = 1;
+      dev_flag(p.dev_status, kDevTimeout);
+    }
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  if (warp == 1) tmem_dealloc(tmem, 512);
+}
+
+// Joins the pieces of the units that several CTAs share. Block (b, y) looks at the unit inside of which
+// the part of CTA b + 1 begins (meta) and works when that CTA is the first such of its unit: the pieces
+// are the last one of CTA b (place 1) and the first one (place 0) of every CTA up to meta[1]. 16 rows a block.
+__global__ void __launch_bounds__(256) cache_tiles_join_kernel(const __grid_constant__ CacheAttnParams p) {
+  pdl_wait();
+  const int b = blockIdx.x + 1;
+  const int32_t* meta = p.meta + (long long)b * kMetaWords;
+  if (meta[0] == 0) return;
+  const CacheInfo& c = p.c;
+  const int last = meta[1], seq0 = meta[2], g = meta[3], tok0 = meta[4], L = meta[5];
+  const int TT = p.tile_tokens, G = c.group;
+  const int row = blockIdx.y * 16 + (threadIdx.x >> 4), cc = (threadIdx.x & 15) * 8;
+  const int r = row & 127, tok = tok0 + (row >> 7) * TT + r / G;
+  if (r >= TT * G || tok >= L) return;
+  auto place = [&](int k) { return (2ll * k + (k == b - 1)) * 256 + row; };
+  float m = -INFINITY;
+  for (int k = b - 1; k <= last; ++k) {
+    const float2 ml = *reinterpret_cast<const float2*>(p.part_ml + 2 * place(k));
+    m = fmaxf(m, ml.x);
+  }
+  const float mu = m == -INFINITY ? 0.f : m;
+  float l = 0.f, acc[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+  for (int k = b - 1; k <= last; ++k) {
+    const float2 ml = *reinterpret_cast<const float2*>(p.part_ml + 2 * place(k));
+    if (ml.y == 0.f) continue;  // nothing of the row in this piece (its O may be unwritten)
+    const float w = ex2_approx(ml.x - mu);
+    l += w * ml.y;
+    const float4* src = reinterpret_cast<const float4*>(p.part_o + place(k) * kHeadDim + cc);
+    const float4 a = src[0], e = src[1];
+    acc[0] += w * a.x; acc[1] += w * a.y; acc[2] += w * a.z; acc[3] += w * a.w;
+    acc[4] += w * e.x; acc[5] += w * e.y; acc[6] += w * e.z; acc[7] += w * e.w;
+  }
+  const bool any = l > 0.f || l != l;
+  const float inv = any ? 1.f / l : 0.f;
+  const long long t = (long long)seq0 + tok;
+  const int h = g * G + r % G;
+  uint4 o;
+  o.x = pack_bf16x2(acc[0] * inv, acc[1] * inv);
+  o.y = pack_bf16x2(acc[2] * inv, acc[3] * inv);
+  o.z = pack_bf16x2(acc[4] * inv, acc[5] * inv);
+  o.w = pack_bf16x2(acc[6] * inv, acc[7] * inv);
+  *reinterpret_cast<uint4*>(p.out + (t * c.hq + h) * kHeadDim + cc) = o;
+  if ((threadIdx.x & 15) == 0) {
+    const float z = any ? mu + log2f(l) : -INFINITY;
+    if (p.lse2) p.lse2[(long long)h * c.total_tokens + t] = z;
+    if (p.lse) p.lse[(long long)h * c.total_tokens + t] = z * 0.6931471805599453f;
+  }
+}
+
+}  // namespace tiles
+
+cudaError_t launch_cache_tiles(const CacheAttnParams& p, int sms, cudaStream_t st) {
+  static unsigned long long attr[kMaxCachedDevices] = {};
+  cudaError_t e = set_max_smem(reinterpret_cast<const void*>(tiles::cache_tiles_kernel), tiles::smem_bytes(kMaxSeqs), attr);
+  if (e != cudaSuccess) return e;
+  tiles::cache_tiles_kernel<<<sms, tiles::kThreads, tiles::smem_bytes(p.c.num_seqs), st>>>(p);
+  if ((e = cudaGetLastError()) != cudaSuccess || sms < 2) return e;
+  return launch_pdl(tiles::cache_tiles_join_kernel, dim3(sms - 1, 16), 256, 0, st, p);
+}
+
+}  // namespace fp

@@ -134,16 +134,21 @@ struct AppendParams {
   int32_t* dev_status;
 };
 
-struct CacheAttnParams {
+// Tensor maps first: they must be 64-byte aligned (rows schedule: unused).
+struct __align__(64) CacheAttnParams {
+  CUtensorMap tm_q;           // q as [T][Hq][128]: boxes of 64 columns x group heads x tile_tokens tokens
+  CUtensorMap tm_k, tm_v;     // the cache's rows x Hkv * 128: boxes of 64 columns x box_rows rows
+  int32_t tile_tokens;        // tokens of a 128-row tile: 128 / group
+  int32_t box_rows;           // rows of a K/V copy: the largest power of two up to 128 that divides page_size
   CacheInfo c;
   const uint16_t* q;          // [T, Hq, d], rows q_stride elements apart
   int64_t q_stride;
   float scale_log2;           // softmax_scale * log2(e)
   uint16_t* out;              // [T, Hq, d] bf16 bits
   float* lse;                 // [Hq, T] or null (natural log)
-  float* lse2;                // [Hq, T] workspace, log2 units (for the weights)
+  float* lse2;                // [Hq, T] workspace, log2 units (for the weights), or null
   float* part_o;              // workspace: partial outputs [2 * grid][rows][128], not normalised
-  float* part_ml;             // workspace: their running max (log2 units) and row sum [2 * grid][2][rows]
+  float* part_ml;             // workspace: their running max (log2 units) and row sum, 2 * grid * rows of each
   int32_t* meta;              // workspace: the unit that each CTA's range begins inside of [grid][kMetaWords]
   float decay;                // weights = decay * weights + this call's; < 0: weights are left alone
   int32_t* dev_status;
@@ -199,12 +204,15 @@ cudaError_t launch_attn(const AttnParams& p, int grid, cudaStream_t st);
 cudaError_t launch_append(const AppendParams& p, cudaStream_t st);
 cudaError_t launch_select(const SelectParams& p, cudaStream_t st);
 cudaError_t launch_compact(const CompactParams& p, cudaStream_t st);
-int cache_attn_grid(int sms);               // CTAs of the attention launch on a device of sms SMs
+constexpr int kMetaWords = 8;               // ints per CTA that describe the unit its share begins inside of
+// Schedule of the attention call: 16-row tiles (fp_cache_attn.cu) or 128-row tiles (fp_cache_tiles.cu).
+bool cache_attn_tiled(int32_t max_new, int32_t group);
 struct CacheAttnLayout {                    // byte offsets of its workspace
   int64_t part_o, part_ml, meta, lse2, total;
 };
-CacheAttnLayout cache_attn_layout(int sms, int64_t hq, int64_t total_tokens);
-cudaError_t launch_cache_attn(const CacheAttnParams& p, int sms, cudaStream_t st);
+CacheAttnLayout cache_attn_layout(int sms, bool tiled, int64_t hq, int64_t total_tokens);
+cudaError_t launch_cache_attn(const CacheAttnParams& p, bool tiled, int sms, cudaStream_t st);
+cudaError_t launch_cache_tiles(const CacheAttnParams& p, int sms, cudaStream_t st);
 cudaError_t launch_exp2_selftest(const float* x, float* y_poly, float* y_mufu, long long n, cudaStream_t st);
 
 }  // namespace fp
