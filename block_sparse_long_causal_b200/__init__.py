@@ -397,25 +397,28 @@ def _rows_of(t, name: str, tokens: int, heads: int, d: int, device):
     """Pointer and token-row stride of a bf16 [tokens, heads, head_dim] tensor whose rows may lie apart (a
     slice of a fused projection)."""
     _want(t, name, torch.bfloat16, device)
-    if tuple(t.shape) != (tokens, heads, d):
+    if t.shape != (tokens, heads, d):
         raise ValueError(f"{name} must be [{tokens}, {heads}, {d}], got {list(t.shape)}")
     if tokens == 0:
         return None, 0
-    if t.stride(2) != 1 or (heads > 1 and t.stride(1) != d):
+    st = t.stride()
+    if st[2] != 1 or (heads > 1 and st[1] != d):
         raise ValueError(f"{name}: the heads of a token must be contiguous")
-    return C.c_void_p(t.data_ptr()), int(t.stride(0)) if tokens > 1 else 0
+    return t.data_ptr(), st[0] if tokens > 1 else 0
 
 
-def _want(t, name: str, dtype, device, numel=None):
+def _want(t, name: str, dtype, device, numel=None) -> int:
+    """Check a tensor argument; its address. These calls are made once per token and layer: the checks are
+    plain attribute reads."""
     if not isinstance(t, torch.Tensor):
         raise ValueError(f"{name} must be a tensor")
-    if t.dtype != dtype:
+    if t.dtype is not dtype:
         raise ValueError(f"{name} must be {dtype}, got {t.dtype}")
     if t.device != device:
         raise ValueError(f"{name} is on {t.device}, the cache on {device}")
     if numel is not None and (t.numel() != numel or not t.is_contiguous()):
         raise ValueError(f"{name} must be contiguous with {numel} elements")
-    return t
+    return t.data_ptr()
 
 
 class KVCache:
@@ -456,13 +459,13 @@ class KVCache:
             self.c.weights = weights.data_ptr()
         if positions is not None:
             self.c.positions = positions.data_ptr()
+        # what every call looks up, as plain attributes
+        self.ref, self.p_ref = C.byref(self.c), p.ref
+        self.tokens, self.seqs = int(p.total_tokens), int(p.num_seqs)
+        self.hq, self.hkv, self.d = int(p.num_q_heads), hkv, d
 
     def __getattr__(self, name):
         return getattr(self.__dict__["c"], name)
-
-    @property
-    def ref(self):
-        return C.byref(self.c)
 
 
 def kv_cache(p: Problem, k_cache, v_cache, lens, block_table, page_size: int, weights=None, positions=None,
@@ -471,25 +474,33 @@ def kv_cache(p: Problem, k_cache, v_cache, lens, block_table, page_size: int, we
 
 
 def _cache_args(p: Problem, c: KVCache, next_pos, dev_status):
+    """Addresses of next_pos and dev_status (None: NULL)."""
     if p is not c.p:
         raise ValueError("the cache was described for another problem (kv_cache(p, ...))")
-    for name, t, n in (("next_pos", next_pos, p.num_seqs), ("dev_status", dev_status, 1)):
-        if t is not None:
-            _want(t, name, torch.int32, c.device, n)
+    return (None if next_pos is None else _want(next_pos, "next_pos", torch.int32, c.device, c.seqs),
+            None if dev_status is None else _want(dev_status, "dev_status", torch.int32, c.device, 1))
 
 
 def _call(c: KVCache, fn, *args, stream):
     """fn on the cache's device, on `stream` or that device's current one."""
-    with torch.cuda.device(c.device):
-        _check(fn(*args, _stream(stream)))
+    dev = c.device
+    if dev.type != "cuda":
+        raise ValueError(f"the cache is on {dev}: the kernels run on a CUDA device only")
+    if torch.cuda.current_device() != dev.index:
+        with torch.cuda.device(dev):
+            return _call(c, fn, *args, stream=stream)
+    raw = torch._C._cuda_getCurrentRawStream(dev.index) if stream is None else _stream(stream)
+    st = fn(c.p_ref, c.ref, *args, raw)
+    if st != FP_OK:
+        _check(st)
 
 
 def cache_append(p: Problem, c: KVCache, k, v, next_pos=None, dev_status=None, stream=None):
     """fp_cache_append: the new tokens' K and V rows into their slots."""
-    _cache_args(p, c, next_pos, dev_status)
-    kp, ks = _rows_of(k, "k", p.total_tokens, p.num_kv_heads, p.head_dim, c.device)
-    vp, vs = _rows_of(v, "v", p.total_tokens, p.num_kv_heads, p.head_dim, c.device)
-    _call(c, _lib.fp_cache_append, p.ref, c.ref, kp, ks, vp, vs, _ptr(next_pos), _ptr(dev_status), stream=stream)
+    pos, status = _cache_args(p, c, next_pos, dev_status)
+    kp, ks = _rows_of(k, "k", c.tokens, c.hkv, c.d, c.device)
+    vp, vs = _rows_of(v, "v", c.tokens, c.hkv, c.d, c.device)
+    _call(c, _lib.fp_cache_append, kp, ks, vp, vs, pos, status, stream=stream)
 
 
 def cache_attn_workspace(p: Problem, c: KVCache) -> int:
@@ -502,42 +513,41 @@ def cache_attn_workspace(p: Problem, c: KVCache) -> int:
 def cache_attn(p: Problem, c: KVCache, q, softmax_scale: float, workspace, out, lse=None, decay=None, dev_status=None,
                stream=None):
     """fp_cache_attn; decay None leaves the cache's weights alone."""
-    _cache_args(p, c, None, dev_status)
-    qp, qs = _rows_of(q, "q", p.total_tokens, p.num_q_heads, p.head_dim, c.device)
-    _want(out, "out", torch.bfloat16, c.device, p.total_tokens * p.num_q_heads * p.head_dim)
-    if lse is not None:
-        _want(lse, "lse", torch.float32, c.device, p.total_tokens * p.num_q_heads)
-    if workspace.device != c.device:
-        raise ValueError(f"workspace is on {workspace.device}, the cache on {c.device}")
-    if decay is not None and not 0.0 <= decay <= 1.0:
+    _, status = _cache_args(p, c, None, dev_status)
+    qp, qs = _rows_of(q, "q", c.tokens, c.hq, c.d, c.device)
+    rows = c.tokens * c.hq
+    op = _want(out, "out", torch.bfloat16, c.device, rows * c.d)
+    lp = None if lse is None else _want(lse, "lse", torch.float32, c.device, rows)
+    if workspace.device != c.device or not workspace.is_contiguous():
+        raise ValueError(f"workspace must be contiguous on {c.device}")
+    if decay is None:
+        decay = -1.0
+    elif not 0.0 <= decay <= 1.0:
         raise ValueError("decay must be in [0, 1]")
-    _call(c, _lib.fp_cache_attn, p.ref, c.ref, qp, qs, float(softmax_scale), _ptr(workspace),
-          workspace.numel() * workspace.element_size(), _ptr(out), _ptr(lse), -1.0 if decay is None else float(decay),
-          _ptr(dev_status), stream=stream)
+    _call(c, _lib.fp_cache_attn, qp, qs, softmax_scale, workspace.data_ptr(),
+          workspace.numel() * workspace.element_size(), op, lp, decay, status, stream=stream)
 
 
-def _move_args(p: Problem, c: KVCache, budget: int, moves, move_counts, new_lens):
-    n = p.num_seqs * p.num_kv_heads
-    _want(moves, "moves", torch.int32, c.device, 2 * n * budget)
-    _want(move_counts, "move_counts", torch.int32, c.device, n)
-    _want(new_lens, "new_lens", torch.int32, c.device, p.num_seqs)
+def _move_args(c: KVCache, budget: int, moves, move_counts, new_lens):
+    n = c.seqs * c.hkv
+    return (_want(moves, "moves", torch.int32, c.device, 2 * n * budget),
+            _want(move_counts, "move_counts", torch.int32, c.device, n),
+            _want(new_lens, "new_lens", torch.int32, c.device, c.seqs))
 
 
 def cache_select(p: Problem, c: KVCache, budget: int, sinks: int, recent: int, next_pos, moves, move_counts, new_lens,
                  dev_status=None, stream=None):
     """fp_cache_select: the slots that stay, as moves int32 [num_seqs, Hkv, budget, 2]."""
-    _cache_args(p, c, next_pos, dev_status)
-    _move_args(p, c, int(budget), moves, move_counts, new_lens)
-    _call(c, _lib.fp_cache_select, p.ref, c.ref, int(budget), int(sinks), int(recent), _ptr(next_pos), _ptr(moves),
-          _ptr(move_counts), _ptr(new_lens), _ptr(dev_status), stream=stream)
+    pos, status = _cache_args(p, c, next_pos, dev_status)
+    out = _move_args(c, budget, moves, move_counts, new_lens)
+    _call(c, _lib.fp_cache_select, budget, sinks, recent, pos, *out, status, stream=stream)
 
 
 def cache_compact(p: Problem, c: KVCache, budget: int, moves, move_counts, new_lens, dev_status=None, stream=None):
     """fp_cache_compact: apply the moves of cache_select and set lens."""
-    _cache_args(p, c, None, dev_status)
-    _move_args(p, c, int(budget), moves, move_counts, new_lens)
-    _call(c, _lib.fp_cache_compact, p.ref, c.ref, int(budget), _ptr(moves), _ptr(move_counts), _ptr(new_lens),
-          _ptr(dev_status), stream=stream)
+    _, status = _cache_args(p, c, None, dev_status)
+    out = _move_args(c, budget, moves, move_counts, new_lens)
+    _call(c, _lib.fp_cache_compact, budget, *out, status, stream=stream)
 
 
 class SparsePrefill:

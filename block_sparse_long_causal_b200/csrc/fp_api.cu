@@ -226,7 +226,7 @@ unsigned long long context_id() {
   return id;
 }
 
-cudaError_t set_max_smem(const void* func, int bytes, unsigned long long (&done)[kMaxCachedDevices]) {
+cudaError_t set_max_smem(const void* func, int bytes, unsigned long long (&done)[kMaxCachedDevices], bool carveout) {
   static std::mutex mu;
   int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);
@@ -238,6 +238,8 @@ cudaError_t set_max_smem(const void* func, int bytes, unsigned long long (&done)
     if (id != 0 && done[dev] == id) return cudaSuccess;
   }
   e = cudaFuncSetAttribute(func, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+  if (e == cudaSuccess && carveout)
+    e = cudaFuncSetAttribute(func, cudaFuncAttributePreferredSharedMemoryCarveout, cudaSharedmemCarveoutMaxShared);
   if (e == cudaSuccess && cached) done[dev] = context_id();  // the call above made the context current
   return e;
 }
@@ -863,7 +865,7 @@ fp_status fp_cache_select(const fp_problem* p, const fp_kv_cache* c, int32_t bud
   a.move_counts = move_counts;
   a.new_lens = new_lens;
   a.dev_status = dev_status;
-  return cuda_status(fp::launch_select(a, static_cast<cudaStream_t>(stream)), "selection launch");
+  return cuda_status(fp::launch_select(a, sm_count(), static_cast<cudaStream_t>(stream)), "selection launch");
 }
 
 fp_status fp_cache_compact(const fp_problem* p, const fp_kv_cache* c, int32_t budget, const int32_t* moves,
@@ -879,7 +881,7 @@ fp_status fp_cache_compact(const fp_problem* p, const fp_kv_cache* c, int32_t bu
   a.move_counts = move_counts;
   a.new_lens = new_lens;
   a.dev_status = dev_status;
-  return cuda_status(fp::launch_compact(a, static_cast<cudaStream_t>(stream)), "compaction launch");
+  return cuda_status(fp::launch_compact(a, sm_count(), static_cast<cudaStream_t>(stream)), "compaction launch");
 }
 
 fp_status fp_selftest_exp2(const float* x, float* y_poly, float* y_mufu, int64_t n, void* stream) {

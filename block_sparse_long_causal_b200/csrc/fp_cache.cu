@@ -72,103 +72,170 @@ __device__ __forceinline__ uint32_t rank_key(float w, bool safe) {
   return (b & 0x80000000u) ? ~b : (b | 0x80000000u);
 }
 
-constexpr int kSelThreads = 1024;
+constexpr int kSelThreads = 512, kSelWarps = kSelThreads / 32;
+constexpr int kSelCluster = 16;      // largest cluster
+constexpr int kSelSpan = 8192;       // slots a CTA is meant to take (16 a thread)
+constexpr int kSelKeysMax = 24576;   // keys kept in shared memory (96 KB: two CTAs fit an SM)
 
-// One CTA per (sequence, kv-head). The key of rank `budget` is found by a radix select (four passes of
-// eight bits over the keys, each a histogram of the keys that match the prefix so far); then every warp
-// counts, over its own contiguous range of slots, the slots above and at the threshold, and after a
-// scan writes its holes (evicted slots below the budget) and sources (kept slots at or past it) in
-// ascending order.
-__global__ void __launch_bounds__(kSelThreads) select_kernel(const SelectParams p) {
+// One cluster per (sequence, kv-head); each of its CTAs takes a contiguous range of the slots, a
+// contiguous part of it per warp. The slots are read once: their keys stay in shared memory (a range
+// longer than kSelKeysMax is read again in every pass). The key of rank `budget` is found by a radix select,
+// four passes of eight bits over the keys that match the prefix so far; the CTAs' histograms are summed
+// through distributed shared memory, one cluster barrier a pass. Then every warp counts its slots above and
+// at the threshold, and after a scan over the cluster's warps writes its holes (evicted slots below the
+// budget) and sources (kept slots at or past it) in ascending order.
+__global__ void __launch_bounds__(kSelThreads, 2) select_kernel(const SelectParams p, const int keys_cap) {
+  extern __shared__ uint32_t s_keys[];
+  __shared__ unsigned s_hist[2][256];
+  __shared__ unsigned s_tot[8], s_pick[2];
+  __shared__ int4 s_cnt[kSelWarps];                // slots above / at the threshold, below / past the budget
+  __shared__ int s_eq[kSelCluster * kSelWarps + 1], s_hole[kSelCluster * kSelWarps + 1], s_from[kSelCluster * kSelWarps + 1];
+  __shared__ int s_part[3][8];
+  const cg::cluster_group cluster = cg::this_cluster();
+  const int rank = (int)cluster.block_rank(), C = (int)cluster.num_blocks();
   const CacheInfo& c = p.c;
-  const int s = blockIdx.x / c.hkv, g = blockIdx.x % c.hkv;
+  const int sg = blockIdx.x / C, s = sg / c.hkv, g = sg % c.hkv;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  constexpr int kWarps = kSelThreads / 32;
-  __shared__ unsigned s_hist[256];
-  __shared__ unsigned s_prefix, s_need;
-  __shared__ int s_gt[2][kWarps], s_eq[2][kWarps];
   const int lo = __ldg(c.cu_seqlens + s), hi = __ldg(c.cu_seqlens + s + 1), len = c.lens[s], L = hi - lo;
-  int32_t* moves = p.moves + ((long long)s * c.hkv + g) * p.budget * 2;
+  int32_t* moves = p.moves + (long long)sg * p.budget * 2;
   const bool bad_seq = L < 0 || len < 0 || len > c.max_len - L;
   const int n = bad_seq ? 0 : len + L;
-  if (tid == 0 && bad_seq) dev_flag(p.dev_status, kDevBadProblem);
-  if (tid == 0 && g == 0) p.new_lens[s] = bad_seq ? len : min(n, p.budget);
+  if (tid == 0 && rank == 0) {
+    if (bad_seq) dev_flag(p.dev_status, kDevBadProblem);
+    if (g == 0) p.new_lens[s] = bad_seq ? len : min(n, p.budget);
+  }
   if (n <= p.budget) {  // nothing to evict (or a sequence that is skipped: no moves, lens as it was)
-    if (tid == 0) p.move_counts[(long long)s * c.hkv + g] = 0;
-    for (int i = tid; i < 2 * p.budget; i += kSelThreads) moves[i] = -1;
+    if (tid == 0 && rank == 0) p.move_counts[sg] = 0;
+    for (long long i = rank * kSelThreads + tid; i < 2ll * p.budget; i += C * kSelThreads) moves[i] = -1;
     return;
   }
   // positions at or past `young` are protected (the difference cannot overflow: 64 bits)
   const long long young = (long long)(p.next_pos ? p.next_pos[s] : len) + L - p.recent;
   bool bad_page = false;
-  auto key_of = [&](int u) -> uint32_t {
+  auto read_key = [&](int u) -> uint32_t {
     const long long w = slot_word(c, s, g, u);
     if (w < 0) {
       bad_page = true;
       return 0u;
     }
-    const int pos = c.positions ? c.positions[w] : u;
-    return rank_key(c.weights[w], pos < p.sinks || pos >= young);
+    const int pos = c.positions ? __ldg(c.positions + w) : u;
+    return rank_key(__ldg(c.weights + w), pos < p.sinks || pos >= young);
   };
+  const int wspan = (int)((((long long)n + C * kSelWarps - 1) / (C * kSelWarps) + 31) & ~31ll);  // slots a warp
+  const long long first = (long long)rank * kSelWarps * wspan;
+  const int base = (int)min((long long)n, first);
+  const int u0 = (int)min((long long)n, first + warp * wspan), u1 = min(n, u0 + wspan);
+  const bool kept = kSelWarps * wspan <= keys_cap;
+  if (kept) {
+#pragma unroll 8
+    for (int u = u0 + lane; u < u1; u += 32) s_keys[u - base] = read_key(u);
+    __syncwarp();  // a warp reads back its own keys only
+  }
+  auto key_of = [&](int u) -> uint32_t { return kept ? s_keys[u - base] : read_key(u); };
+  if (tid < 256) s_hist[0][tid] = 0;
+  __syncthreads();
   unsigned prefix = 0, need = (unsigned)p.budget;  // `need` keys of the current prefix class stay
-  for (int shift = 24; shift >= 0; shift -= 8) {
-    for (int i = tid; i < 256; i += kSelThreads) s_hist[i] = 0;
-    __syncthreads();
-    for (int u = tid; u < n; u += kSelThreads) {
-      const uint32_t k = key_of(u);
-      if (shift == 24 || (k >> (shift + 8)) == prefix) atomicAdd(&s_hist[(k >> shift) & 255u], 1u);
+#pragma unroll 1
+  for (int pass = 0; pass < 4; ++pass) {
+    const int shift = 24 - 8 * pass;
+    unsigned* hist = s_hist[pass & 1];
+    for (int u = u0; u < u1; u += 32) {
+      const bool in = u + lane < u1;
+      const uint32_t k = in ? key_of(u + lane) : 0u;
+      const bool match = in && (pass == 0 || (k >> (shift + 8)) == prefix);
+      const unsigned act = __ballot_sync(kFullMask, match);
+      if (match) {  // equal digits of a warp (protected slots, ties) are added once
+        const unsigned dig = (k >> shift) & 255u, same = __match_any_sync(act, dig);
+        if (lane == __ffs(same) - 1) atomicAdd(&hist[dig], (unsigned)__popc(same));
+      }
+    }
+    cluster.sync();
+    // digit d of the whole cluster in thread 255 - d, so that an inclusive scan counts the larger digits
+    unsigned cnt = 0, incl = 0;
+    if (tid < 256) {
+      for (int r = 0; r < C; ++r) cnt += *cluster.map_shared_rank(&hist[255 - tid], r);
+      incl = cnt;
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const unsigned x = __shfl_up_sync(kFullMask, incl, o);
+        if (lane >= o) incl += x;
+      }
+      if (lane == 31) s_tot[warp] = incl;
+      // the other buffer is read by no CTA any more: all have passed the barrier above
+      s_hist[(pass + 1) & 1][tid] = 0;
     }
     __syncthreads();
-    if (tid == 0) {
-      unsigned left = need;
-      int b = 255;
-      while (b > 0 && s_hist[b] < left) left -= s_hist[b--];
-      s_prefix = (prefix << 8) | (unsigned)b;
-      s_need = left;
+    if (tid < 256) {
+      for (int w = 0; w < warp; ++w) incl += s_tot[w];
+      if (incl >= need && incl - cnt < need) {
+        s_pick[0] = 255u - tid;
+        s_pick[1] = need - (incl - cnt);
+      }
     }
     __syncthreads();
-    prefix = s_prefix;
-    need = s_need;
+    prefix = (prefix << 8) | s_pick[0];
+    need = s_pick[1];
   }
   const uint32_t thr = prefix;  // keys above thr stay, and the first `need` slots whose key is thr
-  const int span = ((n + kWarps - 1) / kWarps + 31) & ~31;
-  const int u0 = min(n, warp * span), u1 = min(n, u0 + span);
-  int gt[2] = {0, 0}, eq[2] = {0, 0};  // below / at or past the budget
+  int4 cnt = make_int4(0, 0, 0, 0);
   for (int u = u0; u < u1; u += 32) {
     const bool in = u + lane < u1;
     const uint32_t k = in ? key_of(u + lane) : 0u;
-    const unsigned below = __ballot_sync(kFullMask, in && u + lane < p.budget);
+    const unsigned below = __ballot_sync(kFullMask, u + lane < p.budget);
     const unsigned mg = __ballot_sync(kFullMask, in && k > thr), me = __ballot_sync(kFullMask, in && k == thr);
-    gt[0] += __popc(mg & below);
-    gt[1] += __popc(mg & ~below);
-    eq[0] += __popc(me & below);
-    eq[1] += __popc(me & ~below);
+    cnt.x += __popc(mg & below);
+    cnt.y += __popc(mg & ~below);
+    cnt.z += __popc(me & below);
+    cnt.w += __popc(me & ~below);
   }
-  if (lane == 0)
-    for (int i = 0; i < 2; ++i) {
-      s_gt[i][warp] = gt[i];
-      s_eq[i][warp] = eq[i];
-    }
+  if (lane == 0) s_cnt[warp] = cnt;
+  cluster.sync();
+  // ---- scans over the cluster's warps in slot order: slots at the threshold before a warp, then its
+  // holes and sources (the kept slots at the threshold are the first `need` of them)
+  const int W = C * kSelWarps;
+  int4 mine = make_int4(0, 0, 0, 0);
+  if (tid < W) mine = *cluster.map_shared_rank(&s_cnt[tid % kSelWarps], tid / kSelWarps);
+  int eq = mine.z + mine.w, eqi = eq;
+  if (tid < 256) {
+    eqi = warp_incl_scan(eq);
+    if (lane == 31) s_part[0][warp] = eqi;
+  }
   __syncthreads();
-  // kept slots at the threshold are the first `need` in slot order: walk the warps before this one
-  int eq_before = 0, hole = 0, from = 0, total = 0;
-  {
-    int e = 0;
-    for (int w = 0; w < kWarps; ++w) {
-      const int a = min(n, w * span), b = min(n, a + span);
-      const int room = max(0, (int)need - e);
-      const int k0 = min(s_eq[0][w], room), k1 = min(s_eq[1][w], room - k0);
-      const int holes = max(0, min(b, p.budget) - min(a, p.budget)) - s_gt[0][w] - k0;
-      const int stay = s_gt[1][w] + k1;
-      if (w < warp) {
-        hole += holes;
-        from += stay;
-        eq_before += s_eq[0][w] + s_eq[1][w];
-      }
-      total += stay;
-      e += s_eq[0][w] + s_eq[1][w];
+  int hole = 0, from = 0, hi_ = 0, fi = 0;
+  if (tid < 256) {
+    for (int w = 0; w < warp; ++w) eqi += s_part[0][w];
+    if (tid < W) {
+      const int room = max(0, (int)need - (eqi - eq));
+      const int k0 = min(mine.z, room), k1 = min(mine.w, room - k0);
+      const long long wa = (long long)tid * wspan;
+      const int a = (int)min((long long)n, wa), b = (int)min((long long)n, wa + wspan);
+      hole = min(b, p.budget) - min(a, p.budget) - mine.x - k0;
+      from = mine.y + k1;
+    }
+    hi_ = warp_incl_scan(hole);
+    fi = warp_incl_scan(from);
+    if (lane == 31) {
+      s_part[1][warp] = hi_;
+      s_part[2][warp] = fi;
     }
   }
+  __syncthreads();
+  if (tid < 256) {
+    for (int w = 0; w < warp; ++w) {
+      hi_ += s_part[1][w];
+      fi += s_part[2][w];
+    }
+    s_eq[tid] = eqi - eq;
+    s_hole[tid] = hi_ - hole;
+    s_from[tid] = fi - from;
+    if (tid == 255) s_from[256] = fi;
+  }
+  __syncthreads();
+  const int me_w = rank * kSelWarps + warp;
+  int eq_before = s_eq[me_w];
+  hole = s_hole[me_w];
+  from = s_from[me_w];
+  const int total = s_from[256];
   for (int u = u0; u < u1; u += 32) {
     const bool in = u + lane < u1;
     const uint32_t k = in ? key_of(u + lane) : 0u;
@@ -177,32 +244,56 @@ __global__ void __launch_bounds__(kSelThreads) select_kernel(const SelectParams 
     const bool keep = in && (k > thr || (k == thr && eq_before + __popc(me & lt) < (int)need));
     const bool low = u + lane < p.budget;
     const unsigned mh = __ballot_sync(kFullMask, in && low && !keep), ms = __ballot_sync(kFullMask, keep && !low);
-    if (in && low && !keep) moves[2 * (hole + __popc(mh & lt)) + 1] = u + lane;
-    if (keep && !low) moves[2 * (from + __popc(ms & lt))] = u + lane;
+    if (in && low && !keep) moves[2ll * (hole + __popc(mh & lt)) + 1] = u + lane;
+    if (keep && !low) moves[2ll * (from + __popc(ms & lt))] = u + lane;
     hole += __popc(mh);
     from += __popc(ms);
     eq_before += __popc(me);
   }
-  for (int i = 2 * total + tid; i < 2 * p.budget; i += kSelThreads) moves[i] = -1;
-  if (tid == 0) p.move_counts[(long long)s * c.hkv + g] = total;
+  for (long long i = 2ll * total + rank * kSelThreads + tid; i < 2ll * p.budget; i += C * kSelThreads) moves[i] = -1;
+  if (tid == 0 && rank == 0) p.move_counts[sg] = total;
   if (bad_page) dev_flag(p.dev_status, kDevBadProblem);
+  cluster.sync();  // no CTA ends while another still reads its counts
 }
 
-cudaError_t launch_select(const SelectParams& p, cudaStream_t st) {
-  select_kernel<<<p.c.num_seqs * p.c.hkv, kSelThreads, 0, st>>>(p);
-  return cudaGetLastError();
+cudaError_t launch_select(const SelectParams& p, int sms, cudaStream_t st) {
+  static unsigned long long attr[kMaxCachedDevices] = {};
+  const void* fn = reinterpret_cast<const void*>(select_kernel);
+  cudaError_t e = set_max_smem(fn, kSelKeysMax * 4, attr);
+  if (e == cudaSuccess) e = cudaFuncSetAttribute(fn, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
+  if (e != cudaSuccess) return e;
+  // clusters grow with the longest sequence that there may be, while one wave of two CTAs an SM holds them
+  const long long pairs = (long long)p.c.num_seqs * p.c.hkv;
+  int C = 1;
+  while (C < kSelCluster && (long long)C * kSelSpan < p.c.max_len && pairs * C * 2 <= 2 * sms) C *= 2;
+  const long long span = (((long long)p.c.max_len + C * kSelWarps - 1) / (C * kSelWarps) + 31) / 32 * 32 * kSelWarps;
+  const int cap = (int)(span < kSelKeysMax ? span : kSelKeysMax);
+  cudaLaunchAttribute at[1];
+  at[0].id = cudaLaunchAttributeClusterDimension;
+  at[0].val.clusterDim.x = C;
+  at[0].val.clusterDim.y = at[0].val.clusterDim.z = 1;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)(pairs * C));
+  cfg.blockDim = dim3(kSelThreads);
+  cfg.dynamicSmemBytes = (size_t)cap * 4;
+  cfg.stream = st;
+  cfg.attrs = at;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, select_kernel, p, cap);
 }
 
 // ------------------------------------------------------------------------ compaction ------------
-// One warp per move: lanes 0..15 carry the K row, lanes 16..31 the V row, 16 bytes each. Sources lie at
-// or past the budget and destinations below it (checked), so no move reads what another one writes
-// and the order of the moves does not matter.
+// A warp takes eight moves at a time: their entries and page look-ups in eight lanes at once, then the rows
+// with all eight loads in flight, lanes 0..15 the K row and lanes 16..31 the V row, 16 bytes each. Sources
+// lie at or past the budget and destinations below it (checked), so no move reads what another one
+// writes and the order of the moves does not matter.
+constexpr int kMovesW = 8;
 __global__ void __launch_bounds__(256) compact_kernel(const CompactParams p) {
   const CacheInfo& c = p.c;
   const int lane = threadIdx.x & 31, sg = blockIdx.x / p.parts, part = blockIdx.x % p.parts;
   const int s = sg / c.hkv, g = sg % c.hkv;
   const int cnt = p.move_counts[sg];
-  const int slots = min((long long)c.max_len, (long long)c.max_pages * c.page_size);
+  const int slots = (int)min((long long)c.max_len, (long long)c.max_pages * c.page_size);
   if (part == 0 && threadIdx.x == 0) {
     if (cnt < 0 || cnt > p.budget) dev_flag(p.dev_status, kDevBadList);
     if (g == 0) {
@@ -212,32 +303,53 @@ __global__ void __launch_bounds__(256) compact_kernel(const CompactParams p) {
     }
   }
   const int2* moves = reinterpret_cast<const int2*>(p.moves) + (long long)sg * p.budget;
-  for (int i = part * 8 + (threadIdx.x >> 5); i < min(cnt, p.budget); i += p.parts * 8) {
-    const int2 mv = moves[i];
-    if (mv.x < p.budget || mv.x >= slots || mv.y < 0 || mv.y >= p.budget || mv.y >= slots) {
-      if (lane == 0) dev_flag(p.dev_status, kDevBadList);
-      continue;
+  const int n = min(cnt, p.budget);
+  for (long long i = (part * 8 + (threadIdx.x >> 5)) * kMovesW; i < n; i += p.parts * 8 * kMovesW) {
+    long long src = -1, dst = -1;
+    if (lane < kMovesW && i + lane < n) {
+      const int2 mv = moves[i + lane];
+      if (mv.x < p.budget || mv.x >= slots || mv.y < 0 || mv.y >= p.budget || mv.y >= slots) {
+        dev_flag(p.dev_status, kDevBadList);
+      } else {
+        src = slot_row(c, s, mv.x);
+        dst = slot_row(c, s, mv.y);
+        if (src < 0 || dst < 0) {
+          dev_flag(p.dev_status, kDevBadProblem);
+          src = -1;
+        }
+      }
     }
-    const long long src = slot_row(c, s, mv.x), dst = slot_row(c, s, mv.y);
-    if (src < 0 || dst < 0) {
-      if (lane == 0) dev_flag(p.dev_status, kDevBadProblem);
-      continue;
+    float w = 0.f;
+    int pos = 0;
+    const long long ps = src / c.page_size, pd = dst / c.page_size;
+    const long long ws = (ps * c.hkv + g) * c.page_size + (src - ps * c.page_size);
+    const long long wd = (pd * c.hkv + g) * c.page_size + (dst - pd * c.page_size);
+    if (src >= 0 && c.weights) w = c.weights[ws];
+    if (src >= 0 && c.positions) pos = c.positions[ws];
+    uint4* rows = reinterpret_cast<uint4*>(lane < 16 ? c.k : c.v) + (lane & 15);
+    uint4 v[kMovesW];
+#pragma unroll
+    for (int m = 0; m < kMovesW; ++m) {
+      const long long a = __shfl_sync(kFullMask, src, m);
+      if (a >= 0) v[m] = rows[(a * c.hkv + g) * 16];
     }
-    uint4* base = reinterpret_cast<uint4*>(lane < 16 ? c.k : c.v) + (lane & 15);
-    base[(dst * c.hkv + g) * 16] = base[(src * c.hkv + g) * 16];
-    if (lane < 2) {
-      const long long ws = (src / c.page_size * c.hkv + g) * c.page_size + src % c.page_size;
-      const long long wd = (dst / c.page_size * c.hkv + g) * c.page_size + dst % c.page_size;
-      if (lane == 0 && c.weights) c.weights[wd] = c.weights[ws];
-      if (lane == 1 && c.positions) c.positions[wd] = c.positions[ws];
+#pragma unroll
+    for (int m = 0; m < kMovesW; ++m) {
+      const long long a = __shfl_sync(kFullMask, src, m), b = __shfl_sync(kFullMask, dst, m);
+      if (a >= 0) rows[(b * c.hkv + g) * 16] = v[m];
     }
+    if (src >= 0 && c.weights) c.weights[wd] = w;
+    if (src >= 0 && c.positions) c.positions[wd] = pos;
   }
 }
 
-cudaError_t launch_compact(const CompactParams& in, cudaStream_t st) {
+cudaError_t launch_compact(const CompactParams& in, int sms, cudaStream_t st) {
   CompactParams p = in;
-  p.parts = p.budget < 64 * 64 ? (p.budget + 63) / 64 : 64;
-  compact_kernel<<<p.c.num_seqs * p.c.hkv * p.parts, 256, 0, st>>>(p);
+  // about four CTAs an SM over all pairs, and no more than one chunk a warp needs
+  const long long pairs = (long long)p.c.num_seqs * p.c.hkv, most = ((long long)p.budget + 8 * kMovesW - 1) / (8 * kMovesW);
+  const long long want = (4ll * sms + pairs - 1) / pairs;
+  p.parts = (int)(want < most ? want : most);
+  compact_kernel<<<(unsigned)(pairs * p.parts), 256, 0, st>>>(p);
   return cudaGetLastError();
 }
 

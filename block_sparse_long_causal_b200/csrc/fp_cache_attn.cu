@@ -295,8 +295,7 @@ __global__ void __launch_bounds__(kRowThreads, 2) cache_rows_kernel(const __grid
       if (whole) w[i] *= lt > 0.f || lt != lt ? 1.f / lt : 0.f;
       if (warp == 0 && (lane & 3) == 0) {
         if (!whole) {
-          p.part_ml[slot * 2 * kRowsT + r] = mt;
-          p.part_ml[slot * 2 * kRowsT + kRowsT + r] = lt;
+          *reinterpret_cast<float2*>(p.part_ml + 2 * (slot * kRowsT + r)) = make_float2(mt, lt);
         } else {
           const int pr = cur.rt * kRowsT + r;
           if (pr < cur.L * c.group) {
@@ -344,48 +343,89 @@ __global__ void __launch_bounds__(kRowThreads, 2) cache_rows_kernel(const __grid
   cp_async_wait<0>();
 }
 
-// Joins the pieces of a unit that several CTAs share. Block b looks at the unit inside of which the
-// range of CTA b + 1 begins (meta), and works when that CTA is the first such of its unit: the pieces
-// are the last one of CTA b (slot 1) and the first one (slot 0) of every CTA up to meta[1].
-__global__ void __launch_bounds__(256) cache_join_kernel(const __grid_constant__ CacheAttnParams p) {
+// Joins the pieces of the units that several CTAs share. Block (b, y) looks at the unit inside of which the
+// share of CTA b + 1 begins (meta) and works when that CTA is the first such of its unit: the pieces are
+// the last one of CTA b (place 1) and the first one (place 0) of every CTA up to meta[1]. 16 rows a block.
+// The time is one chain of dependent reads (meta, maxima, accumulators), so the pieces of a row are read
+// side by side: 32 maxima a warp at once, and where rows are few the warps share a row's pieces.
+template <bool kTiled>
+__global__ void __launch_bounds__(512) cache_join_kernel(const __grid_constant__ CacheAttnParams p) {
+  constexpr int kRowsU = kTiled ? 2 * kTileM : kRowsT;  // rows of a piece
+  __shared__ float4 s_acc[16][32];
   pdl_wait();
   const int b = blockIdx.x + 1;
-  const int32_t* meta = p.meta + (long long)b * kMetaWords;
-  if (meta[0] == 0) return;
+  const int4 meta = *reinterpret_cast<const int4*>(p.meta + (long long)b * kMetaWords);
+  const int2 meta2 = *reinterpret_cast<const int2*>(p.meta + (long long)b * kMetaWords + 4);
+  if (meta.x == 0) return;
   const CacheInfo& c = p.c;
-  const int last = meta[1], seq0 = meta[2], g = meta[3], row0 = meta[4], rows = meta[5];
-  const int r = threadIdx.x >> 4, cc = (threadIdx.x & 15) * 8;
-  const int pr = row0 + r;
-  if (pr >= rows) return;
-  float m = -INFINITY;
-  for (int k = b - 1; k <= last; ++k) {
-    const long long slot = 2ll * k + (k == b - 1);
-    m = fmaxf(m, p.part_ml[slot * 2 * kRowsT + r]);
+  const int P = meta.y - b + 2, seq0 = meta.z, g = meta.w, G = c.group;
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  // meta2: first token and tokens of the sequence (tiled), first packed row and packed rows (not)
+  int wr = 1;  // warps that share a row
+  if (!kTiled)
+    while (wr < 16 && 16 / (2 * wr) >= meta2.y - meta2.x) wr *= 2;
+  const int row = blockIdx.y * 16 + warp / wr, slice = warp % wr;
+  int tok, head;
+  bool in;
+  if (kTiled) {
+    const int r = row & 127, TT = p.tile_tokens;
+    tok = meta2.x + (row >> 7) * TT + r / G;
+    head = r % G;
+    in = r < TT * G && tok < meta2.y;
+  } else {
+    const int pr = meta2.x + row;
+    tok = pr / G;
+    head = pr % G;
+    in = pr < meta2.y && row < kRowsU;
   }
+  if (wr == 1 && !in) return;
+  auto place = [&](int k) { return (2ll * (b - 1 + k) + (k == 0)) * kRowsU + (in ? row : 0); };
+  auto ml_of = [&](int k) {
+    return k < P ? *reinterpret_cast<const float2*>(p.part_ml + 2 * place(k)) : make_float2(-INFINITY, 0.f);
+  };
+  float m = -INFINITY;
+  for (int k = lane; k < P; k += 32) m = fmaxf(m, ml_of(k).x);
+#pragma unroll
+  for (int o = 16; o >= 1; o >>= 1) m = fmaxf(m, __shfl_xor_sync(kAll, m, o));
   const float mu = m == -INFINITY ? 0.f : m;
-  float l = 0.f, acc[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
-  for (int k = b - 1; k <= last; ++k) {
-    const long long slot = 2ll * k + (k == b - 1);
-    const float w = ex2_approx(p.part_ml[slot * 2 * kRowsT + r] - mu);
-    l += w * p.part_ml[slot * 2 * kRowsT + kRowsT + r];
-    const float4* src = reinterpret_cast<const float4*>(p.part_o + (slot * kRowsT + r) * kHeadDim + cc);
-    const float4 a = src[0], d = src[1];
-    acc[0] += w * a.x; acc[1] += w * a.y; acc[2] += w * a.z; acc[3] += w * a.w;
-    acc[4] += w * d.x; acc[5] += w * d.y; acc[6] += w * d.z; acc[7] += w * d.w;
+  float l = 0.f;
+  float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+  for (int k0 = 0; k0 < P; k0 += 32) {
+    const float2 ml = ml_of(k0 + lane);
+    const float w = ml.y != 0.f ? ex2_approx(ml.x - mu) : 0.f;  // sum 0: nothing of the row in this piece
+    if (ml.y != 0.f) l += w * ml.y;
+    const unsigned use = __ballot_sync(kAll, ml.y != 0.f);      // its O may be unwritten
+    const int top = min(32, P - k0);
+#pragma unroll 8
+    for (int j = slice; j < top; j += wr) {
+      const float wj = __shfl_sync(kAll, w, j);
+      if ((use >> j) & 1) {
+        const float4 a = __ldcg(reinterpret_cast<const float4*>(p.part_o + place(k0 + j) * kHeadDim) + lane);
+        acc.x += wj * a.x; acc.y += wj * a.y; acc.z += wj * a.z; acc.w += wj * a.w;
+      }
+    }
+  }
+#pragma unroll
+  for (int o = 16; o >= 1; o >>= 1) l += __shfl_xor_sync(kAll, l, o);
+  if (wr > 1) {
+    s_acc[warp][lane] = acc;
+    __syncthreads();
+    if (slice != 0 || !in) return;
+    for (int q = 1; q < wr; ++q) {
+      const float4 a = s_acc[warp + q][lane];
+      acc.x += a.x; acc.y += a.y; acc.z += a.z; acc.w += a.w;
+    }
   }
   const bool any = l > 0.f || l != l;
   const float inv = any ? 1.f / l : 0.f;
-  const int t = seq0 + pr / c.group, h = g * c.group + pr % c.group;
-  uint4 o;
-  o.x = pack_bf16x2(acc[0] * inv, acc[1] * inv);
-  o.y = pack_bf16x2(acc[2] * inv, acc[3] * inv);
-  o.z = pack_bf16x2(acc[4] * inv, acc[5] * inv);
-  o.w = pack_bf16x2(acc[6] * inv, acc[7] * inv);
-  *reinterpret_cast<uint4*>(p.out + ((long long)t * c.hq + h) * kHeadDim + cc) = o;
-  if ((threadIdx.x & 15) == 0) {
-    const float v = any ? mu + log2f(l) : -INFINITY;
-    if (p.lse2) p.lse2[(long long)h * c.total_tokens + t] = v;
-    if (p.lse) p.lse[(long long)h * c.total_tokens + t] = v * 0.6931471805599453f;
+  const long long t = (long long)seq0 + tok;
+  const int h = g * G + head;
+  *reinterpret_cast<uint2*>(p.out + (t * c.hq + h) * kHeadDim + lane * 4) =
+      make_uint2(pack_bf16x2(acc.x * inv, acc.y * inv), pack_bf16x2(acc.z * inv, acc.w * inv));
+  if (lane == 0) {
+    const float z = any ? mu + log2f(l) : -INFINITY;
+    if (p.lse2) p.lse2[(long long)h * c.total_tokens + t] = z;
+    if (p.lse) p.lse[(long long)h * c.total_tokens + t] = z * 0.6931471805599453f;
   }
 }
 
@@ -501,21 +541,32 @@ CacheAttnLayout cache_attn_layout(int sms, bool tiled, int64_t hq, int64_t total
   return w;
 }
 
+// Every kernel of a call asks for the same split of the SM's memory (the largest shared part): between
+// kernels that differ in it the SM has to drain first, which costs microseconds.
+cudaError_t launch_cache_join(const CacheAttnParams& p, bool tiled, int ctas, cudaStream_t st) {
+  if (ctas < 2) return cudaSuccess;
+  void (*fn)(const CacheAttnParams) = tiled ? cache_join_kernel<true> : cache_join_kernel<false>;
+  static unsigned long long attr[2][kMaxCachedDevices] = {};
+  const cudaError_t e = set_max_smem(reinterpret_cast<const void*>(fn), 0, attr[tiled], true);
+  if (e != cudaSuccess) return e;
+  return launch_pdl(fn, dim3(ctas - 1, tiled ? 16 : 1), 512, 0, st, p);
+}
+
 cudaError_t launch_cache_attn(const CacheAttnParams& p, bool tiled, int sms, cudaStream_t st) {
   static unsigned long long attr[kMaxCachedDevices] = {}, attr_w[kMaxCachedDevices] = {};
   cudaError_t e;
   if (tiled) {
     if ((e = launch_cache_tiles(p, sms, st)) != cudaSuccess) return e;
   } else {
-    e = set_max_smem(reinterpret_cast<const void*>(cache_rows_kernel), row_smem(kMaxSeqs), attr);
+    e = set_max_smem(reinterpret_cast<const void*>(cache_rows_kernel), row_smem(kMaxSeqs), attr, true);
     if (e != cudaSuccess) return e;
     const int grid = 2 * sms;
     cache_rows_kernel<<<grid, kRowThreads, row_smem(p.c.num_seqs), st>>>(p);
     if ((e = cudaGetLastError()) != cudaSuccess) return e;
-    if ((e = launch_pdl(cache_join_kernel, dim3(grid - 1), 256, 0, st, p)) != cudaSuccess) return e;
+    if ((e = launch_cache_join(p, false, grid, st)) != cudaSuccess) return e;
   }
   if (!(p.decay >= 0.f)) return cudaSuccess;
-  if ((e = set_max_smem(reinterpret_cast<const void*>(cache_weights_kernel), weights_smem(kMaxSeqs), attr_w)) !=
+  if ((e = set_max_smem(reinterpret_cast<const void*>(cache_weights_kernel), weights_smem(kMaxSeqs), attr_w, true)) !=
       cudaSuccess)
     return e;
   cache_weights_kernel<<<8 * sms, kRowThreads, weights_smem(p.c.num_seqs), st>>>(p);

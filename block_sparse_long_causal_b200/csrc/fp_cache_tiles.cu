@@ -672,55 +672,6 @@ __global__ void __launch_bounds__(kThreads, 1) cache_tiles_kernel(const __grid_c
   if (warp == 1) tmem_dealloc(tmem, 512);
 }
 
-// Joins the pieces of the units that several CTAs share. Block (b, y) looks at the unit inside of which
-// the part of CTA b + 1 begins (meta) and works when that CTA is the first such of its unit: the pieces
-// are the last one of CTA b (place 1) and the first one (place 0) of every CTA up to meta[1]. 16 rows a block.
-__global__ void __launch_bounds__(256) cache_tiles_join_kernel(const __grid_constant__ CacheAttnParams p) {
-  pdl_wait();
-  const int b = blockIdx.x + 1;
-  const int32_t* meta = p.meta + (long long)b * kMetaWords;
-  if (meta[0] == 0) return;
-  const CacheInfo& c = p.c;
-  const int last = meta[1], seq0 = meta[2], g = meta[3], tok0 = meta[4], L = meta[5];
-  const int TT = p.tile_tokens, G = c.group;
-  const int row = blockIdx.y * 16 + (threadIdx.x >> 4), cc = (threadIdx.x & 15) * 8;
-  const int r = row & 127, tok = tok0 + (row >> 7) * TT + r / G;
-  if (r >= TT * G || tok >= L) return;
-  auto place = [&](int k) { return (2ll * k + (k == b - 1)) * 256 + row; };
-  float m = -INFINITY;
-  for (int k = b - 1; k <= last; ++k) {
-    const float2 ml = *reinterpret_cast<const float2*>(p.part_ml + 2 * place(k));
-    m = fmaxf(m, ml.x);
-  }
-  const float mu = m == -INFINITY ? 0.f : m;
-  float l = 0.f, acc[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
-  for (int k = b - 1; k <= last; ++k) {
-    const float2 ml = *reinterpret_cast<const float2*>(p.part_ml + 2 * place(k));
-    if (ml.y == 0.f) continue;  // nothing of the row in this piece (its O may be unwritten)
-    const float w = ex2_approx(ml.x - mu);
-    l += w * ml.y;
-    const float4* src = reinterpret_cast<const float4*>(p.part_o + place(k) * kHeadDim + cc);
-    const float4 a = src[0], e = src[1];
-    acc[0] += w * a.x; acc[1] += w * a.y; acc[2] += w * a.z; acc[3] += w * a.w;
-    acc[4] += w * e.x; acc[5] += w * e.y; acc[6] += w * e.z; acc[7] += w * e.w;
-  }
-  const bool any = l > 0.f || l != l;
-  const float inv = any ? 1.f / l : 0.f;
-  const long long t = (long long)seq0 + tok;
-  const int h = g * G + r % G;
-  uint4 o;
-  o.x = pack_bf16x2(acc[0] * inv, acc[1] * inv);
-  o.y = pack_bf16x2(acc[2] * inv, acc[3] * inv);
-  o.z = pack_bf16x2(acc[4] * inv, acc[5] * inv);
-  o.w = pack_bf16x2(acc[6] * inv, acc[7] * inv);
-  *reinterpret_cast<uint4*>(p.out + (t * c.hq + h) * kHeadDim + cc) = o;
-  if ((threadIdx.x & 15) == 0) {
-    const float z = any ? mu + log2f(l) : -INFINITY;
-    if (p.lse2) p.lse2[(long long)h * c.total_tokens + t] = z;
-    if (p.lse) p.lse[(long long)h * c.total_tokens + t] = z * 0.6931471805599453f;
-  }
-}
-
 }  // namespace tiles
 
 cudaError_t launch_cache_tiles(const CacheAttnParams& p, int sms, cudaStream_t st) {
@@ -729,7 +680,7 @@ cudaError_t launch_cache_tiles(const CacheAttnParams& p, int sms, cudaStream_t s
   if (e != cudaSuccess) return e;
   tiles::cache_tiles_kernel<<<sms, tiles::kThreads, tiles::smem_bytes(p.c.num_seqs), st>>>(p);
   if ((e = cudaGetLastError()) != cudaSuccess || sms < 2) return e;
-  return launch_pdl(tiles::cache_tiles_join_kernel, dim3(sms - 1, 16), 256, 0, st, p);
+  return launch_cache_join(p, true, sms, st);
 }
 
 }  // namespace fp

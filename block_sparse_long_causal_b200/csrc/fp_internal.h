@@ -192,7 +192,9 @@ unsigned long long context_id();
 // attribute belongs to the current device's context, so `done[dev]` remembers the context id it was
 // set in (ordinals >= kMaxCachedDevices set it at every call).
 constexpr int kMaxCachedDevices = 64;
-cudaError_t set_max_smem(const void* func, int bytes, unsigned long long (&done)[kMaxCachedDevices]);
+// carveout: also ask for the largest shared part of the SM's memory at every launch.
+cudaError_t set_max_smem(const void* func, int bytes, unsigned long long (&done)[kMaxCachedDevices],
+                         bool carveout = false);
 
 cudaError_t launch_pool(const PoolParams& p, int grid, cudaStream_t st);
 cudaError_t launch_search(const SearchParams& p, cudaStream_t st);
@@ -202,8 +204,8 @@ cudaError_t launch_topp(const SearchParams& p, float gamma, float* scores, cudaS
 cudaError_t launch_attn(const AttnParams& p, int grid, cudaStream_t st);
 // Key/value cache (fp_cache.cu, fp_cache_attn.cu).
 cudaError_t launch_append(const AppendParams& p, cudaStream_t st);
-cudaError_t launch_select(const SelectParams& p, cudaStream_t st);
-cudaError_t launch_compact(const CompactParams& p, cudaStream_t st);
+cudaError_t launch_select(const SelectParams& p, int sms, cudaStream_t st);
+cudaError_t launch_compact(const CompactParams& p, int sms, cudaStream_t st);
 constexpr int kMetaWords = 8;               // ints per CTA that describe the unit its share begins inside of
 // Schedule of the attention call: 16-row tiles (fp_cache_attn.cu) or 128-row tiles (fp_cache_tiles.cu).
 bool cache_attn_tiled(int32_t max_new, int32_t group);
@@ -213,6 +215,8 @@ struct CacheAttnLayout {                    // byte offsets of its workspace
 CacheAttnLayout cache_attn_layout(int sms, bool tiled, int64_t hq, int64_t total_tokens);
 cudaError_t launch_cache_attn(const CacheAttnParams& p, bool tiled, int sms, cudaStream_t st);
 cudaError_t launch_cache_tiles(const CacheAttnParams& p, int sms, cudaStream_t st);
+// Joins the pieces of the units that several of `ctas` CTAs shared.
+cudaError_t launch_cache_join(const CacheAttnParams& p, bool tiled, int ctas, cudaStream_t st);
 cudaError_t launch_exp2_selftest(const float* x, float* y_poly, float* y_mufu, long long n, cudaStream_t st);
 
 }  // namespace fp
