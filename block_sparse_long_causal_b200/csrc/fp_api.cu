@@ -788,7 +788,7 @@ fp_status fp_cache_attn_workspace(const fp_problem* p, const fp_kv_cache* c, int
   if (st != FP_OK) return st;
   if (!bytes) return fail(FP_ERR_INVALID_ARG, "bytes must be non-NULL");
   const bool tiled = fp::cache_attn_tiled(c->max_new, p->num_q_heads / p->num_kv_heads);
-  *bytes = fp::cache_attn_layout(sm_count(), tiled, p->num_q_heads, p->total_tokens).total;
+  *bytes = fp::cache_attn_layout(sm_count(), tiled, cache_info(p, c), c->weights != nullptr).total;
   return FP_OK;
 }
 
@@ -809,7 +809,8 @@ fp_status fp_cache_attn(const fp_problem* p, const fp_kv_cache* c, const void* q
   const int sms = sm_count();
   const int group = p->num_q_heads / p->num_kv_heads;
   const bool tiled = fp::cache_attn_tiled(c->max_new, group);
-  const fp::CacheAttnLayout w = fp::cache_attn_layout(sms, tiled, p->num_q_heads, p->total_tokens);
+  a.c = cache_info(p, c);
+  const fp::CacheAttnLayout w = fp::cache_attn_layout(sms, tiled, a.c, c->weights != nullptr);
   if (!workspace) return fail(FP_ERR_INVALID_ARG, "workspace must be non-NULL");
   if ((reinterpret_cast<uintptr_t>(workspace) & 255u) != 0)
     return fail(FP_ERR_INVALID_ARG, "workspace must be 256-byte aligned");
@@ -818,12 +819,14 @@ fp_status fp_cache_attn(const fp_problem* p, const fp_kv_cache* c, const void* q
                 (long long)workspace_bytes, (long long)w.total);
   char* base = static_cast<char*>(workspace);
   const float scale = softmax_scale > 0.f ? softmax_scale : 1.0f / std::sqrt((float)p->head_dim);
-  a.c = cache_info(p, c);
   a.q = static_cast<const uint16_t*>(q);
   a.scale_log2 = scale * 1.4426950408889634f;
   a.out = static_cast<uint16_t*>(out);
   a.lse = lse;
   a.lse2 = decay >= 0.f ? reinterpret_cast<float*>(base + w.lse2) : nullptr;
+  a.scores = decay >= 0.f && !tiled ? reinterpret_cast<float*>(base + w.scores) : nullptr;
+  a.score_rows = w.score_rows;
+  a.score_tiles = w.score_tiles;
   a.part_o = reinterpret_cast<float*>(base + w.part_o);
   a.part_ml = reinterpret_cast<float*>(base + w.part_ml);
   a.meta = reinterpret_cast<int32_t*>(base + w.meta);

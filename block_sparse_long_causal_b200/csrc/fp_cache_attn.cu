@@ -1,15 +1,20 @@
 // fp_cache_attn.cu -- attention of new tokens over a paged key/value cache, with the attention weight
-// that every cached slot collects.
+// that every cached slot collects: the schedule for few rows (single tokens, short drafts), the join of
+// split units for both schedules, and the entry that picks one.
 //
 //   o_th = sum_u p_thu v_u,  p_thu = exp(scale q_th . k_u - lse_th),  u <= lens[s] + t
 //   w_ug = decay * w_ug + sum_{t, h in group g} p_thu
 //
-// A unit is 16 packed rows (token-major: row r is token r / G, q-head r % G of the group) of one
-// (sequence, kv-head); its keys are cut into tiles of 64. All tiles of all units form one line that
-// the CTAs share out evenly, whatever the lengths: a CTA's range may begin or end inside a unit, and the
-// pieces of such a unit are joined from the workspace by a second kernel. Every warp takes 16 keys of a
-// tile with its own ring of cp.async stages, its own running maximum, row sum and accumulator, so warps
-// never wait for one another inside a unit.
+// Bound by reading K and V once: a unit is one (sequence, kv-head) with all its rows (row r: token r / G,
+// q-head r % G of the group), 8 NT of them at most, and its keys are cut into tiles of 64. All tiles of all
+// units form one line that the CTAs share out evenly, whatever the lengths: a CTA's share may begin or end
+// inside a unit, and the pieces of such a unit are joined from the workspace by a second kernel. Every
+// warp takes 16 keys of a tile with its own ring of cp.async stages, its own running maximum, row sum and
+// accumulator, so warps never wait for one another inside a unit.
+//
+// The products are formed transposed, keys and columns along the 16-row side of the matrix instruction and the
+// unit's rows along its 8-column side (S^T = K Q^T, O^T = V^T P^T): with the four rows of a token over
+// a group of four heads that halves the instructions and the accumulator registers.
 #include <cmath>
 
 #include "fp_cache.cuh"
@@ -19,17 +24,15 @@ namespace fp {
 namespace {
 
 constexpr unsigned kAll = 0xffffffffu;
-constexpr int kRowsT = 16;                  // packed rows of a unit
+constexpr int kRowsMax = 16;                // rows of a unit
 constexpr int kKeysW = 16;                  // keys of a tile per warp
 constexpr int kWarps = 4, kRowThreads = 32 * kWarps;
 constexpr int kKeysT = kKeysW * kWarps;     // keys of a tile
 constexpr int kStages = 3;
 constexpr int kStageBytes = 2 * kKeysW * kHeadDim * 2;  // K then V of one warp's 16 keys
-constexpr int kJoinCols = 32;               // output columns joined at a time
-constexpr int kOffJoin = kWarps * kStages * kStageBytes;
-constexpr int kOffMl = kOffJoin + kWarps * kRowsT * kJoinCols * 4;  // float m[warp][16], l[warp][16]
-constexpr int kOffTabR = kOffMl + 2 * kWarps * kRowsT * 4 + 64;
-constexpr int row_smem(int S) { return kOffTabR + 8 * (S + 1); }
+constexpr int kOffMl = kWarps * kStages * kStageBytes;  // float m[warp][16], l[warp][16]
+constexpr int kRowSmem = kOffMl + 2 * kWarps * kRowsMax * 4;
+static_assert(kRowsMax * kHeadDim * 4 <= kStageBytes, "a consumed stage holds the warp's result when a unit is joined");
 
 __device__ __forceinline__ void cp_async16(uint32_t dst, const void* src, bool valid) {
   asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(valid ? 16 : 0) : "memory");
@@ -38,13 +41,18 @@ __device__ __forceinline__ void cp_async_commit() { asm volatile("cp.async.commi
 template <int N>
 __device__ __forceinline__ void cp_async_wait() { asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory"); }
 
-__device__ __forceinline__ void ldsm4(uint32_t a, uint32_t& r0, uint32_t& r1, uint32_t& r2, uint32_t& r3) {
+__device__ __forceinline__ void ldsm4(uint32_t a, uint32_t (&r)[4]) {
   asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0, %1, %2, %3}, [%4];"
-               : "=r"(r0), "=r"(r1), "=r"(r2), "=r"(r3) : "r"(a) : "memory");
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]) : "r"(a) : "memory");
 }
-__device__ __forceinline__ void ldsm4t(uint32_t a, uint32_t& r0, uint32_t& r1, uint32_t& r2, uint32_t& r3) {
+__device__ __forceinline__ void ldsm4t(uint32_t a, uint32_t (&r)[4]) {
   asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0, %1, %2, %3}, [%4];"
-               : "=r"(r0), "=r"(r1), "=r"(r2), "=r"(r3) : "r"(a) : "memory");
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]) : "r"(a) : "memory");
+}
+__device__ __forceinline__ uint32_t movmatrix(uint32_t x) {  // transposes an 8x8 matrix of 16-bit elements
+  uint32_t y;
+  asm("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(x));
+  return y;
 }
 __device__ __forceinline__ void mma16816(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
   asm volatile(
@@ -53,159 +61,209 @@ __device__ __forceinline__ void mma16816(float (&d)[4], const uint32_t (&a)[4], 
       : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
 
-// A unit and the tile of it that a cursor stands on.
+// A place on the line.
 struct Cursor {
-  int s, g, rt;          // sequence, kv-head, row tile
+  int s, g, kt;          // sequence, kv-head, tile
   int seq0, L, len, n;   // first new token, new tokens, slots before them, keys
-  int rts, kts;          // row tiles, key tiles of the sequence's units
-  int kt;                // tile
-  long long unit0;       // line position of the unit's first tile
+  int kts;               // tiles of the sequence's units
 };
+__device__ __forceinline__ int unit_tiles(int L, int n) { return L > 0 ? (n + kKeysT - 1) / kKeysT : 0; }
 __device__ __forceinline__ void load_seq(Cursor& u, const CacheInfo& c, int s) {
   u.s = s;
   u.seq0 = __ldg(c.cu_seqlens + s);
   u.L = __ldg(c.cu_seqlens + s + 1) - u.seq0;
   u.len = c.lens[s];
   u.n = u.len + u.L;
-  u.rts = (u.L * c.group + kRowsT - 1) / kRowsT;
-  u.kts = (u.n + kKeysT - 1) / kKeysT;
+  u.kts = unit_tiles(u.L, u.n);
 }
-__device__ __forceinline__ Cursor cursor_at(const CacheInfo& c, const long long* tab, long long x) {
-  Cursor u;
-  load_seq(u, c, find_seq64(tab, c.num_seqs, x));
-  const long long local = x - tab[u.s];
-  const long long unit = local / u.kts;
-  u.kt = (int)(local - unit * u.kts);
-  u.g = (int)(unit / u.rts);
-  u.rt = (int)(unit - (long long)u.g * u.rts);
-  u.unit0 = x - u.kt;
-  return u;
-}
-// Step to the next tile of the line; more: there is one.
-__device__ __forceinline__ void cursor_next(Cursor& u, const CacheInfo& c, const long long* tab, bool more) {
+// Step to the next tile of the line. more: there is one.
+__device__ __forceinline__ void cursor_next(Cursor& u, const CacheInfo& c, bool more) {
   if (++u.kt < u.kts || !more) return;
   u.kt = 0;
-  u.unit0 += u.kts;
-  if (++u.rt < u.rts) return;
-  u.rt = 0;
   if (++u.g < c.hkv) return;
   u.g = 0;
-  load_seq(u, c, find_seq64(tab, c.num_seqs, u.unit0));
+  int s = u.s;
+  do load_seq(u, c, ++s);
+  while (u.kts == 0 && s + 1 < c.num_seqs);
+}
+// Share of CTA i: [share(i), share(i + 1)), the first `rem` ones one tile longer.
+struct Shares {
+  long long q;
+  int rem, ctas;
+  __device__ __forceinline__ long long at(int i) const { return i * q + min(i, rem); }
+};
+// Every warp by itself: lane i sums the tiles of a contiguous run of sequences, a scan gives the total, and
+// the lane whose run holds the start of the CTA's share walks it. No shared memory and no barrier: this
+// chain is most of what a short call waits for. The device arrays are checked against the host's
+// description here, before any other access depends on them.
+__device__ __forceinline__ bool find_share(const CacheInfo& c, Shares& sh, Cursor& u, long long max_tiles, int32_t* dev_status) {
+  const int lane = threadIdx.x & 31, S = c.num_seqs, per = (S + 31) / 32;
+  const int a = min(S, lane * per), b = min(S, a + per);
+  long long sum = 0;
+  bool bad = lane == 0 && (__ldg(c.cu_seqlens) != 0 || __ldg(c.cu_seqlens + S) != c.total_tokens);
+#pragma unroll 4
+  for (int s = a; s < b; ++s) {
+    const int lo = __ldg(c.cu_seqlens + s), hi = __ldg(c.cu_seqlens + s + 1), len = c.lens[s];
+    const bool ok = lo >= 0 && hi >= lo && hi <= c.total_tokens && hi - lo <= c.max_new && len >= 0 &&
+                    len <= c.max_len - (hi - lo);
+    bad |= !ok;
+    if (ok) sum += (long long)c.hkv * unit_tiles(hi - lo, len + hi - lo);
+  }
+  if (__any_sync(kAll, bad)) {
+    if (threadIdx.x == 0 && blockIdx.x == 0) dev_flag(dev_status, kDevBadProblem);
+    return false;
+  }
+  const long long incl = warp_incl_scan(sum), total = __shfl_sync(kAll, incl, 31);
+  if (total > max_tiles) {  // more tiles than the workspace has scores for: sequences share pages
+    if (threadIdx.x == 0 && blockIdx.x == 0) dev_flag(dev_status, kDevBadProblem);
+    return false;
+  }
+  sh.ctas = (int)min((long long)gridDim.x, total);
+  const int me = blockIdx.x;
+  if (me >= sh.ctas) return false;
+  if (total < 0x7fffffffll) {
+    sh.q = (unsigned)total / (unsigned)sh.ctas;
+    sh.rem = (int)((unsigned)total % (unsigned)sh.ctas);
+  } else {
+    sh.q = total / sh.ctas;
+    sh.rem = (int)(total % sh.ctas);
+  }
+  const long long x0 = sh.at(me);
+  const bool mine = incl - sum <= x0 && x0 < incl;
+  if (mine) {
+    long long left = x0 - (incl - sum);
+    for (int s = a;; ++s) {
+      load_seq(u, c, s);
+      const long long tiles = (long long)c.hkv * u.kts;
+      if (left < tiles) break;
+      left -= tiles;
+    }
+    u.g = left < 0x7fffffffll ? (int)((unsigned)left / (unsigned)u.kts) : (int)(left / u.kts);
+    u.kt = (int)(left - (long long)u.g * u.kts);
+  }
+  const int src = __ffs(__ballot_sync(kAll, mine)) - 1;
+  u.s = __shfl_sync(kAll, u.s, src);
+  u.g = __shfl_sync(kAll, u.g, src);
+  u.kt = __shfl_sync(kAll, u.kt, src);
+  u.seq0 = __shfl_sync(kAll, u.seq0, src);
+  u.L = __shfl_sync(kAll, u.L, src);
+  u.len = __shfl_sync(kAll, u.len, src);
+  u.n = u.len + u.L;
+  u.kts = unit_tiles(u.L, u.n);
+  return true;
 }
 
+template <int NT>
 __global__ void __launch_bounds__(kRowThreads, 2) cache_rows_kernel(const __grid_constant__ CacheAttnParams p) {
   extern __shared__ __align__(128) unsigned char smem[];
+  pdl_wait();
   const CacheInfo& c = p.c;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  long long* tab = reinterpret_cast<long long*>(smem + kOffTabR);
-  long long* s_scan = reinterpret_cast<long long*>(smem + kOffMl);  // before the ring is used
-  int* s_bad = reinterpret_cast<int*>(smem + kOffMl + 64);
-  const bool ok = cache_table<kRowThreads>(c, tab, s_scan, s_bad, p.dev_status, [&](int, int L, int n) -> long long {
-    return (long long)c.hkv * ((L * c.group + kRowsT - 1) / kRowsT) * ((n + kKeysT - 1) / kKeysT);
-  });
-  pdl_trigger();
-  const long long total = ok ? tab[c.num_seqs] : 0;
-  const int ctas = (int)min((long long)gridDim.x, total);  // CTAs with work: every one has a tile
-  const int me = blockIdx.x;
-  const long long x0 = me < ctas ? total * me / ctas : 0, x1 = me < ctas ? total * (me + 1) / ctas : 0;
+  Shares sh;
+  Cursor cur;
   int32_t* meta = p.meta + (long long)blockIdx.x * kMetaWords;
-  if (x0 >= x1) {
+  const bool work = find_share(c, sh, cur, p.scores ? p.score_tiles : 0x7fffffffffffffffll, p.dev_status);
+  pdl_trigger();
+  if (!work) {
     if (tid == 0) meta[0] = 0;
     return;
   }
-  const uint32_t ring = smem_u32(smem) + warp * kStages * kStageBytes;
-  Cursor ld = cursor_at(c, tab, x0);
-  Cursor cur = ld;
+  const int me = blockIdx.x;
+  const long long x0 = sh.at(me), x1 = sh.at(me + 1);
+  Cursor ld = cur;
   if (tid == 0) {
-    // a range that begins inside a unit: its first CTA but one joins the unit's pieces
-    const bool inside = cur.kt > 0;
-    const long long prev0 = me > 0 ? total * (me - 1) / ctas : 0;
-    meta[0] = inside && prev0 <= cur.unit0;
-    if (inside) {
-      // the last CTA whose range begins inside the unit
-      const long long end = cur.unit0 + cur.kts;
-      int last = me;
-      while (last + 1 < ctas && total * (last + 1) / ctas < end) ++last;
+    const long long unit0 = x0 - cur.kt, end = unit0 + cur.kts;  // the unit that the share begins in
+    meta[0] = cur.kt > 0 && sh.at(me - 1) <= unit0;  // its first CTA but one: its pieces are joined in its name
+    if (cur.kt > 0) {
+      int last = me;  // the last CTA whose share begins inside the unit
+      while (last + 1 < sh.ctas && sh.at(last + 1) < end) ++last;
       meta[1] = last;
       meta[2] = cur.seq0;
       meta[3] = cur.g;
-      meta[4] = cur.rt * kRowsT;
+      meta[4] = 0;
       meta[5] = cur.L * c.group;
     }
   }
-
-  // ---- loads: tile x of the line into stage (x - x0) % kStages
+  const uint32_t ring = smem_u32(smem) + warp * kStages * kStageBytes;
+  // ---- loads: tile x of the line into stage (x - x0) % kStages. The page of a tile is looked up one tile ahead.
+  auto row_of = [&](const Cursor& u) -> long long {
+    const int key0 = u.kt * kKeysT + warp * kKeysW;  // pages hold whole groups of 16 slots
+    return key0 < u.n ? slot_row(c, u.s, key0) : -1;
+  };
+  long long row0 = row_of(ld);
+  int put = 0;
   auto load = [&](long long x) {
     if (x < x1) {
-      const uint32_t st = ring + (uint32_t)((x - x0) % kStages) * kStageBytes;
-      const int key0 = ld.kt * kKeysT + warp * kKeysW;  // pages hold whole groups of 16 slots
-      const long long row0 = key0 < ld.n ? slot_row(c, ld.s, key0) : -1;
+      const uint32_t st = ring + (uint32_t)put * kStageBytes;
+      put = put + 1 == kStages ? 0 : put + 1;
+      const int key0 = ld.kt * kKeysT + warp * kKeysW;
       if (key0 < ld.n && row0 < 0 && lane == 0) dev_flag(p.dev_status, kDevBadProblem);
       // a bad page and the slots past the sequence's end read as zeros
       const int live = row0 < 0 ? 0 : min(kKeysW, ld.n - key0);
-      const long long base = ((row0 < 0 ? 0 : row0) * c.hkv + ld.g) * kHeadDim;
+      const long long base = ((row0 < 0 ? 0 : row0) * c.hkv + ld.g) * kHeadDim + (lane & 15) * 8;
 #pragma unroll
       for (int i = 0; i < 8; ++i) {
-        const int r = 2 * i + (lane >> 4), ch = lane & 15;
-        const long long off = r < live ? base + (long long)r * c.hkv * kHeadDim + ch * 8 : 0;
-        const uint32_t d = st + r * 256 + ((ch ^ (r & 7)) << 4);
+        const int r = 2 * i + (lane >> 4);
+        const long long off = r < live ? base + (long long)r * c.hkv * kHeadDim : 0;
+        const uint32_t d = st + r * 256 + (((lane & 15) ^ (r & 7)) << 4);
         cp_async16(d, c.k + off, r < live);
         cp_async16(d + kKeysW * 256, c.v + off, r < live);
       }
-      cursor_next(ld, c, tab, x + 1 < x1);
+      cursor_next(ld, c, x + 1 < x1);
+      if (x + 1 < x1) row0 = row_of(ld);
     }
     cp_async_commit();
   };
 #pragma unroll
   for (int i = 0; i < kStages - 1; ++i) load(x0 + i);
 
-  uint32_t qf[8][4];
-  float o[16][4], l[2], m[2];
-  const int qr = lane >> 2, qc = (lane & 3) * 2;
-  float* s_join = reinterpret_cast<float*>(smem + kOffJoin);
+  uint32_t qf[NT][8][2];
+  float o[8][NT][4], l[NT][2], m[NT][2];
+  int last[NT][2];                                // the last key that a row sees
+  const int kr = lane >> 2, rc = (lane & 3) * 2;  // this thread's keys kr, kr + 8 and rows rc, rc + 1 (+ 8 t)
   float* s_m = reinterpret_cast<float*>(smem + kOffMl);
-  float* s_l = s_m + kWarps * kRowsT;
+  float* s_l = s_m + kWarps * kRowsMax;
   bool fresh = true;
-  int first_kt = 0;
+  int first_kt = 0, get = 0;
   for (long long x = x0; x < x1; ++x) {
     if (fresh) {
       fresh = false;
       first_kt = cur.kt;
 #pragma unroll
-      for (int i = 0; i < 16; ++i) o[i][0] = o[i][1] = o[i][2] = o[i][3] = 0.f;
-      l[0] = l[1] = 0.f;
-      m[0] = m[1] = -INFINITY;
-      const uint16_t* q0[2];
-      bool in[2];
+      for (int t = 0; t < NT; ++t) {
 #pragma unroll
-      for (int i = 0; i < 2; ++i) {
-        const int r = cur.rt * kRowsT + qr + 8 * i;
-        in[i] = r < cur.L * c.group;
-        q0[i] = p.q + (long long)(cur.seq0 + (in[i] ? r / c.group : 0)) * p.q_stride +
-                (cur.g * c.group + (in[i] ? r % c.group : 0)) * kHeadDim + qc;
-      }
+        for (int i = 0; i < 8; ++i) o[i][t][0] = o[i][t][1] = o[i][t][2] = o[i][t][3] = 0.f;
+        l[t][0] = l[t][1] = 0.f;
+        m[t][0] = m[t][1] = -INFINITY;
+        last[t][0] = cur.len + (8 * t + rc) / c.group;
+        last[t][1] = cur.len + (8 * t + rc + 1) / c.group;
+        const int r = 8 * t + kr;
+        const bool in = r < cur.L * c.group;
+        const uint16_t* q0 = p.q + (long long)(cur.seq0 + (in ? r / c.group : 0)) * p.q_stride +
+                             (cur.g * c.group + (in ? r % c.group : 0)) * kHeadDim + rc;
 #pragma unroll
-      for (int kk = 0; kk < 8; ++kk)
-#pragma unroll
-        for (int i = 0; i < 2; ++i) {
-          qf[kk][i] = in[i] ? __ldg(reinterpret_cast<const uint32_t*>(q0[i] + kk * 16)) : 0u;
-          qf[kk][2 + i] = in[i] ? __ldg(reinterpret_cast<const uint32_t*>(q0[i] + kk * 16 + 8)) : 0u;
+        for (int kk = 0; kk < 8; ++kk) {
+          qf[t][kk][0] = in ? __ldg(reinterpret_cast<const uint32_t*>(q0 + kk * 16)) : 0u;
+          qf[t][kk][1] = in ? __ldg(reinterpret_cast<const uint32_t*>(q0 + kk * 16 + 8)) : 0u;
         }
+      }
     }
     load(x + kStages - 1);
     cp_async_wait<kStages - 1>();
     __syncwarp();
-    const uint32_t sk = ring + (uint32_t)((x - x0) % kStages) * kStageBytes, sv = sk + kKeysW * 256;
-    // S = Q K^T: 16 rows x 16 keys
-    float sc[2][4] = {{0.f, 0.f, 0.f, 0.f}, {0.f, 0.f, 0.f, 0.f}};
+    const uint32_t sk = ring + (uint32_t)get * kStageBytes, sv = sk + kKeysW * 256;
+    // S^T = K Q^T: 16 keys x 8 NT rows
+    float sc[NT][4];
+#pragma unroll
+    for (int t = 0; t < NT; ++t) sc[t][0] = sc[t][1] = sc[t][2] = sc[t][3] = 0.f;
     {
-      const int r = (lane & 7) + ((lane >> 4) << 3), h = (lane >> 3) & 1;
+      const int r = (lane & 7) + (((lane >> 3) & 1) << 3), h = lane >> 4;
 #pragma unroll
       for (int kk = 0; kk < 8; ++kk) {
-        uint32_t b0, b1, b2, b3;
-        ldsm4(sk + r * 256 + (((2 * kk + h) ^ (r & 7)) << 4), b0, b1, b2, b3);
-        mma16816(sc[0], qf[kk], b0, b1);
-        mma16816(sc[1], qf[kk], b2, b3);
+        uint32_t a[4];
+        ldsm4(sk + r * 256 + (((2 * kk + h) ^ (r & 7)) << 4), a);
+#pragma unroll
+        for (int t = 0; t < NT; ++t) mma16816(sc[t], a, qf[t][kk][0], qf[t][kk][1]);
       }
     }
     const int key0 = cur.kt * kKeysT + warp * kKeysW;
@@ -213,134 +271,179 @@ __global__ void __launch_bounds__(kRowThreads, 2) cache_rows_kernel(const __grid
     const bool edge = key0 + kKeysW - 1 > cur.len;
     bool grow = false;
 #pragma unroll
-    for (int i = 0; i < 2; ++i) {
-      const int last = edge ? min(cur.n - 1, cur.len + (cur.rt * kRowsT + qr + 8 * i) / c.group) : 0x7fffffff;
+    for (int t = 0; t < NT; ++t)
 #pragma unroll
       for (int e = 0; e < 4; ++e) {
-        float& v = sc[e >> 1][2 * i + (e & 1)];
-        const int key = key0 + (e >> 1) * 8 + qc + (e & 1);
-        v = key <= last ? v * p.scale_log2 : -INFINITY;
-        grow |= v > m[i] + 8.f;
+        const int key = key0 + kr + (e >> 1) * 8;
+        const bool seen = !edge || (key <= last[t][e & 1] && key < cur.n);
+        sc[t][e] = seen ? sc[t][e] * p.scale_log2 : -INFINITY;
+        grow |= sc[t][e] > m[t][e & 1] + 8.f;
       }
+    if (p.scores) {  // for the weights pass: 64 keys x score_rows of a tile
+      float* dst = p.scores + (x * kKeysT + warp * kKeysW + kr) * p.score_rows;
+#pragma unroll
+      for (int t = 0; t < NT; ++t)
+        if (8 * t + rc < p.score_rows) {
+          *reinterpret_cast<float2*>(dst + 8 * t + rc) = make_float2(sc[t][0], sc[t][1]);
+          *reinterpret_cast<float2*>(dst + 8 * p.score_rows + 8 * t + rc) = make_float2(sc[t][2], sc[t][3]);
+        }
     }
     // the reference maximum follows only when a score passes it by 2^8 (any reference gives the same
     // quotient; 8 keeps every term finite and the sums exact enough in 32 bits)
     if (__any_sync(kAll, grow)) {
 #pragma unroll
-      for (int i = 0; i < 2; ++i) {
-        float mx = fmaxf(fmaxf(sc[0][2 * i], sc[0][2 * i + 1]), fmaxf(sc[1][2 * i], sc[1][2 * i + 1]));
-        mx = fmaxf(mx, __shfl_xor_sync(kAll, mx, 1));
-        mx = fmaxf(mx, __shfl_xor_sync(kAll, mx, 2));
-        const float mn = fmaxf(m[i], mx);
-        const float a = mn == -INFINITY ? 1.f : ex2_approx(m[i] - mn);
-        m[i] = mn;
-        l[i] *= a;
+      for (int t = 0; t < NT; ++t)
 #pragma unroll
-        for (int j = 0; j < 16; ++j) {
-          o[j][2 * i] *= a;
-          o[j][2 * i + 1] *= a;
+        for (int i = 0; i < 2; ++i) {
+          float mx = fmaxf(sc[t][i], sc[t][2 + i]);
+          mx = fmaxf(mx, __shfl_xor_sync(kAll, mx, 4));
+          mx = fmaxf(mx, __shfl_xor_sync(kAll, mx, 8));
+          mx = fmaxf(mx, __shfl_xor_sync(kAll, mx, 16));
+          const float mn = fmaxf(m[t][i], mx);
+          const float a = mn == -INFINITY ? 1.f : ex2_approx(m[t][i] - mn);
+          m[t][i] = mn;
+          l[t][i] *= a;
+#pragma unroll
+          for (int j = 0; j < 8; ++j) {
+            o[j][t][i] *= a;
+            o[j][t][2 + i] *= a;
+          }
         }
-      }
     }
-    uint32_t pf[4];
+    uint32_t pf[NT][2];
 #pragma unroll
-    for (int i = 0; i < 2; ++i) {
-      const float mu = m[i] == -INFINITY ? 0.f : m[i];
-#pragma unroll
-      for (int j = 0; j < 2; ++j) {
-        const float e0 = ex2_approx(sc[j][2 * i] - mu), e1 = ex2_approx(sc[j][2 * i + 1] - mu);
-        l[i] += e0 + e1;
-        pf[2 * j + i] = pack_bf16x2(e0, e1);  // the tensor cores take bf16: half a step is 2^-9 of each term
-      }
+    for (int t = 0; t < NT; ++t) {
+      const float mu0 = m[t][0] == -INFINITY ? 0.f : m[t][0], mu1 = m[t][1] == -INFINITY ? 0.f : m[t][1];
+      const float e0 = ex2_approx(sc[t][0] - mu0), e1 = ex2_approx(sc[t][1] - mu1);
+      const float e2 = ex2_approx(sc[t][2] - mu0), e3 = ex2_approx(sc[t][3] - mu1);
+      l[t][0] += e0 + e2;
+      l[t][1] += e1 + e3;
+      // the tensor cores take bf16 (half a step is 2^-9 of each term); [key][row] becomes [row][key]
+      pf[t][0] = movmatrix(pack_bf16x2(e0, e1));
+      pf[t][1] = movmatrix(pack_bf16x2(e2, e3));
     }
-    {
-      const int r = (lane & 7) + (((lane >> 3) & 1) << 3), h = lane >> 4;
+    {  // O^T += V^T P^T: 16 columns at a time
+      const int r = (lane & 7) + ((lane >> 4) << 3), h = (lane >> 3) & 1;
 #pragma unroll
       for (int j = 0; j < 8; ++j) {
-        uint32_t b0, b1, b2, b3;
-        ldsm4t(sv + r * 256 + (((2 * j + h) ^ (r & 7)) << 4), b0, b1, b2, b3);
-        mma16816(o[2 * j], pf, b0, b1);
-        mma16816(o[2 * j + 1], pf, b2, b3);
+        uint32_t a[4];
+        ldsm4t(sv + r * 256 + (((2 * j + h) ^ (r & 7)) << 4), a);
+#pragma unroll
+        for (int t = 0; t < NT; ++t) mma16816(o[j][t], a, pf[t][0], pf[t][1]);
       }
     }
     __syncwarp();  // every lane has read the stage before it is loaded again
     const bool ends = cur.kt + 1 == cur.kts;
-    if (!ends && x + 1 < x1) {
-      cursor_next(cur, c, tab, true);
-      continue;
-    }
-    // ---- the unit's piece is complete: join the warps
+    if (ends || x + 1 == x1) {
+      // ---- the unit's piece is complete: join the warps through the stages that they have just consumed
 #pragma unroll
-    for (int i = 0; i < 2; ++i) {
-      l[i] += __shfl_xor_sync(kAll, l[i], 1);
-      l[i] += __shfl_xor_sync(kAll, l[i], 2);
-      if ((lane & 3) == 0) {
-        s_m[warp * kRowsT + qr + 8 * i] = m[i];
-        s_l[warp * kRowsT + qr + 8 * i] = l[i];
-      }
-    }
-    __syncthreads();
-    const bool whole = ends && first_kt == 0;
-    const long long slot = 2ll * blockIdx.x + (first_kt == 0 ? 1 : 0);  // a piece from a unit's start: slot 1
-    float w[2];
+      for (int t = 0; t < NT; ++t)
 #pragma unroll
-    for (int i = 0; i < 2; ++i) {
-      const int r = qr + 8 * i;
-      float mt = s_m[r];
-      for (int k = 1; k < kWarps; ++k) mt = fmaxf(mt, s_m[k * kRowsT + r]);
-      const float mu = mt == -INFINITY ? 0.f : mt;
-      float lt = 0.f;
-      for (int k = 0; k < kWarps; ++k) lt += s_l[k * kRowsT + r] * ex2_approx(s_m[k * kRowsT + r] - mu);
-      w[i] = ex2_approx(m[i] - mu);
-      if (whole) w[i] *= lt > 0.f || lt != lt ? 1.f / lt : 0.f;
-      if (warp == 0 && (lane & 3) == 0) {
-        if (!whole) {
-          *reinterpret_cast<float2*>(p.part_ml + 2 * (slot * kRowsT + r)) = make_float2(mt, lt);
-        } else {
-          const int pr = cur.rt * kRowsT + r;
-          if (pr < cur.L * c.group) {
-            const long long at =
-                (long long)(cur.g * c.group + pr % c.group) * c.total_tokens + cur.seq0 + pr / c.group;
-            const float v = lt > 0.f || lt != lt ? mu + log2f(lt) : -INFINITY;
-            if (p.lse2) p.lse2[at] = v;
-            if (p.lse) p.lse[at] = v * 0.6931471805599453f;
+        for (int i = 0; i < 2; ++i) {
+          l[t][i] += __shfl_xor_sync(kAll, l[t][i], 4);
+          l[t][i] += __shfl_xor_sync(kAll, l[t][i], 8);
+          l[t][i] += __shfl_xor_sync(kAll, l[t][i], 16);
+          if (kr == 0) {
+            s_m[warp * kRowsMax + 8 * t + rc + i] = m[t][i];
+            s_l[warp * kRowsMax + 8 * t + rc + i] = l[t][i];
           }
         }
-      }
-    }
-    for (int cb = 0; cb < kHeadDim / kJoinCols; ++cb) {
+      __syncthreads();
+      float* s_o = reinterpret_cast<float*>(smem + (sk - smem_u32(smem)));  // [row][128], columns swizzled
 #pragma unroll
-      for (int j = 0; j < 16; ++j)
-        if (j / 4 == cb) {
+      for (int t = 0; t < NT; ++t)
 #pragma unroll
-          for (int i = 0; i < 2; ++i)
-            *reinterpret_cast<float2*>(s_join + (warp * kRowsT + qr + 8 * i) * kJoinCols + (j & 3) * 8 + qc) =
-                make_float2(o[j][2 * i] * w[i], o[j][2 * i + 1] * w[i]);
+        for (int i = 0; i < 2; ++i) {
+          const int r = 8 * t + rc + i;
+          float mt = s_m[r];
+          for (int k = 1; k < kWarps; ++k) mt = fmaxf(mt, s_m[k * kRowsMax + r]);
+          const float w = ex2_approx(m[t][i] - (mt == -INFINITY ? 0.f : mt));
+          const int swz = ((r >> 1) & 3) * 8;
+#pragma unroll
+          for (int j = 0; j < 8; ++j) {
+            s_o[r * kHeadDim + ((16 * j + kr) ^ swz)] = o[j][t][i] * w;
+            s_o[r * kHeadDim + ((16 * j + 8 + kr) ^ swz)] = o[j][t][2 + i] * w;
+          }
         }
       __syncthreads();
-      {
-        const int r = tid >> 3, cc = (tid & 7) * 4;  // 16 rows x 8 groups of four columns
-        float4 a = *reinterpret_cast<const float4*>(s_join + r * kJoinCols + cc);
+      const bool whole = ends && first_kt == 0;
+      const long long slot = 2ll * blockIdx.x + (first_kt == 0 ? 1 : 0);  // a piece from a unit's start: place 1
+      // thread: four columns of every fourth row
+      const int cc = lane * 4;
+      for (int r = warp; r < cur.L * c.group; r += kWarps) {
+        float mt = s_m[r];
+        for (int k = 1; k < kWarps; ++k) mt = fmaxf(mt, s_m[k * kRowsMax + r]);
+        const float mu = mt == -INFINITY ? 0.f : mt;
+        float lt = 0.f;
+        for (int k = 0; k < kWarps; ++k) lt += s_l[k * kRowsMax + r] * ex2_approx(s_m[k * kRowsMax + r] - mu);
+        const float* src = reinterpret_cast<const float*>(smem + get * kStageBytes) + r * kHeadDim +
+                           (cc ^ (((r >> 1) & 3) * 8));
+        float4 a = *reinterpret_cast<const float4*>(src);
         for (int k = 1; k < kWarps; ++k) {
-          const float4 b = *reinterpret_cast<const float4*>(s_join + (k * kRowsT + r) * kJoinCols + cc);
+          const float4 b = *reinterpret_cast<const float4*>(src + k * (kStages * kStageBytes / 4));
           a.x += b.x; a.y += b.y; a.z += b.z; a.w += b.w;
         }
         if (!whole) {
-          *reinterpret_cast<float4*>(p.part_o + (slot * kRowsT + r) * kHeadDim + cb * kJoinCols + cc) = a;
+          *reinterpret_cast<float4*>(p.part_o + (slot * kRowsMax + r) * kHeadDim + cc) = a;
+          if (lane == 0) *reinterpret_cast<float2*>(p.part_ml + 2 * (slot * kRowsMax + r)) = make_float2(mt, lt);
         } else {
-          const int pr = cur.rt * kRowsT + r;
-          if (pr < cur.L * c.group)
-            *reinterpret_cast<uint2*>(p.out + ((long long)(cur.seq0 + pr / c.group) * c.hq + cur.g * c.group +
-                                               pr % c.group) * kHeadDim + cb * kJoinCols + cc) =
-                make_uint2(pack_bf16x2(a.x, a.y), pack_bf16x2(a.z, a.w));
+          const bool any = lt > 0.f || lt != lt;
+          const float inv = any ? 1.f / lt : 0.f;
+          const long long t = (long long)cur.seq0 + r / c.group;
+          const int h = cur.g * c.group + r % c.group;
+          *reinterpret_cast<uint2*>(p.out + (t * c.hq + h) * kHeadDim + cc) =
+              make_uint2(pack_bf16x2(a.x * inv, a.y * inv), pack_bf16x2(a.z * inv, a.w * inv));
+          if (lane == 0) {
+            const float z = any ? mu + log2f(lt) : -INFINITY;
+            const long long at = (long long)h * c.total_tokens + t;
+            if (p.lse2) p.lse2[at] = z;
+            if (p.lse) p.lse[at] = z * 0.6931471805599453f;
+          }
         }
       }
       __syncthreads();
+      fresh = true;
     }
-    fresh = true;
-    cursor_next(cur, c, tab, x + 1 < x1);
+    get = get + 1 == kStages ? 0 : get + 1;
+    cursor_next(cur, c, x + 1 < x1);
   }
   cp_async_wait<0>();
+}
+
+// Weights of the few-row schedule, from the scores that it left in the workspace (a hundredth of the
+// bytes of K): tile x of the line again, one thread per key.
+__global__ void __launch_bounds__(256) cache_rows_weights_kernel(const __grid_constant__ CacheAttnParams p) {
+  pdl_wait();
+  const CacheInfo& c = p.c;
+  Shares sh;
+  Cursor u;
+  if (!find_share(c, sh, u, p.score_tiles, nullptr)) return;
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, rs = p.score_rows;
+  const long long x0 = sh.at(blockIdx.x), x1 = sh.at(blockIdx.x + 1);
+  // warps 2 i and 2 i + 1 take tile x0 + i, + 4, ...: their halves of its keys
+  int ahead = warp >> 1;
+  for (long long x = x0; x < x1; ++x, cursor_next(u, c, x < x1)) {
+    if (ahead-- > 0) continue;
+    ahead = 3;
+    const int key = u.kt * kKeysT + (warp & 1) * 32 + lane;
+    const float* sc = p.scores + (x * kKeysT + (warp & 1) * 32 + lane) * rs;
+    const int rows = u.L * c.group;
+    if (key >= u.n) continue;
+    const long long at = slot_word(c, u.s, u.g, key);
+    if (at < 0) continue;  // flagged by the attention
+    const float old = p.decay > 0.f ? p.decay * c.weights[at] : 0.f;
+    float w = 0.f;
+    for (int r = 0; r < rows; r += 2) {
+      const float2 v = __ldcg(reinterpret_cast<const float2*>(sc + r));
+      const int h0 = u.g * c.group + r % c.group, t0 = u.seq0 + r / c.group;
+      w += ex2_approx(v.x - __ldcg(p.lse2 + (long long)h0 * c.total_tokens + t0));
+      if (r + 1 < rows) {
+        const int h1 = u.g * c.group + (r + 1) % c.group, t1 = u.seq0 + (r + 1) / c.group;
+        w += ex2_approx(v.y - __ldcg(p.lse2 + (long long)h1 * c.total_tokens + t1));
+      }
+    }
+    c.weights[at] = old + w;
+  }
 }
 
 // Joins the pieces of the units that several CTAs share. Block (b, y) looks at the unit inside of which the
@@ -350,7 +453,7 @@ __global__ void __launch_bounds__(kRowThreads, 2) cache_rows_kernel(const __grid
 // side by side: 32 maxima a warp at once, and where rows are few the warps share a row's pieces.
 template <bool kTiled>
 __global__ void __launch_bounds__(512) cache_join_kernel(const __grid_constant__ CacheAttnParams p) {
-  constexpr int kRowsU = kTiled ? 2 * kTileM : kRowsT;  // rows of a piece
+  constexpr int kRowsU = kTiled ? 2 * kTileM : kRowsMax;  // rows of a piece
   __shared__ float4 s_acc[16][32];
   pdl_wait();
   const int b = blockIdx.x + 1;
@@ -472,15 +575,15 @@ __global__ void __launch_bounds__(kRowThreads) cache_weights_kernel(const __grid
     float w[2][2] = {{0.f, 0.f}, {0.f, 0.f}};  // [8-key half][column] of this thread's rows
     const int rows = L * c.group;
     // tokens before key0 - len do not see any key of this warp
-    const int rt0 = key0 > len ? (key0 - len) * c.group / kRowsT : 0;
-    for (int rt = rt0; rt * kRowsT < rows; ++rt) {
+    const int rt0 = key0 > len ? (key0 - len) * c.group / kRowsMax : 0;
+    for (int rt = rt0; rt * kRowsMax < rows; ++rt) {
       float sc[2][4] = {{0.f, 0.f, 0.f, 0.f}, {0.f, 0.f, 0.f, 0.f}};
       const uint16_t* q0[2];
       float lse2[2];
       int last[2];
 #pragma unroll
       for (int i = 0; i < 2; ++i) {
-        const int r = rt * kRowsT + qr + 8 * i;
+        const int r = rt * kRowsMax + qr + 8 * i;
         const bool in = r < rows;
         const int t = in ? r / c.group : 0, h = g * c.group + (in ? r % c.group : 0);
         q0[i] = p.q + (long long)(seq0 + t) * p.q_stride + h * kHeadDim + qc;
@@ -490,15 +593,15 @@ __global__ void __launch_bounds__(kRowThreads) cache_weights_kernel(const __grid
       const int r = (lane & 7) + ((lane >> 4) << 3), hh = (lane >> 3) & 1;
 #pragma unroll
       for (int kk = 0; kk < 8; ++kk) {
-        uint32_t a[4], b0, b1, b2, b3;
+        uint32_t a[4], b[4];
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
           a[i] = __ldg(reinterpret_cast<const uint32_t*>(q0[i] + kk * 16));
           a[2 + i] = __ldg(reinterpret_cast<const uint32_t*>(q0[i] + kk * 16 + 8));
         }
-        ldsm4(sk + r * 256 + (((2 * kk + hh) ^ (r & 7)) << 4), b0, b1, b2, b3);
-        mma16816(sc[0], a, b0, b1);
-        mma16816(sc[1], a, b2, b3);
+        ldsm4(sk + r * 256 + (((2 * kk + hh) ^ (r & 7)) << 4), b);
+        mma16816(sc[0], a, b[0], b[1]);
+        mma16816(sc[1], a, b[2], b[3]);
       }
 #pragma unroll
       for (int i = 0; i < 2; ++i)
@@ -527,17 +630,24 @@ constexpr int weights_smem(int S) { return kWarps * kKeysW * 256 + 128 + 8 * (S 
 
 }  // namespace
 
-bool cache_attn_tiled(int32_t max_new, int32_t group) { return (int64_t)max_new * group > kRowsT; }
+bool cache_attn_tiled(int32_t max_new, int32_t group) { return (int64_t)max_new * group > kRowsMax; }
 
-CacheAttnLayout cache_attn_layout(int sms, bool tiled, int64_t hq, int64_t total_tokens) {
+CacheAttnLayout cache_attn_layout(int sms, bool tiled, const CacheInfo& c, bool scores) {
   auto up = [](int64_t x) { return (x + 255) & ~(int64_t)255; };
-  const int64_t grid = tiled ? sms : 2 * sms, rows = 2 * grid * (tiled ? 2 * kTileM : kRowsT);
+  const int64_t grid = tiled ? sms : 2 * sms, rows = 2 * grid * (tiled ? 2 * kTileM : kRowsMax);
   CacheAttnLayout w;
   w.part_o = 0;
   w.part_ml = up(w.part_o + rows * kHeadDim * 4);
   w.meta = up(w.part_ml + rows * 2 * 4);
   w.lse2 = up(w.meta + grid * kMetaWords * 4);
-  w.total = up(w.lse2 + hq * total_tokens * 4);
+  w.scores = up(w.lse2 + (int64_t)c.hq * c.total_tokens * 4);
+  w.score_rows = (c.max_new * c.group + 1) / 2 * 2;
+  // tiles of a call that writes weights: by the longest sequence that there may be, and by the pages, which no
+  // two sequences share then
+  const int64_t by_len = (int64_t)c.num_seqs * ((c.max_len + kKeysT - 1) / kKeysT);
+  const int64_t by_page = ((int64_t)c.num_pages * c.page_size + kKeysT - 1) / kKeysT + c.num_seqs;
+  w.score_tiles = (by_len < by_page ? by_len : by_page) * c.hkv;
+  w.total = tiled || !scores ? w.scores : up(w.scores + w.score_tiles * kKeysT * w.score_rows * 4);
   return w;
 }
 
@@ -553,24 +663,24 @@ cudaError_t launch_cache_join(const CacheAttnParams& p, bool tiled, int ctas, cu
 }
 
 cudaError_t launch_cache_attn(const CacheAttnParams& p, bool tiled, int sms, cudaStream_t st) {
-  static unsigned long long attr[kMaxCachedDevices] = {}, attr_w[kMaxCachedDevices] = {};
+  static unsigned long long attr[3][kMaxCachedDevices] = {}, attr_w[kMaxCachedDevices] = {};
   cudaError_t e;
   if (tiled) {
-    if ((e = launch_cache_tiles(p, sms, st)) != cudaSuccess) return e;
-  } else {
-    e = set_max_smem(reinterpret_cast<const void*>(cache_rows_kernel), row_smem(kMaxSeqs), attr, true);
-    if (e != cudaSuccess) return e;
-    const int grid = 2 * sms;
-    cache_rows_kernel<<<grid, kRowThreads, row_smem(p.c.num_seqs), st>>>(p);
-    if ((e = cudaGetLastError()) != cudaSuccess) return e;
-    if ((e = launch_cache_join(p, false, grid, st)) != cudaSuccess) return e;
+    if ((e = launch_cache_tiles(p, sms, st)) != cudaSuccess || !(p.decay >= 0.f)) return e;
+    if ((e = set_max_smem(reinterpret_cast<const void*>(cache_weights_kernel), weights_smem(kMaxSeqs), attr_w, true)) !=
+        cudaSuccess)
+      return e;
+    cache_weights_kernel<<<8 * sms, kRowThreads, weights_smem(p.c.num_seqs), st>>>(p);
+    return cudaGetLastError();
   }
-  if (!(p.decay >= 0.f)) return cudaSuccess;
-  if ((e = set_max_smem(reinterpret_cast<const void*>(cache_weights_kernel), weights_smem(kMaxSeqs), attr_w, true)) !=
-      cudaSuccess)
+  const int nt = p.c.max_new * p.c.group <= 8 ? 1 : 2, grid = 2 * sms;
+  void (*fn)(const CacheAttnParams) = nt == 1 ? cache_rows_kernel<1> : cache_rows_kernel<2>;
+  if ((e = set_max_smem(reinterpret_cast<const void*>(fn), kRowSmem, attr[nt - 1], true)) != cudaSuccess) return e;
+  if ((e = launch_pdl(fn, dim3(grid), kRowThreads, kRowSmem, st, p)) != cudaSuccess) return e;
+  if ((e = launch_cache_join(p, false, grid, st)) != cudaSuccess || !(p.decay >= 0.f)) return e;
+  if ((e = set_max_smem(reinterpret_cast<const void*>(cache_rows_weights_kernel), 0, attr[2], true)) != cudaSuccess)
     return e;
-  cache_weights_kernel<<<8 * sms, kRowThreads, weights_smem(p.c.num_seqs), st>>>(p);
-  return cudaGetLastError();
+  return launch_pdl(cache_rows_weights_kernel, dim3(4 * sms), 256, 0, st, p);
 }
 
 }  // namespace fp

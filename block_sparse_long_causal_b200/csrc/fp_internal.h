@@ -150,6 +150,9 @@ struct __align__(64) CacheAttnParams {
   float* part_o;              // workspace: partial outputs [2 * grid][rows][128], not normalised
   float* part_ml;             // workspace: their running max (log2 units) and row sum, 2 * grid * rows of each
   int32_t* meta;              // workspace: the unit that each CTA's range begins inside of [grid][kMetaWords]
+  float* scores;              // workspace: scaled scores [tile of the line][64 keys][score_rows] (few rows), or null
+  int32_t score_rows;
+  int64_t score_tiles;        // tiles that fit
   float decay;                // weights = decay * weights + this call's; < 0: weights are left alone
   int32_t* dev_status;
   uint64_t wait_limit_ns;
@@ -210,9 +213,11 @@ constexpr int kMetaWords = 8;               // ints per CTA that describe the un
 // Schedule of the attention call: 16-row tiles (fp_cache_attn.cu) or 128-row tiles (fp_cache_tiles.cu).
 bool cache_attn_tiled(int32_t max_new, int32_t group);
 struct CacheAttnLayout {                    // byte offsets of its workspace
-  int64_t part_o, part_ml, meta, lse2, total;
+  int64_t part_o, part_ml, meta, lse2, scores, total;
+  int64_t score_tiles;
+  int32_t score_rows;
 };
-CacheAttnLayout cache_attn_layout(int sms, bool tiled, int64_t hq, int64_t total_tokens);
+CacheAttnLayout cache_attn_layout(int sms, bool tiled, const CacheInfo& c, bool scores);
 cudaError_t launch_cache_attn(const CacheAttnParams& p, bool tiled, int sms, cudaStream_t st);
 cudaError_t launch_cache_tiles(const CacheAttnParams& p, int sms, cudaStream_t st);
 // Joins the pieces of the units that several of `ctas` CTAs shared.
