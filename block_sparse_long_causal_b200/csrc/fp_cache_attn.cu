@@ -86,17 +86,18 @@ __device__ __forceinline__ void cursor_next(Cursor& u, const CacheInfo& c, bool 
   do load_seq(u, c, ++s);
   while (u.kts == 0 && s + 1 < c.num_seqs);
 }
-// Share of CTA i: [share(i), share(i + 1)), the first `rem` ones one tile longer.
+// Share of CTA (or warp) i of `ctas`: [share(i), share(i + 1)), the first `rem` ones one tile longer.
 struct Shares {
   long long q;
   int rem, ctas;
   __device__ __forceinline__ long long at(int i) const { return i * q + min(i, rem); }
 };
 // Every warp by itself: lane i sums the tiles of a contiguous run of sequences, a scan gives the total, and
-// the lane whose run holds the start of the CTA's share walks it. No shared memory and no barrier: this
+// the lane whose run holds the start of share `me` walks it. No shared memory and no barrier: this
 // chain is most of what a short call waits for. The device arrays are checked against the host's
 // description here, before any other access depends on them.
-__device__ __forceinline__ bool find_share(const CacheInfo& c, Shares& sh, Cursor& u, long long max_tiles, int32_t* dev_status) {
+__device__ __forceinline__ bool find_share(const CacheInfo& c, Shares& sh, Cursor& u, int me, int parts, long long max_tiles,
+                                           int32_t* dev_status) {
   const int lane = threadIdx.x & 31, S = c.num_seqs, per = (S + 31) / 32;
   const int a = min(S, lane * per), b = min(S, a + per);
   long long sum = 0;
@@ -118,8 +119,7 @@ __device__ __forceinline__ bool find_share(const CacheInfo& c, Shares& sh, Curso
     if (threadIdx.x == 0 && blockIdx.x == 0) dev_flag(dev_status, kDevBadProblem);
     return false;
   }
-  sh.ctas = (int)min((long long)gridDim.x, total);
-  const int me = blockIdx.x;
+  sh.ctas = (int)min((long long)parts, total);
   if (me >= sh.ctas) return false;
   if (total < 0x7fffffffll) {
     sh.q = (unsigned)total / (unsigned)sh.ctas;
@@ -162,7 +162,7 @@ __global__ void __launch_bounds__(kRowThreads, 2) cache_rows_kernel(const __grid
   Shares sh;
   Cursor cur;
   int32_t* meta = p.meta + (long long)blockIdx.x * kMetaWords;
-  const bool work = find_share(c, sh, cur, p.scores ? p.score_tiles : 0x7fffffffffffffffll, p.dev_status);
+  const bool work = find_share(c, sh, cur, blockIdx.x, gridDim.x, p.scores ? p.score_tiles : 0x7fffffffffffffffll, p.dev_status);
   pdl_trigger();
   if (!work) {
     if (tid == 0) meta[0] = 0;
@@ -411,38 +411,47 @@ __global__ void __launch_bounds__(kRowThreads, 2) cache_rows_kernel(const __grid
 }
 
 // Weights of the few-row schedule, from the scores that it left in the workspace (a hundredth of the
-// bytes of K): tile x of the line again, one thread per key.
+// bytes of K): the line of tiles again, shared out over the warps; a lane takes keys lane and lane + 32 of a tile.
 __global__ void __launch_bounds__(256) cache_rows_weights_kernel(const __grid_constant__ CacheAttnParams p) {
   pdl_wait();
   const CacheInfo& c = p.c;
   Shares sh;
   Cursor u;
-  if (!find_share(c, sh, u, p.score_tiles, nullptr)) return;
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, rs = p.score_rows;
-  const long long x0 = sh.at(blockIdx.x), x1 = sh.at(blockIdx.x + 1);
-  // warps 2 i and 2 i + 1 take tile x0 + i, + 4, ...: their halves of its keys
-  int ahead = warp >> 1;
+  const int me = blockIdx.x * (blockDim.x >> 5) + (threadIdx.x >> 5), lane = threadIdx.x & 31, rs = p.score_rows;
+  if (!find_share(c, sh, u, me, gridDim.x * (blockDim.x >> 5), p.score_tiles, nullptr)) return;
+  const long long x0 = sh.at(me), x1 = sh.at(me + 1);
+  float z = 0.f;  // lane r: lse2 of the unit's row r
+  int s = -1, g = -1;
   for (long long x = x0; x < x1; ++x, cursor_next(u, c, x < x1)) {
-    if (ahead-- > 0) continue;
-    ahead = 3;
-    const int key = u.kt * kKeysT + (warp & 1) * 32 + lane;
-    const float* sc = p.scores + (x * kKeysT + (warp & 1) * 32 + lane) * rs;
     const int rows = u.L * c.group;
-    if (key >= u.n) continue;
-    const long long at = slot_word(c, u.s, u.g, key);
-    if (at < 0) continue;  // flagged by the attention
-    const float old = p.decay > 0.f ? p.decay * c.weights[at] : 0.f;
-    float w = 0.f;
+    if (u.s != s || u.g != g) {
+      s = u.s;
+      g = u.g;
+      z = lane < rows ? __ldcg(p.lse2 + (long long)(g * c.group + lane % c.group) * c.total_tokens + u.seq0 +
+                               lane / c.group)
+                      : INFINITY;
+    }
+    const float* sc = p.scores + (x * kKeysT + lane) * rs;
+    long long at[2];
+    float old[2] = {0.f, 0.f}, w[2] = {0.f, 0.f};
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      const int key = u.kt * kKeysT + 32 * i + lane;
+      at[i] = key < u.n ? slot_word(c, s, g, key) : -1;  // a bad page was flagged by the attention
+      if (at[i] >= 0 && p.decay > 0.f) old[i] = c.weights[at[i]];
+    }
     for (int r = 0; r < rows; r += 2) {
-      const float2 v = __ldcg(reinterpret_cast<const float2*>(sc + r));
-      const int h0 = u.g * c.group + r % c.group, t0 = u.seq0 + r / c.group;
-      w += ex2_approx(v.x - __ldcg(p.lse2 + (long long)h0 * c.total_tokens + t0));
-      if (r + 1 < rows) {
-        const int h1 = u.g * c.group + (r + 1) % c.group, t1 = u.seq0 + (r + 1) / c.group;
-        w += ex2_approx(v.y - __ldcg(p.lse2 + (long long)h1 * c.total_tokens + t1));
+      const float z0 = __shfl_sync(kAll, z, r), z1 = __shfl_sync(kAll, z, r + 1);
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        const float2 v = __ldcg(reinterpret_cast<const float2*>(sc + 32 * i * rs + r));
+        w[i] += ex2_approx(v.x - z0);
+        if (r + 1 < rows) w[i] += ex2_approx(v.y - z1);
       }
     }
-    c.weights[at] = old + w;
+#pragma unroll
+    for (int i = 0; i < 2; ++i)
+      if (at[i] >= 0) c.weights[at[i]] = p.decay > 0.f ? fmaf(p.decay, old[i], w[i]) : w[i];
   }
 }
 
@@ -532,102 +541,6 @@ __global__ void __launch_bounds__(512) cache_join_kernel(const __grid_constant__
   }
 }
 
-// ------------------------------------------------------------------------ collected weights -----
-// Every warp takes 16 keys of one (sequence, kv-head) and walks the rows of its new tokens, 16 at a
-// time: S again from Q and K, then p = 2^(S - lse2) summed over the rows. No two warps touch one
-// weight, so the sum's order is fixed.
-__global__ void __launch_bounds__(kRowThreads) cache_weights_kernel(const __grid_constant__ CacheAttnParams p) {
-  extern __shared__ __align__(128) unsigned char smem[];
-  const CacheInfo& c = p.c;
-  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  uint32_t sk = smem_u32(smem) + warp * kKeysW * 256;
-  long long* tab = reinterpret_cast<long long*>(smem + kWarps * kKeysW * 256 + 128);
-  long long* s_scan = reinterpret_cast<long long*>(smem + kWarps * kKeysW * 256);
-  int* s_bad = reinterpret_cast<int*>(s_scan + kWarps);
-  const bool ok = cache_table<kRowThreads>(c, tab, s_scan, s_bad, p.dev_status, [&](int, int L, int n) -> long long {
-    return L > 0 ? (long long)c.hkv * ((n + kKeysT - 1) / kKeysT) : 0ll;
-  });
-  const long long total = ok ? tab[c.num_seqs] : 0;
-  const int qr = lane >> 2, qc = (lane & 3) * 2;
-  for (long long x = blockIdx.x; x < total; x += gridDim.x) {
-    const int s = find_seq64(tab, c.num_seqs, x);
-    const int seq0 = __ldg(c.cu_seqlens + s), L = __ldg(c.cu_seqlens + s + 1) - seq0, len = c.lens[s], n = len + L;
-    const int kts = (n + kKeysT - 1) / kKeysT;
-    const int g = (int)((x - tab[s]) / kts), kt = (int)((x - tab[s]) % kts);
-    const int key0 = kt * kKeysT + warp * kKeysW;
-    if (key0 >= n) continue;
-    const long long row0 = slot_row(c, s, key0);
-    if (row0 < 0) {
-      if (lane == 0) dev_flag(p.dev_status, kDevBadProblem);
-      continue;
-    }
-    const int live = min(kKeysW, n - key0);
-    __syncwarp();
-#pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      const int r = 2 * i + (lane >> 4), ch = lane & 15;
-      cp_async16(sk + r * 256 + ((ch ^ (r & 7)) << 4),
-                 c.k + ((row0 + (r < live ? r : 0)) * c.hkv + g) * kHeadDim + ch * 8, r < live);
-    }
-    cp_async_commit();
-    cp_async_wait<0>();
-    __syncwarp();
-    float w[2][2] = {{0.f, 0.f}, {0.f, 0.f}};  // [8-key half][column] of this thread's rows
-    const int rows = L * c.group;
-    // tokens before key0 - len do not see any key of this warp
-    const int rt0 = key0 > len ? (key0 - len) * c.group / kRowsMax : 0;
-    for (int rt = rt0; rt * kRowsMax < rows; ++rt) {
-      float sc[2][4] = {{0.f, 0.f, 0.f, 0.f}, {0.f, 0.f, 0.f, 0.f}};
-      const uint16_t* q0[2];
-      float lse2[2];
-      int last[2];
-#pragma unroll
-      for (int i = 0; i < 2; ++i) {
-        const int r = rt * kRowsMax + qr + 8 * i;
-        const bool in = r < rows;
-        const int t = in ? r / c.group : 0, h = g * c.group + (in ? r % c.group : 0);
-        q0[i] = p.q + (long long)(seq0 + t) * p.q_stride + h * kHeadDim + qc;
-        lse2[i] = __ldg(p.lse2 + (long long)h * c.total_tokens + seq0 + t);
-        last[i] = in ? len + t : -1;
-      }
-      const int r = (lane & 7) + ((lane >> 4) << 3), hh = (lane >> 3) & 1;
-#pragma unroll
-      for (int kk = 0; kk < 8; ++kk) {
-        uint32_t a[4], b[4];
-#pragma unroll
-        for (int i = 0; i < 2; ++i) {
-          a[i] = __ldg(reinterpret_cast<const uint32_t*>(q0[i] + kk * 16));
-          a[2 + i] = __ldg(reinterpret_cast<const uint32_t*>(q0[i] + kk * 16 + 8));
-        }
-        ldsm4(sk + r * 256 + (((2 * kk + hh) ^ (r & 7)) << 4), b);
-        mma16816(sc[0], a, b[0], b[1]);
-        mma16816(sc[1], a, b[2], b[3]);
-      }
-#pragma unroll
-      for (int i = 0; i < 2; ++i)
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          const int key = key0 + (e >> 1) * 8 + qc + (e & 1);
-          if (key <= last[i]) w[e >> 1][e & 1] += ex2_approx(fmaf(sc[e >> 1][2 * i + (e & 1)], p.scale_log2, -lse2[i]));
-        }
-    }
-#pragma unroll
-    for (int e = 0; e < 4; ++e) {
-      float v = w[e >> 1][e & 1];
-      v += __shfl_xor_sync(kAll, v, 4);
-      v += __shfl_xor_sync(kAll, v, 8);
-      v += __shfl_xor_sync(kAll, v, 16);
-      const int k = (e >> 1) * 8 + qc + (e & 1);
-      if (lane < 4 && k < live) {
-        const long long page = row0 / c.page_size;
-        float* dst = c.weights + (page * c.hkv + g) * c.page_size + (row0 - page * c.page_size) + k;
-        *dst = p.decay > 0.f ? fmaf(p.decay, *dst, v) : v;
-      }
-    }
-  }
-}
-constexpr int weights_smem(int S) { return kWarps * kKeysW * 256 + 128 + 8 * (S + 1); }
-
 }  // namespace
 
 bool cache_attn_tiled(int32_t max_new, int32_t group) { return (int64_t)max_new * group > kRowsMax; }
@@ -663,15 +576,11 @@ cudaError_t launch_cache_join(const CacheAttnParams& p, bool tiled, int ctas, cu
 }
 
 cudaError_t launch_cache_attn(const CacheAttnParams& p, bool tiled, int sms, cudaStream_t st) {
-  static unsigned long long attr[3][kMaxCachedDevices] = {}, attr_w[kMaxCachedDevices] = {};
+  static unsigned long long attr[3][kMaxCachedDevices] = {};
   cudaError_t e;
   if (tiled) {
     if ((e = launch_cache_tiles(p, sms, st)) != cudaSuccess || !(p.decay >= 0.f)) return e;
-    if ((e = set_max_smem(reinterpret_cast<const void*>(cache_weights_kernel), weights_smem(kMaxSeqs), attr_w, true)) !=
-        cudaSuccess)
-      return e;
-    cache_weights_kernel<<<8 * sms, kRowThreads, weights_smem(p.c.num_seqs), st>>>(p);
-    return cudaGetLastError();
+    return launch_cache_weights(p, sms, st);
   }
   const int nt = p.c.max_new * p.c.group <= 8 ? 1 : 2, grid = 2 * sms;
   void (*fn)(const CacheAttnParams) = nt == 1 ? cache_rows_kernel<1> : cache_rows_kernel<2>;
