@@ -2,6 +2,8 @@
 // of the slots that stay by collected attention weight, compaction.
 #include <cooperative_groups.h>
 
+#include <type_traits>
+
 #include "fp_cache.cuh"
 
 namespace cg = cooperative_groups;
@@ -76,18 +78,21 @@ constexpr int kSelThreads = 512, kSelWarps = kSelThreads / 32;
 constexpr int kSelCluster = 16;      // largest cluster
 constexpr int kSelSpan = 8192;       // slots a CTA is meant to take (16 a thread)
 constexpr int kSelKeysMax = 24576;   // keys kept in shared memory (96 KB: two CTAs fit an SM)
+constexpr int kSelBins = 2048;
+static_assert(kSelBins == 4 * kSelThreads, "a thread sums four bins");
 
 // One cluster per (sequence, kv-head); each of its CTAs takes a contiguous range of the slots, a
 // contiguous part of it per warp. The slots are read once: their keys stay in shared memory (a range
 // longer than kSelKeysMax is read again in every pass). The key of rank `budget` is found by a radix select,
-// four passes of eight bits over the keys that match the prefix so far; the CTAs' histograms are summed
-// through distributed shared memory, one cluster barrier a pass. Then every warp counts its slots above and
-// at the threshold, and after a scan over the cluster's warps writes its holes (evicted slots below the
-// budget) and sources (kept slots at or past it) in ascending order.
+// three passes of 11, 11 and 10 bits over the keys that match the prefix so far; a CTA adds its
+// occupied bins (few: weights cluster) to every CTA's sums through distributed shared memory, one cluster
+// barrier a pass. Then every warp counts its slots above and at the threshold, and after a scan over the cluster's warps writes its holes (evicted slots below
+// the budget) and sources (kept slots at or past it) in ascending order.
+// Bound by latency (a few thousand slots a CTA): the loops keep several slots a lane in flight.
 __global__ void __launch_bounds__(kSelThreads, 2) select_kernel(const SelectParams p, const int keys_cap) {
   extern __shared__ uint32_t s_keys[];
-  __shared__ unsigned s_hist[2][256];
-  __shared__ unsigned s_tot[8], s_pick[2];
+  __shared__ __align__(16) unsigned s_hist[kSelBins], s_sum[2][kSelBins];
+  __shared__ unsigned s_tot[kSelWarps], s_pick[2];
   __shared__ int4 s_cnt[kSelWarps];                // slots above / at the threshold, below / past the budget
   __shared__ int s_eq[kSelCluster * kSelWarps + 1], s_hole[kSelCluster * kSelWarps + 1], s_from[kSelCluster * kSelWarps + 1];
   __shared__ int s_part[3][8];
@@ -112,84 +117,138 @@ __global__ void __launch_bounds__(kSelThreads, 2) select_kernel(const SelectPara
   // positions at or past `young` are protected (the difference cannot overflow: 64 bits)
   const long long young = (long long)(p.next_pos ? p.next_pos[s] : len) + L - p.recent;
   bool bad_page = false;
-  auto read_key = [&](int u) -> uint32_t {
-    const long long w = slot_word(c, s, g, u);
-    if (w < 0) {
-      bad_page = true;
-      return 0u;
+  // keys of slots u, u + 32, ... (K of them; past the last slot: anything), all their reads in flight together
+  auto read_keys = [&](int u, uint32_t* out, auto count) {
+    constexpr int K = decltype(count)::value;
+    long long w[K];
+    float val[K];
+    int pos[K];
+#pragma unroll
+    for (int i = 0; i < K; ++i) w[i] = slot_word(c, s, g, min(u + 32 * i, n - 1));
+#pragma unroll
+    for (int i = 0; i < K; ++i) {
+      val[i] = __ldg(c.weights + max(w[i], 0ll));
+      pos[i] = c.positions ? __ldg(c.positions + max(w[i], 0ll)) : u + 32 * i;
     }
-    const int pos = c.positions ? __ldg(c.positions + w) : u;
-    return rank_key(__ldg(c.weights + w), pos < p.sinks || pos >= young);
+#pragma unroll
+    for (int i = 0; i < K; ++i) {
+      bad_page |= w[i] < 0;
+      out[i] = w[i] < 0 ? 0u : rank_key(val[i], pos[i] < p.sinks || pos[i] >= young);
+    }
   };
   const int wspan = (int)((((long long)n + C * kSelWarps - 1) / (C * kSelWarps) + 31) & ~31ll);  // slots a warp
   const long long first = (long long)rank * kSelWarps * wspan;
   const int base = (int)min((long long)n, first);
   const int u0 = (int)min((long long)n, first + warp * wspan), u1 = min(n, u0 + wspan);
   const bool kept = kSelWarps * wspan <= keys_cap;
+  *reinterpret_cast<uint4*>(&s_hist[4 * tid]) = make_uint4(0, 0, 0, 0);
+  *reinterpret_cast<uint4*>(&s_sum[0][4 * tid]) = make_uint4(0, 0, 0, 0);
   if (kept) {
-#pragma unroll 8
-    for (int u = u0 + lane; u < u1; u += 32) s_keys[u - base] = read_key(u);
+    for (int u = u0 + lane; u < u1; u += 32 * 8) {
+      uint32_t k[8];
+      read_keys(u, k, std::integral_constant<int, 8>());
+#pragma unroll
+      for (int i = 0; i < 8; ++i)
+        if (u + 32 * i < u1) s_keys[u + 32 * i - base] = k[i];
+    }
     __syncwarp();  // a warp reads back its own keys only
   }
-  auto key_of = [&](int u) -> uint32_t { return kept ? s_keys[u - base] : read_key(u); };
-  if (tid < 256) s_hist[0][tid] = 0;
-  __syncthreads();
+  // f(slot of lane 0, key) for the warp's slots, 32 at a time in ascending order; lanes past u1 get any key
+  auto each = [&](auto f) {
+    for (int u = u0; u < u1; u += 128) {
+      uint32_t k[4];
+      if (kept) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) k[i] = s_keys[min(u + 32 * i + lane, u1 - 1) - base];
+      } else {
+        read_keys(u + lane, k, std::integral_constant<int, 4>());
+      }
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+        if (u + 32 * i < u1) f(u + 32 * i, k[i]);
+    }
+  };
+  auto sync_all = [&] {
+    if (C == 1) __syncthreads();
+    else cluster.sync();
+  };
+  sync_all();  // every CTA's sums are zero before another adds to them
   unsigned prefix = 0, need = (unsigned)p.budget;  // `need` keys of the current prefix class stay
 #pragma unroll 1
-  for (int pass = 0; pass < 4; ++pass) {
-    const int shift = 24 - 8 * pass;
-    unsigned* hist = s_hist[pass & 1];
-    for (int u = u0; u < u1; u += 32) {
-      const bool in = u + lane < u1;
-      const uint32_t k = in ? key_of(u + lane) : 0u;
-      const bool match = in && (pass == 0 || (k >> (shift + 8)) == prefix);
+  for (int pass = 0; pass < 3; ++pass) {
+    const int shift = pass == 0 ? 21 : pass == 1 ? 10 : 0, bits = pass == 2 ? 10 : 11;
+    const unsigned mask = (1u << bits) - 1u;
+    each([&](int u, uint32_t k) {
+      const bool match = u + lane < u1 && (pass == 0 || (k >> (shift + bits)) == prefix);
       const unsigned act = __ballot_sync(kFullMask, match);
-      if (match) {  // equal digits of a warp (protected slots, ties) are added once
-        const unsigned dig = (k >> shift) & 255u, same = __match_any_sync(act, dig);
-        if (lane == __ffs(same) - 1) atomicAdd(&hist[dig], (unsigned)__popc(same));
-      }
+      // the warp's most likely run of equal digits (protected slots, ties) is added once: that of its first lane
+      const unsigned dig = (k >> shift) & mask;
+      const unsigned lead = __shfl_sync(kFullMask, dig, act ? __ffs(act) - 1 : 0);
+      const unsigned same = __ballot_sync(kFullMask, match && dig == lead);
+      if (match && dig != lead) atomicAdd(&s_hist[dig], 1u);
+      if (lane == 0 && act) atomicAdd(&s_hist[lead], (unsigned)__popc(same));
+    });
+    __syncthreads();
+    // thread t owns bins 2047 - 4 t and the three below, so that an inclusive scan counts the larger digits
+    const int bin = kSelBins - 4 - 4 * tid;
+    uint4 cnt = *reinterpret_cast<const uint4*>(&s_hist[bin]);
+    *reinterpret_cast<uint4*>(&s_hist[bin]) = make_uint4(0, 0, 0, 0);
+    if (C > 1) {
+      unsigned* sums = s_sum[pass & 1];
+      // the other buffer is zeroed for the next pass, which no CTA begins before the barrier below
+      *reinterpret_cast<uint4*>(&s_sum[(pass + 1) & 1][bin]) = make_uint4(0, 0, 0, 0);
+      if (cnt.x | cnt.y | cnt.z | cnt.w)
+        for (int r = 0; r < C; ++r) {
+          unsigned* dst = cluster.map_shared_rank(&sums[bin], r);
+          if (cnt.x) atomicAdd(dst, cnt.x);
+          if (cnt.y) atomicAdd(dst + 1, cnt.y);
+          if (cnt.z) atomicAdd(dst + 2, cnt.z);
+          if (cnt.w) atomicAdd(dst + 3, cnt.w);
+        }
+      cluster.sync();
+      cnt = *reinterpret_cast<const uint4*>(&sums[bin]);
     }
-    cluster.sync();
-    // digit d of the whole cluster in thread 255 - d, so that an inclusive scan counts the larger digits
-    unsigned cnt = 0, incl = 0;
-    if (tid < 256) {
-      for (int r = 0; r < C; ++r) cnt += *cluster.map_shared_rank(&hist[255 - tid], r);
-      incl = cnt;
+    const unsigned sum = cnt.x + cnt.y + cnt.z + cnt.w;
+    unsigned incl = warp_incl_scan(sum);
+    if (lane == 31) s_tot[warp] = incl;
+    __syncthreads();
 #pragma unroll
-      for (int o = 1; o < 32; o <<= 1) {
-        const unsigned x = __shfl_up_sync(kFullMask, incl, o);
-        if (lane >= o) incl += x;
+    for (int w = 0; w < kSelWarps; ++w) incl += w < warp ? s_tot[w] : 0u;
+    unsigned above = incl - sum;  // keys of larger bins
+    if (incl >= need && above < need) {
+      int at = bin + 3;
+      if (above + cnt.w < need) {
+        above += cnt.w;
+        --at;
+        if (above + cnt.z < need) {
+          above += cnt.z;
+          --at;
+          if (above + cnt.y < need) {
+            above += cnt.y;
+            --at;
+          }
+        }
       }
-      if (lane == 31) s_tot[warp] = incl;
-      // the other buffer is read by no CTA any more: all have passed the barrier above
-      s_hist[(pass + 1) & 1][tid] = 0;
+      s_pick[0] = (unsigned)at;
+      s_pick[1] = need - above;
     }
     __syncthreads();
-    if (tid < 256) {
-      for (int w = 0; w < warp; ++w) incl += s_tot[w];
-      if (incl >= need && incl - cnt < need) {
-        s_pick[0] = 255u - tid;
-        s_pick[1] = need - (incl - cnt);
-      }
-    }
-    __syncthreads();
-    prefix = (prefix << 8) | s_pick[0];
+    prefix = (prefix << bits) | s_pick[0];
     need = s_pick[1];
   }
   const uint32_t thr = prefix;  // keys above thr stay, and the first `need` slots whose key is thr
   int4 cnt = make_int4(0, 0, 0, 0);
-  for (int u = u0; u < u1; u += 32) {
+  each([&](int u, uint32_t k) {
     const bool in = u + lane < u1;
-    const uint32_t k = in ? key_of(u + lane) : 0u;
     const unsigned below = __ballot_sync(kFullMask, u + lane < p.budget);
     const unsigned mg = __ballot_sync(kFullMask, in && k > thr), me = __ballot_sync(kFullMask, in && k == thr);
     cnt.x += __popc(mg & below);
     cnt.y += __popc(mg & ~below);
     cnt.z += __popc(me & below);
     cnt.w += __popc(me & ~below);
-  }
+  });
   if (lane == 0) s_cnt[warp] = cnt;
-  cluster.sync();
+  sync_all();
   // ---- scans over the cluster's warps in slot order: slots at the threshold before a warp, then its
   // holes and sources (the kept slots at the threshold are the first `need` of them)
   const int W = C * kSelWarps;
@@ -236,9 +295,8 @@ __global__ void __launch_bounds__(kSelThreads, 2) select_kernel(const SelectPara
   hole = s_hole[me_w];
   from = s_from[me_w];
   const int total = s_from[256];
-  for (int u = u0; u < u1; u += 32) {
+  each([&](int u, uint32_t k) {
     const bool in = u + lane < u1;
-    const uint32_t k = in ? key_of(u + lane) : 0u;
     const unsigned me = __ballot_sync(kFullMask, in && k == thr);
     const unsigned lt = (1u << lane) - 1u;
     const bool keep = in && (k > thr || (k == thr && eq_before + __popc(me & lt) < (int)need));
@@ -249,11 +307,11 @@ __global__ void __launch_bounds__(kSelThreads, 2) select_kernel(const SelectPara
     hole += __popc(mh);
     from += __popc(ms);
     eq_before += __popc(me);
-  }
+  });
   for (long long i = 2ll * total + rank * kSelThreads + tid; i < 2ll * p.budget; i += C * kSelThreads) moves[i] = -1;
   if (tid == 0 && rank == 0) p.move_counts[sg] = total;
   if (bad_page) dev_flag(p.dev_status, kDevBadProblem);
-  cluster.sync();  // no CTA ends while another still reads its counts
+  if (C > 1) cluster.sync();  // no CTA ends while another still reads its counts
 }
 
 cudaError_t launch_select(const SelectParams& p, int sms, cudaStream_t st) {
@@ -288,7 +346,7 @@ cudaError_t launch_select(const SelectParams& p, int sms, cudaStream_t st) {
 // lie at or past the budget and destinations below it (checked), so no move reads what another one
 // writes and the order of the moves does not matter.
 constexpr int kMovesW = 8;
-__global__ void __launch_bounds__(256) compact_kernel(const CompactParams p) {
+__global__ void __launch_bounds__(256, 4) compact_kernel(const CompactParams p) {
   const CacheInfo& c = p.c;
   const int lane = threadIdx.x & 31, sg = blockIdx.x / p.parts, part = blockIdx.x % p.parts;
   const int s = sg / c.hkv, g = sg % c.hkv;
@@ -304,35 +362,44 @@ __global__ void __launch_bounds__(256) compact_kernel(const CompactParams p) {
   }
   const int2* moves = reinterpret_cast<const int2*>(p.moves) + (long long)sg * p.budget;
   const int n = min(cnt, p.budget);
-  for (long long i = (part * 8 + (threadIdx.x >> 5)) * kMovesW; i < n; i += p.parts * 8 * kMovesW) {
-    long long src = -1, dst = -1;
-    if (lane < kMovesW && i + lane < n) {
-      const int2 mv = moves[i + lane];
-      if (mv.x < p.budget || mv.x >= slots || mv.y < 0 || mv.y >= p.budget || mv.y >= slots) {
-        dev_flag(p.dev_status, kDevBadList);
-      } else {
-        src = slot_row(c, s, mv.x);
-        dst = slot_row(c, s, mv.y);
-        if (src < 0 || dst < 0) {
-          dev_flag(p.dev_status, kDevBadProblem);
-          src = -1;
-        }
-      }
+  // lane m < kMovesW: rows of move i + m, or -1
+  auto entry = [&](long long i, long long& src, long long& dst) {
+    src = dst = -1;
+    if (lane >= kMovesW || i + lane >= n) return;
+    const int2 mv = moves[i + lane];
+    if (mv.x < p.budget || mv.x >= slots || mv.y < 0 || mv.y >= p.budget || mv.y >= slots) {
+      dev_flag(p.dev_status, kDevBadList);
+      return;
     }
-    float w = 0.f;
-    int pos = 0;
-    const long long ps = src / c.page_size, pd = dst / c.page_size;
-    const long long ws = (ps * c.hkv + g) * c.page_size + (src - ps * c.page_size);
-    const long long wd = (pd * c.hkv + g) * c.page_size + (dst - pd * c.page_size);
-    if (src >= 0 && c.weights) w = c.weights[ws];
-    if (src >= 0 && c.positions) pos = c.positions[ws];
-    uint4* rows = reinterpret_cast<uint4*>(lane < 16 ? c.k : c.v) + (lane & 15);
+    src = slot_row(c, s, mv.x);
+    dst = slot_row(c, s, mv.y);
+    if (src < 0 || dst < 0) {
+      dev_flag(p.dev_status, kDevBadProblem);
+      src = -1;
+    }
+  };
+  const int step = p.parts * 8 * kMovesW;
+  long long i = (part * 8 + (threadIdx.x >> 5)) * kMovesW, src, dst;
+  if (i >= n) return;
+  entry(i, src, dst);
+  uint4* rows = reinterpret_cast<uint4*>(lane < 16 ? c.k : c.v) + (lane & 15);
+  for (;; i += step) {
     uint4 v[kMovesW];
 #pragma unroll
     for (int m = 0; m < kMovesW; ++m) {
       const long long a = __shfl_sync(kFullMask, src, m);
       if (a >= 0) v[m] = rows[(a * c.hkv + g) * 16];
     }
+    const long long ps = src / c.page_size, pd = dst / c.page_size;
+    const long long ws = (ps * c.hkv + g) * c.page_size + (src - ps * c.page_size);
+    const long long wd = (pd * c.hkv + g) * c.page_size + (dst - pd * c.page_size);
+    float w = 0.f;
+    int pos = 0;
+    if (src >= 0 && c.weights) w = c.weights[ws];
+    if (src >= 0 && c.positions) pos = c.positions[ws];
+    const bool more = i + step < n;
+    long long nsrc = -1, ndst = -1;
+    if (more) entry(i + step, nsrc, ndst);  // the next entries arrive while these rows do
 #pragma unroll
     for (int m = 0; m < kMovesW; ++m) {
       const long long a = __shfl_sync(kFullMask, src, m), b = __shfl_sync(kFullMask, dst, m);
@@ -340,6 +407,9 @@ __global__ void __launch_bounds__(256) compact_kernel(const CompactParams p) {
     }
     if (src >= 0 && c.weights) c.weights[wd] = w;
     if (src >= 0 && c.positions) c.positions[wd] = pos;
+    if (!more) break;
+    src = nsrc;
+    dst = ndst;
   }
 }
 

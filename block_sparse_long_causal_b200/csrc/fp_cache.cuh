@@ -1,8 +1,6 @@
 // fp_cache.cuh -- what the key/value cache kernels share: the launch description of a cache, page
 // look-up and the per-launch tables that turn a work index into (sequence, unit).
 #pragma once
-#include <type_traits>
-
 #include "fp_dev.cuh"
 #include "fp_internal.h"
 #include "fp_seq.cuh"
@@ -14,9 +12,8 @@ namespace fp {
 // pdl_trigger, in the earlier kernel, allows the start (at its end without it).
 __device__ __forceinline__ void pdl_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
 __device__ __forceinline__ void pdl_trigger() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
-template <typename P>
-cudaError_t launch_pdl(void (*kernel)(P), dim3 grid, int threads, int smem, cudaStream_t st,
-                       const std::remove_const_t<P>& p) {
+template <typename... K, typename... A>
+cudaError_t launch_pdl(void (*kernel)(K...), dim3 grid, int threads, int smem, cudaStream_t st, const A&... args) {
   cudaLaunchAttribute at[1];
   at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   at[0].val.programmaticStreamSerializationAllowed = 1;
@@ -27,7 +24,7 @@ cudaError_t launch_pdl(void (*kernel)(P), dim3 grid, int threads, int smem, cuda
   cfg.stream = st;
   cfg.attrs = at;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, kernel, p);
+  return cudaLaunchKernelEx(&cfg, kernel, args...);
 }
 
 // Row of the cache that holds slot u of sequence s, or -1 when the block table points outside the

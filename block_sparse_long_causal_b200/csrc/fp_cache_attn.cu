@@ -455,89 +455,126 @@ __global__ void __launch_bounds__(256) cache_rows_weights_kernel(const __grid_co
   }
 }
 
-// Joins the pieces of the units that several CTAs share. Block (b, y) looks at the unit inside of which the
-// share of CTA b + 1 begins (meta) and works when that CTA is the first such of its unit: the pieces are
-// the last one of CTA b (place 1) and the first one (place 0) of every CTA up to meta[1]. 16 rows a block.
-// The time is one chain of dependent reads (meta, maxima, accumulators), so the pieces of a row are read
-// side by side: 32 maxima a warp at once, and where rows are few the warps share a row's pieces.
+// Joins the pieces of the units that several CTAs share. Entry b of meta describes the unit inside of which
+// the share of CTA b begins and is set for the first such CTA of a unit: the unit's pieces are then the last
+// one of CTA b - 1 (place 1) and the first one (place 0) of every CTA from b to meta[1].
+// The time is one chain of dependent reads (meta, maxima, accumulators), so the work is laid out flat: every
+// block lists the set entries, and the rows of all listed units go round the grid's warps, 32 maxima at
+// once; where there are fewer rows than warps, up to 16 warps of a block share a row's pieces.
+constexpr int kJoinWarps = 16, kJoinUnits = 512;
 template <bool kTiled>
-__global__ void __launch_bounds__(512) cache_join_kernel(const __grid_constant__ CacheAttnParams p) {
+__global__ void __launch_bounds__(32 * kJoinWarps) cache_join_kernel(const __grid_constant__ CacheAttnParams p, int ctas) {
   constexpr int kRowsU = kTiled ? 2 * kTileM : kRowsMax;  // rows of a piece
-  __shared__ float4 s_acc[16][32];
+  __shared__ float4 s_acc[kJoinWarps][32];
+  __shared__ int4 s_meta[kJoinUnits][2];  // set entries; word 0: the CTA
+  __shared__ int s_num[kJoinWarps];
   pdl_wait();
-  const int b = blockIdx.x + 1;
-  const int4 meta = *reinterpret_cast<const int4*>(p.meta + (long long)b * kMetaWords);
-  const int2 meta2 = *reinterpret_cast<const int2*>(p.meta + (long long)b * kMetaWords + 4);
-  if (meta.x == 0) return;
   const CacheInfo& c = p.c;
-  const int P = meta.y - b + 2, seq0 = meta.z, g = meta.w, G = c.group;
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  // meta2: first token and tokens of the sequence (tiled), first packed row and packed rows (not)
-  int wr = 1;  // warps that share a row
-  if (!kTiled)
-    while (wr < 16 && 16 / (2 * wr) >= meta2.y - meta2.x) wr *= 2;
-  const int row = blockIdx.y * 16 + warp / wr, slice = warp % wr;
-  int tok, head;
-  bool in;
-  if (kTiled) {
-    const int r = row & 127, TT = p.tile_tokens;
-    tok = meta2.x + (row >> 7) * TT + r / G;
-    head = r % G;
-    in = r < TT * G && tok < meta2.y;
-  } else {
-    const int pr = meta2.x + row;
-    tok = pr / G;
-    head = pr % G;
-    in = pr < meta2.y && row < kRowsU;
-  }
-  if (wr == 1 && !in) return;
-  auto place = [&](int k) { return (2ll * (b - 1 + k) + (k == 0)) * kRowsU + (in ? row : 0); };
-  auto ml_of = [&](int k) {
-    return k < P ? *reinterpret_cast<const float2*>(p.part_ml + 2 * place(k)) : make_float2(-INFINITY, 0.f);
-  };
-  float m = -INFINITY;
-  for (int k = lane; k < P; k += 32) m = fmaxf(m, ml_of(k).x);
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, G = c.group;
+  // the most rows that a piece of this call can have
+  const int rows = kTiled ? (c.max_new > p.tile_tokens ? kRowsU : kTileM) : min(kRowsU, c.max_new * G);
+  for (int b0 = 0; b0 < ctas; b0 += kJoinUnits) {  // one round on devices of up to 256 SMs
+    __syncthreads();
+    int4 e0 = make_int4(0, 0, 0, 0), e1 = e0;
+    if (b0 + tid < ctas) {
+      const int4* src = reinterpret_cast<const int4*>(p.meta + (long long)(b0 + tid) * kMetaWords);
+      e0 = __ldcg(src);
+      e1 = __ldcg(src + 1);
+    }
+    const unsigned set = __ballot_sync(kAll, e0.x != 0);
+    if (lane == 0) s_num[warp] = __popc(set);
+    __syncthreads();
+    int at = __popc(set & ((1u << lane) - 1u)), num = 0;
 #pragma unroll
-  for (int o = 16; o >= 1; o >>= 1) m = fmaxf(m, __shfl_xor_sync(kAll, m, o));
-  const float mu = m == -INFINITY ? 0.f : m;
-  float l = 0.f;
-  float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-  for (int k0 = 0; k0 < P; k0 += 32) {
-    const float2 ml = ml_of(k0 + lane);
-    const float w = ml.y != 0.f ? ex2_approx(ml.x - mu) : 0.f;  // sum 0: nothing of the row in this piece
-    if (ml.y != 0.f) l += w * ml.y;
-    const unsigned use = __ballot_sync(kAll, ml.y != 0.f);      // its O may be unwritten
-    const int top = min(32, P - k0);
+    for (int w = 0; w < kJoinWarps; ++w) {
+      const int x = s_num[w];
+      at += w < warp ? x : 0;
+      num += x;
+    }
+    if (e0.x != 0) {
+      e0.x = b0 + tid;
+      s_meta[at][0] = e0;
+      s_meta[at][1] = e1;
+    }
+    __syncthreads();
+    if (num == 0) continue;
+    const int tasks = num * rows;
+    int wr = 1;  // warps that share a row
+    while (wr < kJoinWarps && 2ll * wr * tasks <= (long long)gridDim.x * kJoinWarps) wr *= 2;
+    const int per = kJoinWarps / wr, slice = warp % wr;  // rows a block takes at a time
+    for (int task0 = blockIdx.x * per; task0 < tasks; task0 += gridDim.x * per) {
+      const int task = task0 + warp / wr;
+      const int row = task / num, unit = task < tasks ? task - row * num : 0;
+      const int4 meta = s_meta[unit][0], meta2 = s_meta[unit][1];
+      // meta2: first token and tokens of the sequence (tiled), first packed row and packed rows (not)
+      const int b = meta.x, P = meta.y - b + 2, seq0 = meta.z, g = meta.w;
+      int tok, head;
+      bool in = task < tasks;
+      if (kTiled) {
+        const int r = row & 127, TT = p.tile_tokens;
+        tok = meta2.x + (row >> 7) * TT + r / G;
+        head = r % G;
+        in = in && r < TT * G && tok < meta2.y;
+      } else {
+        const int pr = meta2.x + row;
+        tok = pr / G;
+        head = pr % G;
+        in = in && pr < meta2.y;
+      }
+      float l = 0.f, mu = 0.f;
+      float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+      if (in) {
+        auto place = [&](int k) { return (2ll * (b - 1 + k) + (k == 0)) * kRowsU + row; };
+        auto ml_of = [&](int k) {
+          return k < P ? __ldcg(reinterpret_cast<const float2*>(p.part_ml + 2 * place(k))) : make_float2(-INFINITY, 0.f);
+        };
+        const float2 ml0 = ml_of(lane);
+        float m = ml0.x;
+        for (int k = lane + 32; k < P; k += 32) m = fmaxf(m, ml_of(k).x);
+#pragma unroll
+        for (int o = 16; o >= 1; o >>= 1) m = fmaxf(m, __shfl_xor_sync(kAll, m, o));
+        mu = m == -INFINITY ? 0.f : m;
+        for (int k0 = 0; k0 < P; k0 += 32) {
+          const float2 ml = k0 == 0 ? ml0 : ml_of(k0 + lane);
+          const float w = ml.y != 0.f ? ex2_approx(ml.x - mu) : 0.f;  // sum 0: nothing of the row in this piece
+          if (ml.y != 0.f) l += w * ml.y;
+          const unsigned use = __ballot_sync(kAll, ml.y != 0.f);      // its O may be unwritten
+          const int top = min(32, P - k0);
 #pragma unroll 8
-    for (int j = slice; j < top; j += wr) {
-      const float wj = __shfl_sync(kAll, w, j);
-      if ((use >> j) & 1) {
-        const float4 a = __ldcg(reinterpret_cast<const float4*>(p.part_o + place(k0 + j) * kHeadDim) + lane);
-        acc.x += wj * a.x; acc.y += wj * a.y; acc.z += wj * a.z; acc.w += wj * a.w;
+          for (int j = slice; j < top; j += wr) {
+            const float wj = __shfl_sync(kAll, w, j);
+            if ((use >> j) & 1) {
+              const float4 a = __ldcg(reinterpret_cast<const float4*>(p.part_o + place(k0 + j) * kHeadDim) + lane);
+              acc.x += wj * a.x; acc.y += wj * a.y; acc.z += wj * a.z; acc.w += wj * a.w;
+            }
+          }
+        }
+#pragma unroll
+        for (int o = 16; o >= 1; o >>= 1) l += __shfl_xor_sync(kAll, l, o);
+      }
+      if (wr > 1) {
+        s_acc[warp][lane] = acc;
+        __syncthreads();
+        if (slice == 0)
+          for (int q = 1; q < wr; ++q) {
+            const float4 a = s_acc[warp + q][lane];
+            acc.x += a.x; acc.y += a.y; acc.z += a.z; acc.w += a.w;
+          }
+        __syncthreads();
+      }
+      if (!in || slice != 0) continue;
+      const bool any = l > 0.f || l != l;
+      const float inv = any ? 1.f / l : 0.f;
+      const long long t = (long long)seq0 + tok;
+      const int h = g * G + head;
+      *reinterpret_cast<uint2*>(p.out + (t * c.hq + h) * kHeadDim + lane * 4) =
+          make_uint2(pack_bf16x2(acc.x * inv, acc.y * inv), pack_bf16x2(acc.z * inv, acc.w * inv));
+      if (lane == 0) {
+        const float z = any ? mu + log2f(l) : -INFINITY;
+        if (p.lse2) p.lse2[(long long)h * c.total_tokens + t] = z;
+        if (p.lse) p.lse[(long long)h * c.total_tokens + t] = z * 0.6931471805599453f;
       }
     }
-  }
-#pragma unroll
-  for (int o = 16; o >= 1; o >>= 1) l += __shfl_xor_sync(kAll, l, o);
-  if (wr > 1) {
-    s_acc[warp][lane] = acc;
-    __syncthreads();
-    if (slice != 0 || !in) return;
-    for (int q = 1; q < wr; ++q) {
-      const float4 a = s_acc[warp + q][lane];
-      acc.x += a.x; acc.y += a.y; acc.z += a.z; acc.w += a.w;
-    }
-  }
-  const bool any = l > 0.f || l != l;
-  const float inv = any ? 1.f / l : 0.f;
-  const long long t = (long long)seq0 + tok;
-  const int h = g * G + head;
-  *reinterpret_cast<uint2*>(p.out + (t * c.hq + h) * kHeadDim + lane * 4) =
-      make_uint2(pack_bf16x2(acc.x * inv, acc.y * inv), pack_bf16x2(acc.z * inv, acc.w * inv));
-  if (lane == 0) {
-    const float z = any ? mu + log2f(l) : -INFINITY;
-    if (p.lse2) p.lse2[(long long)h * c.total_tokens + t] = z;
-    if (p.lse) p.lse[(long long)h * c.total_tokens + t] = z * 0.6931471805599453f;
   }
 }
 
@@ -566,13 +603,13 @@ CacheAttnLayout cache_attn_layout(int sms, bool tiled, const CacheInfo& c, bool 
 
 // Every kernel of a call asks for the same split of the SM's memory (the largest shared part): between
 // kernels that differ in it the SM has to drain first, which costs microseconds.
-cudaError_t launch_cache_join(const CacheAttnParams& p, bool tiled, int ctas, cudaStream_t st) {
+cudaError_t launch_cache_join(const CacheAttnParams& p, bool tiled, int ctas, int sms, cudaStream_t st) {
   if (ctas < 2) return cudaSuccess;
-  void (*fn)(const CacheAttnParams) = tiled ? cache_join_kernel<true> : cache_join_kernel<false>;
+  void (*fn)(const CacheAttnParams, int) = tiled ? cache_join_kernel<true> : cache_join_kernel<false>;
   static unsigned long long attr[2][kMaxCachedDevices] = {};
   const cudaError_t e = set_max_smem(reinterpret_cast<const void*>(fn), 0, attr[tiled], true);
   if (e != cudaSuccess) return e;
-  return launch_pdl(fn, dim3(ctas - 1, tiled ? 16 : 1), 512, 0, st, p);
+  return launch_pdl(fn, dim3(tiled ? 2 * sms : sms), 32 * kJoinWarps, 0, st, p, ctas);
 }
 
 cudaError_t launch_cache_attn(const CacheAttnParams& p, bool tiled, int sms, cudaStream_t st) {
@@ -586,7 +623,7 @@ cudaError_t launch_cache_attn(const CacheAttnParams& p, bool tiled, int sms, cud
   void (*fn)(const CacheAttnParams) = nt == 1 ? cache_rows_kernel<1> : cache_rows_kernel<2>;
   if ((e = set_max_smem(reinterpret_cast<const void*>(fn), kRowSmem, attr[nt - 1], true)) != cudaSuccess) return e;
   if ((e = launch_pdl(fn, dim3(grid), kRowThreads, kRowSmem, st, p)) != cudaSuccess) return e;
-  if ((e = launch_cache_join(p, false, grid, st)) != cudaSuccess || !(p.decay >= 0.f)) return e;
+  if ((e = launch_cache_join(p, false, grid, sms, st)) != cudaSuccess || !(p.decay >= 0.f)) return e;
   if ((e = set_max_smem(reinterpret_cast<const void*>(cache_rows_weights_kernel), 0, attr[2], true)) != cudaSuccess)
     return e;
   return launch_pdl(cache_rows_weights_kernel, dim3(4 * sms), 256, 0, st, p);

@@ -22,7 +22,7 @@ constexpr unsigned kAll = 0xffffffffu;
 constexpr int kBK = 128;                  // keys of a tile
 constexpr int kStages = 2;                // K ring and V ring
 constexpr int kUnitRing = 4;
-constexpr int kUnitReaders = 9;           // the MMA warp and the 8 softmax warps
+constexpr int kUnitReaders = 10;          // the MMA warp, the tail warp and the 8 softmax warps
 constexpr int kRegsCtl = 104, kRegsSoftmax = 200;
 static_assert(128 * kRegsCtl + 256 * kRegsSoftmax == kThreads * 168, "register split must equal the launch allocation");
 constexpr uint64_t kDrainLimitNs = 1000000000ull;
@@ -30,8 +30,8 @@ constexpr float kFastSumLimit = 65536.f;  // largest row sum that an item withou
 constexpr uint32_t kTile = 128 * 128 * 2, kSlab = 128 * 128;
 constexpr uint32_t kOffQ = 0, kOffK = 2 * kTile, kOffV = kOffK + kStages * kTile, kOffBar = kOffV + kStages * kTile;
 // q_full, q_empty, k_full[], k_empty[], v_full[], v_empty[], s_full[2], p_full[2], o_final[2], x_full, x_done,
-// drain, unit_full[], unit_empty[]
-constexpr int kNumBars = 2 + 4 * kStages + 6 + 3 + 2 * kUnitRing;
+// drain, v_tail[], unit_full[], unit_empty[]
+constexpr int kNumBars = 2 + 4 * kStages + 6 + 3 + kStages + 2 * kUnitRing;
 constexpr uint32_t kOffMisc = kOffBar + kNumBars * 8;                   // tmem base, abort flag, bad flag
 constexpr uint32_t kOffScan = (kOffMisc + 16 + 15) & ~15u;              // int64[12]; the line's start (5 int64)
 constexpr uint32_t kOffUnit = kOffScan + 8 * 12 + 8 * 6;                // unit descriptors
@@ -74,9 +74,9 @@ __device__ __forceinline__ Unit decode(const CacheInfo& c, const long long* tab,
   u.m = pairs - 1 - (local - u.g * pairs);
   return u;
 }
-__device__ __forceinline__ long long gcd64(long long a, long long b) {
+__device__ __forceinline__ unsigned gcd32(unsigned a, unsigned b) {
   while (b) {
-    const long long t = a % b;
+    const unsigned t = a % b;
     a = b;
     b = t;
   }
@@ -85,11 +85,14 @@ __device__ __forceinline__ long long gcd64(long long a, long long b) {
 // The line's i-th unit. A CTA's part covers about N / ctas units in a row, so unit i is reached after the
 // fraction i * ctas / N (mod 1) of the run; ranking the units by that fraction gives the CTAs that
 // run at the same time neighbouring units of the kv-head order. d = gcd(ctas, N): i and i + N / d have
-// the same fraction and follow one another.
-__device__ __forceinline__ long long unit_at(long long i, long long N, int ctas, long long d) {
-  if (N <= ctas) return i;
-  return i * ctas % N + i / (N / d);
+// the same fraction and follow one another. (Calls of more units than that keep the kv-head order.)
+constexpr long long kOrderMax = 1 << 22;
+__device__ __forceinline__ long long unit_at(long long i, long long N, unsigned ctas, unsigned d) {
+  if (N <= ctas || N > kOrderMax) return i;
+  return (unsigned)i * ctas % (unsigned)N + (unsigned)i / ((unsigned)N / d);
 }
+// What a unit weighs on the line: its key tiles and what beginning and ending it costs, in key tiles.
+constexpr int kUnitCost = 3;
 
 __device__ __forceinline__ void tma_load_3d(uint32_t dst, const void* tmap, uint32_t bar, int x, int y, int z) {
   asm volatile(
@@ -110,8 +113,9 @@ __global__ void __launch_bounds__(kThreads, 1) cache_tiles_kernel(const __grid_c
   auto b_v_empty = [&](int i) { return bar0 + 16 + 8 * (3 * kStages + i); };
   const uint32_t b_s_full0 = bar0 + 16 + 32 * kStages, b_p_full0 = b_s_full0 + 16, b_o_final0 = b_p_full0 + 16;
   const uint32_t b_x_full = b_o_final0 + 16, b_x_done = b_x_full + 8, b_drain = b_x_done + 8;
-  auto b_u_full = [&](uint32_t i) { return b_drain + 8 + 8 * (i % kUnitRing); };
-  auto b_u_empty = [&](uint32_t i) { return b_drain + 8 + 8 * (kUnitRing + i % kUnitRing); };
+  auto b_v_tail = [&](int i) { return b_drain + 8 + 8 * i; };
+  auto b_u_full = [&](uint32_t i) { return b_drain + 8 + 8 * (kStages + i % kUnitRing); };
+  auto b_u_empty = [&](uint32_t i) { return b_drain + 8 + 8 * (kStages + kUnitRing + i % kUnitRing); };
   uint32_t* s_tmem = reinterpret_cast<uint32_t*>(smem + kOffMisc);
   volatile int* s_abort = reinterpret_cast<volatile int*>(smem + kOffMisc + 4);
   int* s_bad = reinterpret_cast<int*>(smem + kOffMisc + 8);
@@ -131,6 +135,7 @@ __global__ void __launch_bounds__(kThreads, 1) cache_tiles_kernel(const __grid_c
       mbar_init(b_k_empty(i), 1);
       mbar_init(b_v_full(i), 1);
       mbar_init(b_v_empty(i), 1);
+      mbar_init(b_v_tail(i), 1);
     }
     for (int k = 0; k < 2; ++k) {
       mbar_init(b_s_full0 + 8 * k, 1);
@@ -154,12 +159,13 @@ __global__ void __launch_bounds__(kThreads, 1) cache_tiles_kernel(const __grid_c
     tmem_alloc(smem_u32(s_tmem), 512);
     tmem_relinquish();
   }
+  pdl_wait();
   const bool ok = cache_table<kThreads>(c, tab, s_scan, s_bad, p.dev_status, [&](int, int L, int) -> long long {
     return (long long)c.hkv * (((L + TT - 1) / TT + 1) / 2);
   });
   const long long N = ok ? tab[c.num_seqs] : 0;
   // ---- this CTA's part [x0, x1) of the line, and the unit that x0 falls into
-  const long long d = N > 0 ? gcd64(N, gridDim.x) : 1;
+  const unsigned d = N > gridDim.x && N <= kOrderMax ? gcd32((unsigned)N, gridDim.x) : 1u;
   long long x0 = 0, x1 = 0;
   int ctas = 0;
   {
@@ -167,7 +173,7 @@ __global__ void __launch_bounds__(kThreads, 1) cache_tiles_kernel(const __grid_c
     long long sum = 0;
     for (long long i = a; i < b; ++i) {
       const Unit u = decode(c, tab, TT, unit_at(i, N, gridDim.x, d));
-      sum += key_tiles(u, (2 * u.m + 2) * TT);
+      sum += key_tiles(u, (2 * u.m + 2) * TT) + kUnitCost;
     }
     const long long incl = warp_incl_scan(sum);
     __syncthreads();  // cache_table is done with the scratch
@@ -187,12 +193,12 @@ __global__ void __launch_bounds__(kThreads, 1) cache_tiles_kernel(const __grid_c
         for (long long i = a; i < b; ++i) {
           const Unit u = decode(c, tab, TT, unit_at(i, N, gridDim.x, d));
           const int kts = key_tiles(u, (2 * u.m + 2) * TT);
-          if (x0 < base + kts) {
+          if (x0 < base + kts + kUnitCost) {
             s_start[0] = i;
             s_start[1] = x0 - base;
             int32_t* meta = p.meta + (long long)me * kMetaWords;
             // a part that begins inside a unit: the first such CTA of the unit has the pieces joined
-            const bool inside = x0 > base;
+            const bool inside = x0 > base && x0 < base + kts;
             meta[0] = inside && T * (me - 1) / ctas <= base;
             if (inside) {
               int last = me;  // the last CTA whose part begins inside the unit
@@ -205,7 +211,7 @@ __global__ void __launch_bounds__(kThreads, 1) cache_tiles_kernel(const __grid_c
             }
             break;
           }
-          base += kts;
+          base += kts + kUnitCost;
         }
       }
     } else if (tid == 0) {
@@ -237,18 +243,19 @@ __global__ void __launch_bounds__(kThreads, 1) cache_tiles_kernel(const __grid_c
     for (long long x = x0; x < x1 && !fail; ++i, kt = 0) {
       const Unit u = decode(c, tab, TT, unit_at(i, N, gridDim.x, d));
       Piece pc;
+      pc.kts = key_tiles(u, (2 * u.m + 2) * TT);
+      pc.kt0 = kt;
+      pc.kt1 = (int)min((long long)pc.kts, kt + (x1 - x));
+      x += pc.kts + kUnitCost - kt;
+      if (pc.kt0 >= pc.kts) continue;  // the part begins in what ending the unit costs
       pc.seq0 = u.seq0;
       pc.L = u.L;
       pc.len = u.len;
       pc.g = u.g;
       pc.tok0 = 2 * u.m * TT;
       pc.nslot = pc.tok0 + TT < u.L ? 2 : 1;
-      pc.kts = key_tiles(u, (2 * u.m + 2) * TT);
       pc.kts0 = key_tiles(u, (2 * u.m + 1) * TT);
-      pc.kt0 = kt;
-      pc.kt1 = (int)min((long long)pc.kts, kt + (x1 - x));
       pc.slot = kt == 0 && pc.kt1 == pc.kts ? -1 : 2 * (int)blockIdx.x + (kt == 0 ? 1 : 0);
-      x += pc.kt1 - kt;
       if (uc >= kUnitRing && !all_wait(b_u_empty(uc), ((uc / kUnitRing) - 1) & 1)) { fail = true; break; }
       if (lane == 0) {
         *unit_entry(uc) = pc;
@@ -281,10 +288,11 @@ __global__ void __launch_bounds__(kThreads, 1) cache_tiles_kernel(const __grid_c
           tma_load_2d(dst + kSlab + lane * bh * 128, tm, full, u.g * kHeadDim + 64, row);
         }
       };
-      auto load_v = [&](int row) -> bool {
+      // a tile that reaches past the sequence's last slot goes to the tail warp first
+      auto load_v = [&](int t, int row) -> bool {
         const int vs = vit % kStages;
         if (!all_wait(b_v_empty(vs), ((vit / kStages) & 1) ^ 1)) return false;
-        load(sV + vs * kTile, &p.tm_v, b_v_full(vs), row);
+        load(sV + vs * kTile, &p.tm_v, (t + 1) * kBK > n ? b_v_tail(vs) : b_v_full(vs), row);
         ++vit;
         return true;
       };
@@ -296,12 +304,12 @@ __global__ void __launch_bounds__(kThreads, 1) cache_tiles_kernel(const __grid_c
         if (!all_wait(b_k_empty(ks), ((kit / kStages) & 1) ^ 1)) { fail = true; break; }
         load(sK + ks * kTile, &p.tm_k, b_k_full(ks), row);
         ++kit;
-        if (t > pc.kt0 && !load_v(vrow)) { fail = true; break; }
+        if (t > pc.kt0 && !load_v(t - 1, vrow)) { fail = true; break; }
         vrow = row;
         row = next;
         if (*s_abort) { fail = true; break; }
       }
-      if (!fail && !load_v(vrow)) fail = true;
+      if (!fail && !load_v(pc.kt1 - 1, vrow)) fail = true;
     }
     if (!fail && uc >= kUnitRing && !all_wait(b_u_empty(uc), ((uc / kUnitRing) - 1) & 1)) fail = true;
     if (!fail && lane == 0) {
@@ -334,23 +342,12 @@ __global__ void __launch_bounds__(kThreads, 1) cache_tiles_kernel(const __grid_c
       if (pc.seq0 < 0) break;
       if (!all_wait(b_q_full, uc & 1)) { fail = true; break; }
       tc_fence_after();
-      const int n = pc.len + pc.L;
-      int prev_part = 0, prev_t = 0;
+      int prev_part = 0;
       bool had_pv[2] = {false, false};
-      auto pv = [&](int k, bool fix) -> bool {  // O_k += P_k V of tile prev_t
+      auto pv = [&](int k) -> bool {  // O_k += P_k V of the tile before
         if (!all_wait(b_p_full0 + 8 * k, (cnt[k] - 1) & 1)) return false;
         const int vs = vit % kStages;
         if (!all_wait(b_v_full(vs), (vit / kStages) & 1)) return false;
-        const int live = n - prev_t * kBK;
-        if (fix && live < kBK) {
-          // slots past the sequence's end may hold anything, and 0 * NaN is NaN: their V rows become zeros
-          for (int e = live * 8 + lane; e < kBK * 8; e += 32) {
-            *reinterpret_cast<uint4*>(smem + kOffV + vs * kTile + e * 16) = make_uint4(0, 0, 0, 0);
-            *reinterpret_cast<uint4*>(smem + kOffV + vs * kTile + kSlab + e * 16) = make_uint4(0, 0, 0, 0);
-          }
-          asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
-          __syncwarp();
-        }
         tc_fence_after();
         if (lane == 0) {
           const uint64_t vdesc = sdesc_sw128(sV + vs * kTile, kSlab, 1024);
@@ -389,7 +386,7 @@ __global__ void __launch_bounds__(kThreads, 1) cache_tiles_kernel(const __grid_c
 #pragma unroll
         for (int k = 0; k < 2; ++k)
           if (!fail && ((prev_part >> k) & 1)) {
-            if (!pv(k, k == 0 || !(prev_part & 1))) { fail = true; break; }
+            if (!pv(k)) { fail = true; break; }
             if ((part >> k) & 1) qk(k, kbase);
           }
         if (fail) break;
@@ -403,14 +400,13 @@ __global__ void __launch_bounds__(kThreads, 1) cache_tiles_kernel(const __grid_c
         }
         ++kit;
         prev_part = part;
-        prev_t = t;
         if (*s_abort) { fail = true; break; }
       }
       if (fail) break;
 #pragma unroll
       for (int k = 0; k < 2; ++k)
         if (!fail && ((prev_part >> k) & 1))
-          if (!pv(k, k == 0 || !(prev_part & 1))) fail = true;
+          if (!pv(k)) fail = true;
       if (fail) break;
       if (lane == 0) {
         mma_commit(b_v_empty(vit % kStages));
@@ -426,6 +422,40 @@ __global__ void __launch_bounds__(kThreads, 1) cache_tiles_kernel(const __grid_c
       }
       mma_commit(b_drain);  // every issued product completes before TMEM is released
       mbar_wait(b_drain, 0, kDrainLimitNs);
+    }
+    __syncwarp();
+  } else if (warp == 3) {
+    // =========================================================== V rows behind a sequence's last slot
+    // They may hold anything, and 0 * NaN is NaN: they become zeros before the product reads them.
+    uint32_t vit = 0, tails[2] = {0, 0};
+    static_assert(kStages == 2, "tail barriers' phases");
+    bool fail = false;
+    auto all_wait = [&](uint32_t bar, uint32_t parity) {
+      return __all_sync(kAll, mbar_wait(bar, parity, p.wait_limit_ns));
+    };
+    for (uint32_t uc = 0; !fail; ++uc) {
+      if (!all_wait(b_u_full(uc), (uc / kUnitRing) & 1)) { fail = true; break; }
+      const Piece pc = *unit_entry(uc);
+      __syncwarp();
+      if (lane == 0) mbar_arrive(b_u_empty(uc));
+      if (pc.seq0 < 0) break;
+      vit += pc.kt1 - pc.kt0;
+      const int live = pc.len + pc.L - (pc.kt1 - 1) * kBK;
+      if (live >= kBK) continue;
+      const int vs = (vit - 1) % kStages;
+      const uint32_t phase = vs ? tails[1]++ : tails[0]++;
+      if (!all_wait(b_v_tail(vs), phase & 1)) { fail = true; break; }
+      for (int e = live * 8 + lane; e < kBK * 8; e += 32) {
+        *reinterpret_cast<uint4*>(smem + kOffV + vs * kTile + e * 16) = make_uint4(0, 0, 0, 0);
+        *reinterpret_cast<uint4*>(smem + kOffV + vs * kTile + kSlab + e * 16) = make_uint4(0, 0, 0, 0);
+      }
+      asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+      __syncwarp();
+      if (lane == 0) mbar_arrive(b_v_full(vs));
+    }
+    if (fail && lane == 0) {
+      *s_abort = 1;
+      dev_flag(p.dev_status, kDevTimeout);
     }
     __syncwarp();
   } else if (wg >= 1) {
@@ -678,9 +708,9 @@ cudaError_t launch_cache_tiles(const CacheAttnParams& p, int sms, cudaStream_t s
   static unsigned long long attr[kMaxCachedDevices] = {};
   cudaError_t e = set_max_smem(reinterpret_cast<const void*>(tiles::cache_tiles_kernel), tiles::smem_bytes(kMaxSeqs), attr);
   if (e != cudaSuccess) return e;
-  tiles::cache_tiles_kernel<<<sms, tiles::kThreads, tiles::smem_bytes(p.c.num_seqs), st>>>(p);
-  if ((e = cudaGetLastError()) != cudaSuccess || sms < 2) return e;
-  return launch_cache_join(p, true, sms, st);
+  e = launch_pdl(tiles::cache_tiles_kernel, dim3(sms), tiles::kThreads, tiles::smem_bytes(p.c.num_seqs), st, p);
+  if (e != cudaSuccess) return e;
+  return launch_cache_join(p, true, sms, sms, st);
 }
 
 }  // namespace fp

@@ -313,20 +313,24 @@ __global__ void __launch_bounds__(kThreads, 1) cache_tiles_weights_kernel(const 
   } else if (warp == 2) {
     // =========================================================== -lse2 of the row tiles
     uint32_t it = 0;
+    int tok_r[4], head_r[4];
+    for (int j = 0; j < 4; ++j) {
+      tok_r[j] = (lane + 32 * j) / G;
+      head_r[j] = (lane + 32 * j) % G;
+    }
     for (long long x = x0; x < x1; ++x, ++it) {
       float z[4];
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
-        const int r = lane + 32 * j, tok = u.rt * TT + r / G;
-        const bool in = r < TT * G && tok < u.L;
-        z[j] = in ? -__ldcg(p.lse2 + (long long)(u.g * G + r % G) * c.total_tokens + u.seq0 + tok) : -INFINITY;
+        const int tok = u.rt * TT + tok_r[j];
+        const bool in = tok_r[j] < TT && tok < u.L;
+        z[j] = in ? -__ldcg(p.lse2 + (long long)(u.g * G + head_r[j]) * c.total_tokens + u.seq0 + tok) : -INFINITY;
       }
       if (it >= kS && !all_wait(b_s_empty(it), ((it / kS) - 1) & 1)) { fail = true; break; }
 #pragma unroll
       for (int j = 0; j < 4; ++j) s_z[it % kS * 128 + lane + 32 * j] = z[j];
       mbar_arrive(b_z_full(it));
       step_next(u, c, TT, x + 1 < x1);
-      if (__any_sync(kAll, *s_abort)) { fail = true; break; }
     }
     if (fail && lane == 0) {
       *s_abort = 1;
@@ -341,7 +345,16 @@ __global__ void __launch_bounds__(kThreads, 1) cache_tiles_weights_kernel(const 
     uint32_t it = 0, xc = 0;
     uint64_t acc[4] = {0ull, 0ull, 0ull, 0ull};
     bool first_part = x0 < x1 && u.rt > u.rt0;  // the share begins inside a key tile's steps
+    bool fresh = true;
+    long long at = -1;  // this thread's weight, looked up (and read) while the tile's first step is under way
+    float old = 0.f;
     for (long long x = x0; x < x1; ++x, ++it) {
+      if (fresh) {
+        fresh = false;
+        const int key = u.kt * kBK + r;
+        at = key < u.n && half == (int)(xc & 1) ? slot_word(c, u.s, u.g, key) : -1;
+        old = at >= 0 && p.decay > 0.f ? c.weights[at] : 0.f;
+      }
       if (!all_wait(b_z_full(it), (it / kS) & 1) || !all_wait(b_s_full(it), (it / kS) & 1)) { fail = true; break; }
       tc_fence_after();
       const float* z = s_z + it % kS * 128 + 64 * half;
@@ -381,7 +394,6 @@ __global__ void __launch_bounds__(kThreads, 1) cache_tiles_weights_kernel(const 
       }
       tc_fence_before();
       mbar_arrive(b_s_empty(it));
-      const int g = u.g, kt = u.kt, s = u.s;
       const bool ends = u.rt + 1 == u.R;
       if (ends || x + 1 == x1) {
         float a0, a1, b0, b1;
@@ -389,27 +401,26 @@ __global__ void __launch_bounds__(kThreads, 1) cache_tiles_weights_kernel(const 
         f2_split(fadd2(acc[2], acc[3]), b0, b1);
         float w = (a0 + a1) + (b0 + b1);
         acc[0] = acc[1] = acc[2] = acc[3] = 0ull;
-        if (half == 1) {
+        if (half != (int)(xc & 1)) {  // the warpgroups take turns in handing over and in writing
           if (xc >= 2 && !all_wait(b_x_empty(xc), ((xc / 2) - 1) & 1)) { fail = true; break; }
           s_x[xc % 2 * 128 + r] = w;
           mbar_arrive(b_x_full(xc));
         } else {
           if (!all_wait(b_x_full(xc), (xc / 2) & 1)) { fail = true; break; }
-          w += s_x[xc % 2 * 128 + r];
+          const float v = s_x[xc % 2 * 128 + r];
+          w = half == 0 ? w + v : v + w;
           mbar_arrive(b_x_empty(xc));
           if (ends && !first_part) {
-            const int key = kt * kBK + r;
-            const long long at = key < u.n ? slot_word(c, s, g, key) : -1;
-            if (at >= 0) c.weights[at] = p.decay > 0.f ? fmaf(p.decay, c.weights[at], w) : w;
+            if (at >= 0) c.weights[at] = p.decay > 0.f ? fmaf(p.decay, old, w) : w;
           } else {
             p.part_ml[(2ll * me + (first_part ? 0 : 1)) * 128 + r] = w;
           }
         }
         first_part = false;
         ++xc;
+        fresh = true;
       }
       step_next(u, c, TT, x + 1 < x1);
-      if (__any_sync(kAll, *s_abort)) { fail = true; break; }
     }
     if (fail) {
       *s_abort = 1;

@@ -222,7 +222,7 @@ cudaError_t launch_cache_attn(const CacheAttnParams& p, bool tiled, int sms, cud
 cudaError_t launch_cache_tiles(const CacheAttnParams& p, int sms, cudaStream_t st);
 cudaError_t launch_cache_weights(const CacheAttnParams& p, int sms, cudaStream_t st);
 // Joins the pieces of the units that several of `ctas` CTAs shared.
-cudaError_t launch_cache_join(const CacheAttnParams& p, bool tiled, int ctas, cudaStream_t st);
+cudaError_t launch_cache_join(const CacheAttnParams& p, bool tiled, int ctas, int sms, cudaStream_t st);
 cudaError_t launch_exp2_selftest(const float* x, float* y_poly, float* y_mufu, long long n, cudaStream_t st);
 
 }  // namespace fp
