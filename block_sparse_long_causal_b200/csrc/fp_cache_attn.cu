@@ -28,7 +28,7 @@ constexpr int kRowsMax = 16;                // rows of a unit
 constexpr int kKeysW = 16;                  // keys of a tile per warp
 constexpr int kWarps = 4, kRowThreads = 32 * kWarps;
 constexpr int kKeysT = kKeysW * kWarps;     // keys of a tile
-constexpr int kStages = 3;
+constexpr int kStages = 2, kCtasSm = 3;     // 12 warps an SM: fewer leave its schedulers waiting (see below)
 constexpr int kStageBytes = 2 * kKeysW * kHeadDim * 2;  // K then V of one warp's 16 keys
 constexpr int kOffMl = kWarps * kStages * kStageBytes;  // float m[warp][16], l[warp][16]
 constexpr int kRowSmem = kOffMl + 2 * kWarps * kRowsMax * 4;
@@ -154,8 +154,8 @@ __device__ __forceinline__ bool find_share(const CacheInfo& c, Shares& sh, Curso
 }
 
 template <int NT>
-__global__ void __launch_bounds__(kRowThreads, 2) cache_rows_kernel(const __grid_constant__ CacheAttnParams p) {
-  extern __shared__ __align__(128) unsigned char smem[];
+__global__ void __launch_bounds__(kRowThreads, kCtasSm) cache_rows_kernel(const __grid_constant__ CacheAttnParams p) {
+  extern __shared__ __align__(1024) unsigned char smem[];
   pdl_wait();
   const CacheInfo& c = p.c;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
@@ -192,6 +192,12 @@ __global__ void __launch_bounds__(kRowThreads, 2) cache_rows_kernel(const __grid
   };
   long long row0 = row_of(ld);
   int put = 0;
+  // a lane copies 16 bytes of rows lane / 16, + 2, ...; its places in a stage (128-byte swizzle)
+  const long long lane_off = (long long)(lane >> 4) * c.hkv * kHeadDim + (lane & 15) * 8;
+  const long long row_step = 2ll * c.hkv * kHeadDim;
+  uint32_t put_off[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) put_off[i] = (lane >> 4) * 256 + (((lane & 15) ^ (2 * i + (lane >> 4))) << 4);
   auto load = [&](long long x) {
     if (x < x1) {
       const uint32_t st = ring + (uint32_t)put * kStageBytes;
@@ -200,14 +206,25 @@ __global__ void __launch_bounds__(kRowThreads, 2) cache_rows_kernel(const __grid
       if (key0 < ld.n && row0 < 0 && lane == 0) dev_flag(p.dev_status, kDevBadProblem);
       // a bad page and the slots past the sequence's end read as zeros
       const int live = row0 < 0 ? 0 : min(kKeysW, ld.n - key0);
-      const long long base = ((row0 < 0 ? 0 : row0) * c.hkv + ld.g) * kHeadDim + (lane & 15) * 8;
+      const long long base = ((row0 < 0 ? 0 : row0) * c.hkv + ld.g) * kHeadDim;
+      if (live == kKeysW) {
+        const uint16_t *ks = c.k + base + lane_off, *vs = c.v + base + lane_off;
 #pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        const int r = 2 * i + (lane >> 4);
-        const long long off = r < live ? base + (long long)r * c.hkv * kHeadDim : 0;
-        const uint32_t d = st + r * 256 + (((lane & 15) ^ (r & 7)) << 4);
-        cp_async16(d, c.k + off, r < live);
-        cp_async16(d + kKeysW * 256, c.v + off, r < live);
+        for (int i = 0; i < 8; ++i) {
+          cp_async16(st + i * 512 + put_off[i & 3], ks, true);
+          cp_async16(st + i * 512 + put_off[i & 3] + kKeysW * 256, vs, true);
+          ks += row_step;
+          vs += row_step;
+        }
+      } else {
+#pragma unroll 1
+        for (int i = 0; i < 8; ++i) {
+          const int r = 2 * i + (lane >> 4);
+          const long long off = r < live ? base + (long long)r * c.hkv * kHeadDim + (lane & 15) * 8 : 0;
+          const uint32_t d = st + r * 256 + (((lane & 15) ^ (r & 7)) << 4);
+          cp_async16(d, c.k + off, r < live);
+          cp_async16(d + kKeysW * 256, c.v + off, r < live);
+        }
       }
       cursor_next(ld, c, x + 1 < x1);
       if (x + 1 < x1) row0 = row_of(ld);
@@ -218,11 +235,16 @@ __global__ void __launch_bounds__(kRowThreads, 2) cache_rows_kernel(const __grid
   for (int i = 0; i < kStages - 1; ++i) load(x0 + i);
 
   uint32_t qf[NT][8][2];
-  float o[8][NT][4], l[NT][2], m[NT][2];
+  // m: the reference maximum; mu: the same, 0 while the row has seen no key; thr: how far above mu a score may lie
+  float o[8][NT][4], l[NT][2], m[NT][2], mu[NT][2], thr[NT][2];
   int last[NT][2];                                // the last key that a row sees
   const int kr = lane >> 2, rc = (lane & 3) * 2;  // this thread's keys kr, kr + 8 and rows rc, rc + 1 (+ 8 t)
   float* s_m = reinterpret_cast<float*>(smem + kOffMl);
   float* s_l = s_m + kWarps * kRowsMax;
+  // ldmatrix rows of this lane: K [key][column] as it lies, V transposed
+  const int rk = (lane & 7) + (((lane >> 3) & 1) << 3), rv = (lane & 7) + ((lane >> 4) << 3);
+  const uint32_t get_k = rk * 256 + (((lane >> 4) ^ (rk & 7)) << 4);
+  const uint32_t get_v = rv * 256 + ((((lane >> 3) & 1) ^ (rv & 7)) << 4);
   bool fresh = true;
   int first_kt = 0, get = 0;
   for (long long x = x0; x < x1; ++x) {
@@ -234,7 +256,8 @@ __global__ void __launch_bounds__(kRowThreads, 2) cache_rows_kernel(const __grid
 #pragma unroll
         for (int i = 0; i < 8; ++i) o[i][t][0] = o[i][t][1] = o[i][t][2] = o[i][t][3] = 0.f;
         l[t][0] = l[t][1] = 0.f;
-        m[t][0] = m[t][1] = -INFINITY;
+        m[t][0] = m[t][1] = thr[t][0] = thr[t][1] = -INFINITY;
+        mu[t][0] = mu[t][1] = 0.f;
         last[t][0] = cur.len + (8 * t + rc) / c.group;
         last[t][1] = cur.len + (8 * t + rc + 1) / c.group;
         const int r = 8 * t + kr;
@@ -252,44 +275,62 @@ __global__ void __launch_bounds__(kRowThreads, 2) cache_rows_kernel(const __grid
     cp_async_wait<kStages - 1>();
     __syncwarp();
     const uint32_t sk = ring + (uint32_t)get * kStageBytes, sv = sk + kKeysW * 256;
-    // S^T = K Q^T: 16 keys x 8 NT rows
+    // S^T = K Q^T: 16 keys x 8 NT rows, in two chains
     float sc[NT][4];
-#pragma unroll
-    for (int t = 0; t < NT; ++t) sc[t][0] = sc[t][1] = sc[t][2] = sc[t][3] = 0.f;
     {
-      const int r = (lane & 7) + (((lane >> 3) & 1) << 3), h = lane >> 4;
+      float s2[NT][4];
 #pragma unroll
-      for (int kk = 0; kk < 8; ++kk) {
-        uint32_t a[4];
-        ldsm4(sk + r * 256 + (((2 * kk + h) ^ (r & 7)) << 4), a);
+      for (int t = 0; t < NT; ++t)
 #pragma unroll
-        for (int t = 0; t < NT; ++t) mma16816(sc[t], a, qf[t][kk][0], qf[t][kk][1]);
+        for (int e = 0; e < 4; ++e) sc[t][e] = s2[t][e] = 0.f;
+#pragma unroll
+      for (int kk = 0; kk < 8; kk += 2) {
+        uint32_t a[4], b[4];
+        ldsm4((sk + get_k) ^ (kk << 5), a);
+        ldsm4((sk + get_k) ^ ((kk + 1) << 5), b);
+#pragma unroll
+        for (int t = 0; t < NT; ++t) {
+          mma16816(sc[t], a, qf[t][kk][0], qf[t][kk][1]);
+          mma16816(s2[t], b, qf[t][kk + 1][0], qf[t][kk + 1][1]);
+        }
       }
+#pragma unroll
+      for (int t = 0; t < NT; ++t)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) sc[t][e] += s2[t][e];
     }
     const int key0 = cur.kt * kKeysT + warp * kKeysW;
     // keys up to `len` are seen by every row; past it row r of token t sees keys up to len + t
-    const bool edge = key0 + kKeysW - 1 > cur.len;
-    bool grow = false;
+    if (key0 + kKeysW - 1 > cur.len) {
 #pragma unroll
-    for (int t = 0; t < NT; ++t)
+      for (int t = 0; t < NT; ++t)
 #pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        const int key = key0 + kr + (e >> 1) * 8;
-        const bool seen = !edge || (key <= last[t][e & 1] && key < cur.n);
-        sc[t][e] = seen ? sc[t][e] * p.scale_log2 : -INFINITY;
-        grow |= sc[t][e] > m[t][e & 1] + 8.f;
-      }
+        for (int e = 0; e < 4; ++e) {
+          const int key = key0 + kr + (e >> 1) * 8;
+          if (key > last[t][e & 1] || key >= cur.n) sc[t][e] = -INFINITY;
+        }
+    }
     if (p.scores) {  // for the weights pass: 64 keys x score_rows of a tile
       float* dst = p.scores + (x * kKeysT + warp * kKeysW + kr) * p.score_rows;
 #pragma unroll
       for (int t = 0; t < NT; ++t)
         if (8 * t + rc < p.score_rows) {
-          *reinterpret_cast<float2*>(dst + 8 * t + rc) = make_float2(sc[t][0], sc[t][1]);
-          *reinterpret_cast<float2*>(dst + 8 * p.score_rows + 8 * t + rc) = make_float2(sc[t][2], sc[t][3]);
+          *reinterpret_cast<float2*>(dst + 8 * t + rc) = make_float2(sc[t][0] * p.scale_log2, sc[t][1] * p.scale_log2);
+          *reinterpret_cast<float2*>(dst + 8 * p.score_rows + 8 * t + rc) =
+              make_float2(sc[t][2] * p.scale_log2, sc[t][3] * p.scale_log2);
         }
     }
     // the reference maximum follows only when a score passes it by 2^8 (any reference gives the same
     // quotient; 8 keeps every term finite and the sums exact enough in 32 bits)
+    bool grow = false;
+    float ex[NT][4];
+#pragma unroll
+    for (int t = 0; t < NT; ++t)
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        ex[t][e] = fmaf(sc[t][e], p.scale_log2, -mu[t][e & 1]);
+        grow |= ex[t][e] > thr[t][e & 1];
+      }
     if (__any_sync(kAll, grow)) {
 #pragma unroll
       for (int t = 0; t < NT; ++t)
@@ -299,23 +340,26 @@ __global__ void __launch_bounds__(kRowThreads, 2) cache_rows_kernel(const __grid
           mx = fmaxf(mx, __shfl_xor_sync(kAll, mx, 4));
           mx = fmaxf(mx, __shfl_xor_sync(kAll, mx, 8));
           mx = fmaxf(mx, __shfl_xor_sync(kAll, mx, 16));
-          const float mn = fmaxf(m[t][i], mx);
+          const float mn = fmaxf(m[t][i], mx * p.scale_log2);
           const float a = mn == -INFINITY ? 1.f : ex2_approx(m[t][i] - mn);
           m[t][i] = mn;
+          mu[t][i] = mn == -INFINITY ? 0.f : mn;
+          thr[t][i] = mn == -INFINITY ? -INFINITY : 8.f;
           l[t][i] *= a;
 #pragma unroll
           for (int j = 0; j < 8; ++j) {
             o[j][t][i] *= a;
             o[j][t][2 + i] *= a;
           }
+          ex[t][i] = fmaf(sc[t][i], p.scale_log2, -mu[t][i]);
+          ex[t][2 + i] = fmaf(sc[t][2 + i], p.scale_log2, -mu[t][i]);
         }
     }
     uint32_t pf[NT][2];
 #pragma unroll
     for (int t = 0; t < NT; ++t) {
-      const float mu0 = m[t][0] == -INFINITY ? 0.f : m[t][0], mu1 = m[t][1] == -INFINITY ? 0.f : m[t][1];
-      const float e0 = ex2_approx(sc[t][0] - mu0), e1 = ex2_approx(sc[t][1] - mu1);
-      const float e2 = ex2_approx(sc[t][2] - mu0), e3 = ex2_approx(sc[t][3] - mu1);
+      const float e0 = ex2_approx(ex[t][0]), e1 = ex2_approx(ex[t][1]);
+      const float e2 = ex2_approx(ex[t][2]), e3 = ex2_approx(ex[t][3]);
       l[t][0] += e0 + e2;
       l[t][1] += e1 + e3;
       // the tensor cores take bf16 (half a step is 2^-9 of each term); [key][row] becomes [row][key]
@@ -323,11 +367,10 @@ __global__ void __launch_bounds__(kRowThreads, 2) cache_rows_kernel(const __grid
       pf[t][1] = movmatrix(pack_bf16x2(e2, e3));
     }
     {  // O^T += V^T P^T: 16 columns at a time
-      const int r = (lane & 7) + ((lane >> 4) << 3), h = (lane >> 3) & 1;
 #pragma unroll
       for (int j = 0; j < 8; ++j) {
         uint32_t a[4];
-        ldsm4t(sv + r * 256 + (((2 * j + h) ^ (r & 7)) << 4), a);
+        ldsm4t((sv + get_v) ^ (j << 5), a);
 #pragma unroll
         for (int t = 0; t < NT; ++t) mma16816(o[j][t], a, pf[t][0], pf[t][1]);
       }
@@ -584,7 +627,7 @@ bool cache_attn_tiled(int32_t max_new, int32_t group) { return (int64_t)max_new 
 
 CacheAttnLayout cache_attn_layout(int sms, bool tiled, const CacheInfo& c, bool scores) {
   auto up = [](int64_t x) { return (x + 255) & ~(int64_t)255; };
-  const int64_t grid = tiled ? sms : 2 * sms, rows = 2 * grid * (tiled ? 2 * kTileM : kRowsMax);
+  const int64_t grid = tiled ? sms : kCtasSm * sms, rows = 2 * grid * (tiled ? 2 * kTileM : kRowsMax);
   CacheAttnLayout w;
   w.part_o = 0;
   w.part_ml = up(w.part_o + rows * kHeadDim * 4);
@@ -619,7 +662,7 @@ cudaError_t launch_cache_attn(const CacheAttnParams& p, bool tiled, int sms, cud
     if ((e = launch_cache_tiles(p, sms, st)) != cudaSuccess || !(p.decay >= 0.f)) return e;
     return launch_cache_weights(p, sms, st);
   }
-  const int nt = p.c.max_new * p.c.group <= 8 ? 1 : 2, grid = 2 * sms;
+  const int nt = p.c.max_new * p.c.group <= 8 ? 1 : 2, grid = kCtasSm * sms;
   void (*fn)(const CacheAttnParams) = nt == 1 ? cache_rows_kernel<1> : cache_rows_kernel<2>;
   if ((e = set_max_smem(reinterpret_cast<const void*>(fn), kRowSmem, attr[nt - 1], true)) != cudaSuccess) return e;
   if ((e = launch_pdl(fn, dim3(grid), kRowThreads, kRowSmem, st, p)) != cudaSuccess) return e;
