@@ -614,7 +614,7 @@ __global__ void __launch_bounds__(32 * kJoinWarps) cache_join_kernel(const __gri
           make_uint2(pack_bf16x2(acc.x * inv, acc.y * inv), pack_bf16x2(acc.z * inv, acc.w * inv));
       if (lane == 0) {
         const float z = any ? mu + log2f(l) : -INFINITY;
-        if (p.lse2) p.lse2[(long long)h * c.total_tokens + t] = z;
+        if (p.lse2) p.lse2[(long long)h * c.total_tokens + t] = kTiled ? -z : z;
         if (p.lse) p.lse[(long long)h * c.total_tokens + t] = z * 0.6931471805599453f;
       }
     }

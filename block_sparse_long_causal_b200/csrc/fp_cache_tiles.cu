@@ -677,7 +677,7 @@ __global__ void __launch_bounds__(kThreads, 1) cache_tiles_kernel(const __grid_c
           const float mu = m_run == -INFINITY ? 0.f : m_run;
           const float z = any ? mu + log2f(l_run) : -INFINITY;
           const long long at = (long long)h * c.total_tokens + token;
-          if (p.lse2) p.lse2[at] = z;
+          if (p.lse2) p.lse2[at] = -z;
           if (p.lse) p.lse[at] = z * 0.6931471805599453f;
         } else {  // a row tile without a key tile in this piece: sum 0, and its O is not read
           *reinterpret_cast<float2*>(p.part_ml + 2 * part) = make_float2(n > 0 || dual ? m_run : -INFINITY, l_run);

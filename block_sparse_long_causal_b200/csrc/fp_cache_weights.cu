@@ -1,6 +1,6 @@
 // fp_cache_weights.cu -- the attention weight that cached slots collect from a call of many rows:
 //   w_ug = decay * w_ug + sum_{t, h in group g, u <= lens + t} 2^(scale_log2 q_th . k_u - lse2_th)
-// after the attention has left lse2.
+// after the attention has left -lse2.
 //
 // S^T = K Q^T on the tcgen05 tensor cores with the 128 keys of a tile along the accumulator's lanes and a row
 // tile's 128 rows along its columns, so that a thread owns a key and its sum over rows needs no exchange
@@ -162,6 +162,7 @@ __global__ void __launch_bounds__(kThreads, 1) cache_tiles_weights_kernel(const 
           make_uint4(0, 0, 0, 0);
     asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
   }
+  for (int e = tid; e < kS * 128; e += kThreads) s_z[e] = -INFINITY;  // theirs stay: 2^-inf
   if (warp == 1) {
     tmem_alloc(smem_u32(s_tmem), 512);
     tmem_relinquish();
@@ -311,7 +312,7 @@ __global__ void __launch_bounds__(kThreads, 1) cache_tiles_weights_kernel(const 
     }
     __syncwarp();
   } else if (warp == 2) {
-    // =========================================================== -lse2 of the row tiles
+    // =========================================================== -lse2 of the row tiles, copied as they are
     uint32_t it = 0;
     int tok_r[4], head_r[4];
     for (int j = 0; j < 4; ++j) {
@@ -319,19 +320,19 @@ __global__ void __launch_bounds__(kThreads, 1) cache_tiles_weights_kernel(const 
       head_r[j] = (lane + 32 * j) % G;
     }
     for (long long x = x0; x < x1; ++x, ++it) {
-      float z[4];
-#pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        const int tok = u.rt * TT + tok_r[j];
-        const bool in = tok_r[j] < TT && tok < u.L;
-        z[j] = in ? -__ldcg(p.lse2 + (long long)(u.g * G + head_r[j]) * c.total_tokens + u.seq0 + tok) : -INFINITY;
-      }
       if (it >= kS && !all_wait(b_s_empty(it), ((it / kS) - 1) & 1)) { fail = true; break; }
 #pragma unroll
-      for (int j = 0; j < 4; ++j) s_z[it % kS * 128 + lane + 32 * j] = z[j];
-      mbar_arrive(b_z_full(it));
+      for (int j = 0; j < 4; ++j)
+        if (tok_r[j] < TT) {  // tokens past the sequence's end are masked: any value
+          const int tok = min(u.rt * TT + tok_r[j], u.L - 1);
+          asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(sbase + kOffZ + (it % kS * 128 + lane + 32 * j) * 4),
+                       "l"(p.lse2 + (long long)(u.g * G + head_r[j]) * c.total_tokens + u.seq0 + tok)
+                       : "memory");
+        }
+      asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(b_z_full(it)) : "memory");
       step_next(u, c, TT, x + 1 < x1);
     }
+    asm volatile("cp.async.wait_all;" ::: "memory");
     if (fail && lane == 0) {
       *s_abort = 1;
       dev_flag(p.dev_status, kDevTimeout);

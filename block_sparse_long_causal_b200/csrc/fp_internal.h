@@ -146,7 +146,7 @@ struct __align__(64) CacheAttnParams {
   float scale_log2;           // softmax_scale * log2(e)
   uint16_t* out;              // [T, Hq, d] bf16 bits
   float* lse;                 // [Hq, T] or null (natural log)
-  float* lse2;                // [Hq, T] workspace, log2 units (for the weights), or null
+  float* lse2;                // [Hq, T] workspace, log2 units (for the weights; negated by the 128-row schedule), or null
   float* part_o;              // workspace: partial outputs [2 * grid][rows][128], not normalised
   float* part_ml;             // workspace: their running max (log2 units) and row sum, 2 * grid * rows of each
   int32_t* meta;              // workspace: the unit that each CTA's range begins inside of [grid][kMetaWords]
