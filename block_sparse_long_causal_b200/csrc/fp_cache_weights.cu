@@ -2,15 +2,16 @@
 //   w_ug = decay * w_ug + sum_{t, h in group g, u <= lens + t} 2^(scale_log2 q_th . k_u - lse2_th)
 // after the attention has left -lse2.
 //
-// S^T = K Q^T on the tcgen05 tensor cores with the 128 keys of a tile along the accumulator's lanes and a row
-// tile's 128 rows along its columns, so that a thread owns a key and its sum over rows needs no exchange
-// but one between the two warpgroups, which take 64 columns each. Bound by the exponentials (one per
-// pair of row and key, 16 per SM and clock): four accumulators in TMEM keep the products ahead of them.
+// S^T = K Q^T on the tcgen05 tensor cores with the keys along the accumulator's lanes and a row tile's 128
+// rows along its columns, so that a thread owns a key and its sum over rows needs no exchange. An item is 256
+// keys of one (sequence, kv-head), 128 per warpgroup: the two share the row tiles and run freely beside each
+// other. Bound by the exponentials (one per pair of row and key, 16 per SM and clock); with 128 keys an item,
+// the two warpgroups sharing its columns and adding up at its end, a third of the time was spent on that.
 //
-// A step is one (sequence, kv-head, key tile, row tile); the steps of all key tiles form one line that the CTAs
-// share out evenly, as in the attention: a key tile that several CTAs share leaves one partial sum per piece,
-// added up in the order of the pieces by a second kernel, so the result does not depend on timing. Row tiles
-// stay in shared memory over the key tiles of a kv-head where they fit (kQ of them).
+// A step is one (item, row tile); the steps of all items form one line that the CTAs share out evenly, as in
+// the attention: an item that several CTAs share leaves one partial sum per piece, added up in the order of
+// the pieces by a second kernel, so the result does not depend on timing. Row tiles stay in shared memory over
+// the items of a kv-head where they fit (kQ of them).
 #include "fp_cache.cuh"
 
 namespace fp {
@@ -18,17 +19,16 @@ namespace fp {
 namespace cw {
 
 constexpr unsigned kAll = 0xffffffffu;
-constexpr int kThreads = 384, kBK = 128;
-constexpr int kQ = 4, kK = 2, kS = 4;  // row tiles, key tiles, accumulators
+constexpr int kThreads = 384, kBK = 256;
+constexpr int kQ = 2, kK = 2, kS = 2;  // row tiles, items of keys, pairs of accumulators
 constexpr uint32_t kTile = 128 * 128 * 2, kSlab = 128 * 128;
-constexpr uint32_t kOffQ = 0, kOffK = kQ * kTile, kOffBar = kOffK + kK * kTile;
-// q_full[], q_empty[], k_full[], k_empty[], s_full[], s_empty[], z_full[], x_full[2], x_empty[2], drain
-constexpr int kNumBars = 2 * kQ + 2 * kK + 3 * kS + 4 + 1;
+constexpr uint32_t kOffQ = 0, kOffK = kQ * kTile, kOffBar = kOffK + kK * 2 * kTile;
+// q_full[], q_empty[], k_full[], k_empty[], s_full[][2], s_empty[][2], z_full[], drain
+constexpr int kNumBars = 2 * kQ + 2 * kK + 5 * kS + 1;
 constexpr uint32_t kOffMisc = kOffBar + 8 * kNumBars;                // tmem base, abort flag, bad flag
 constexpr uint32_t kOffScan = (kOffMisc + 16 + 15) & ~15u;           // int64[12]
 constexpr uint32_t kOffZ = kOffScan + 8 * 12;                        // float -lse2[kS][128]
-constexpr uint32_t kOffX = kOffZ + kS * 128 * 4;                     // float[2][128]
-constexpr uint32_t kOffTab = kOffX + 2 * 128 * 4;
+constexpr uint32_t kOffTab = kOffZ + kS * 128 * 4;
 constexpr uint32_t smem_bytes(int S) { return kOffTab + 8 * (S + 1) + 1024; }
 static_assert(smem_bytes(kMaxSeqs) <= 227 * 1024, "shared memory per CTA");
 constexpr uint32_t kIdesc = idesc_bf16_f32(128, 128, 0, 0);
@@ -38,14 +38,14 @@ constexpr uint64_t kDrainLimitNs = 1000000000ull;
 struct Step {
   int s, g, kt, rt;
   int seq0, L, len, n;
-  int R, kts;   // row tiles, key tiles
-  int rt0;      // the first row tile that sees a key of tile kt
+  int R, kts;   // row tiles, items of 256 keys
+  int rt0;      // the first row tile that sees a key of item kt
 };
 __device__ __forceinline__ int first_row_tile(int len, int kt, int TT) {
-  const int past = kt * kBK - len;  // tokens before the first that sees the tile's first key
+  const int past = kt * kBK - len;  // tokens before the first that sees the item's first key
   return past > 0 ? past / TT : 0;
 }
-// steps of one kv-head: tiles up to the one of slot len are seen by every row tile
+// steps of one kv-head: items up to the one of slot len are seen by every row tile
 __device__ __forceinline__ long long head_steps(int L, int n, int TT) {
   if (L <= 0) return 0;
   const int len = n - L, R = (L + TT - 1) / TT, kts = (n + kBK - 1) / kBK, full = min(kts, len / kBK + 1);
@@ -114,18 +114,15 @@ __global__ void __launch_bounds__(kThreads, 1) cache_tiles_weights_kernel(const 
   auto b_q_empty = [&](uint32_t i) { return bar0 + 8 * (kQ + i % kQ); };
   auto b_k_full = [&](uint32_t i) { return bar0 + 8 * (2 * kQ + i % kK); };
   auto b_k_empty = [&](uint32_t i) { return bar0 + 8 * (2 * kQ + kK + i % kK); };
-  auto b_s_full = [&](uint32_t i) { return bar0 + 8 * (2 * kQ + 2 * kK + i % kS); };
-  auto b_s_empty = [&](uint32_t i) { return bar0 + 8 * (2 * kQ + 2 * kK + kS + i % kS); };
-  auto b_z_full = [&](uint32_t i) { return bar0 + 8 * (2 * kQ + 2 * kK + 2 * kS + i % kS); };
-  auto b_x_full = [&](uint32_t i) { return bar0 + 8 * (2 * kQ + 2 * kK + 3 * kS + i % 2); };
-  auto b_x_empty = [&](uint32_t i) { return bar0 + 8 * (2 * kQ + 2 * kK + 3 * kS + 2 + i % 2); };
+  auto b_s_full = [&](uint32_t i, int h) { return bar0 + 8 * (2 * kQ + 2 * kK + 2 * (i % kS) + h); };
+  auto b_s_empty = [&](uint32_t i, int h) { return bar0 + 8 * (2 * kQ + 2 * kK + 2 * kS + 2 * (i % kS) + h); };
+  auto b_z_full = [&](uint32_t i) { return bar0 + 8 * (2 * kQ + 2 * kK + 4 * kS + i % kS); };
   const uint32_t b_drain = bar0 + 8 * (kNumBars - 1);
   uint32_t* s_tmem = reinterpret_cast<uint32_t*>(smem + kOffMisc);
   volatile int* s_abort = reinterpret_cast<volatile int*>(smem + kOffMisc + 4);
   int* s_bad = reinterpret_cast<int*>(smem + kOffMisc + 8);
   long long* s_scan = reinterpret_cast<long long*>(smem + kOffScan);
   float* s_z = reinterpret_cast<float*>(smem + kOffZ);
-  float* s_x = reinterpret_cast<float*>(smem + kOffX);
   long long* tab = reinterpret_cast<long long*>(smem + kOffTab);
   const CacheInfo& c = p.c;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, wg = warp >> 2;
@@ -140,13 +137,11 @@ __global__ void __launch_bounds__(kThreads, 1) cache_tiles_weights_kernel(const 
       mbar_init(b_k_empty(i), 1);
     }
     for (int i = 0; i < kS; ++i) {
-      mbar_init(b_s_full(i), 1);
-      mbar_init(b_s_empty(i), 256);
+      for (int h = 0; h < 2; ++h) {
+        mbar_init(b_s_full(i, h), 1);
+        mbar_init(b_s_empty(i, h), 128);
+      }
       mbar_init(b_z_full(i), 32);
-    }
-    for (int i = 0; i < 2; ++i) {
-      mbar_init(b_x_full(i), 128);
-      mbar_init(b_x_empty(i), 128);
     }
     mbar_init(b_drain, 1);
     *s_abort = 0;
@@ -196,7 +191,7 @@ __global__ void __launch_bounds__(kThreads, 1) cache_tiles_weights_kernel(const 
       const bool inside = u.rt > u.rt0;
       meta[0] = inside && T * (me - 1) / ctas <= item0;
       if (inside) {
-        int last = me;  // the last CTA whose share begins inside the key tile's steps
+        int last = me;  // the last CTA whose share begins inside the item's steps
         while (last + 1 < ctas && T * (last + 1) / ctas < end) ++last;
         meta[1] = last;
         meta[2] = u.s;
@@ -220,7 +215,7 @@ __global__ void __launch_bounds__(kThreads, 1) cache_tiles_weights_kernel(const 
       ++qit;
       return true;
     };
-    bool head = true, tile = true;  // this step begins a kv-head / a key tile (within the share)
+    bool head = true, tile = true;  // this step begins a kv-head / an item (within the share)
     for (long long x = x0; x < x1; ++x) {
       const bool resident = u.R <= kQ;
       if (head && resident) {
@@ -236,10 +231,10 @@ __global__ void __launch_bounds__(kThreads, 1) cache_tiles_weights_kernel(const 
           if (r >= 0) row = (int)r;
         }
         if (kit >= kK && !all_wait(b_k_empty(kit), ((kit / kK) - 1) & 1)) { fail = true; break; }
-        if (lane == 0) mbar_arrive_expect_tx(b_k_full(kit), kTile);
+        if (lane == 0) mbar_arrive_expect_tx(b_k_full(kit), 2 * kTile);
         __syncwarp();
         if (lane < lanes) {
-          const uint32_t dst = sK + kit % kK * kTile + lane * bh * 128;
+          const uint32_t dst = sK + kit % kK * 2 * kTile + lane * bh / 128 * kTile + lane * bh % 128 * 128;
           tma_load_2d(dst, &p.tm_k, b_k_full(kit), u.g * kHeadDim, row);
           tma_load_2d(dst + kSlab, &p.tm_k, b_k_full(kit), u.g * kHeadDim + 64, row);
         }
@@ -275,17 +270,23 @@ __global__ void __launch_bounds__(kThreads, 1) cache_tiles_weights_kernel(const 
         }
         if (!resident && !mbar_wait(b_q_full(qit), (qit / kQ) & 1, p.wait_limit_ns)) { fail = true; break; }
         if (tile && !mbar_wait(b_k_full(kit), (kit / kK) & 1, p.wait_limit_ns)) { fail = true; break; }
-        if (it >= kS && !mbar_wait(b_s_empty(it), ((it / kS) - 1) & 1, p.wait_limit_ns)) { fail = true; break; }
-        tc_fence_after();
         const uint32_t qslot = (resident ? qit + u.rt : qit) % kQ;
         const uint64_t qdesc = sdesc_sw128(sQ + qslot * kTile, 16, 1024);
-        const uint64_t kdesc = sdesc_sw128(sK + kit % kK * kTile, 16, 1024);
 #pragma unroll
-        for (int kk = 0; kk < kHeadDim / 16; ++kk) {
-          const uint32_t off = ((kk >> 2) * kSlab + (kk & 3) * 32) >> 4;
-          mma_ss(tmem + 128 * (it % kS), desc_advance(kdesc, off), desc_advance(qdesc, off), kIdesc, kk > 0 ? 1u : 0u);
+        for (int h = 0; h < 2; ++h) {
+          if (!fail && it >= kS) fail = !mbar_wait(b_s_empty(it, h), ((it / kS) - 1) & 1, p.wait_limit_ns);
+          if (fail) break;
+          tc_fence_after();
+          const uint64_t kdesc = sdesc_sw128(sK + (kit % kK * 2 + h) * kTile, 16, 1024);
+#pragma unroll
+          for (int kk = 0; kk < kHeadDim / 16; ++kk) {
+            const uint32_t off = ((kk >> 2) * kSlab + (kk & 3) * 32) >> 4;
+            mma_ss(tmem + 256 * (it % kS) + 128 * h, desc_advance(kdesc, off), desc_advance(qdesc, off), kIdesc,
+                   kk > 0 ? 1u : 0u);
+          }
+          mma_commit(b_s_full(it, h));
         }
-        mma_commit(b_s_full(it));
+        if (fail) break;
         const int g = u.g, kt = u.kt, s = u.s, R = u.R;
         step_next(u, c, TT, x + 1 < x1);
         head = u.g != g || u.s != s || x + 1 == x1;
@@ -320,7 +321,10 @@ __global__ void __launch_bounds__(kThreads, 1) cache_tiles_weights_kernel(const 
       head_r[j] = (lane + 32 * j) % G;
     }
     for (long long x = x0; x < x1; ++x, ++it) {
-      if (it >= kS && !all_wait(b_s_empty(it), ((it / kS) - 1) & 1)) { fail = true; break; }
+      if (it >= kS && (!all_wait(b_s_empty(it, 0), ((it / kS) - 1) & 1) || !all_wait(b_s_empty(it, 1), ((it / kS) - 1) & 1))) {
+        fail = true;
+        break;
+      }
 #pragma unroll
       for (int j = 0; j < 4; ++j)
         if (tok_r[j] < TT) {  // tokens past the sequence's end are masked: any value
@@ -339,86 +343,78 @@ __global__ void __launch_bounds__(kThreads, 1) cache_tiles_weights_kernel(const 
     }
     __syncwarp();
   } else if (wg >= 1) {
-    // =========================================================== exponentials: thread = key, 64 columns
-    const int half = wg - 1, r = (warp & 3) * 32 + lane;
-    const uint32_t col0 = tmem + ((uint32_t)((warp & 3) * 32) << 16) + 64 * half;
+    // =========================================================== exponentials: thread = key
+    const int half = wg - 1, r = 128 * half + (warp & 3) * 32 + lane;  // the item's key
+    const uint32_t col0 = tmem + ((uint32_t)((warp & 3) * 32) << 16) + 128 * half;
     const uint64_t scale2 = f2_make(p.scale_log2, p.scale_log2);
-    uint32_t it = 0, xc = 0;
+    uint32_t it = 0;
     uint64_t acc[4] = {0ull, 0ull, 0ull, 0ull};
-    bool first_part = x0 < x1 && u.rt > u.rt0;  // the share begins inside a key tile's steps
+    bool first_part = x0 < x1 && u.rt > u.rt0;  // the share begins inside an item's steps
     bool fresh = true;
-    long long at = -1;  // this thread's weight, looked up (and read) while the tile's first step is under way
+    long long at = -1;  // this thread's weight, looked up (and read) while the item's first step is under way
     float old = 0.f;
     for (long long x = x0; x < x1; ++x, ++it) {
       if (fresh) {
         fresh = false;
         const int key = u.kt * kBK + r;
-        at = key < u.n && half == (int)(xc & 1) ? slot_word(c, u.s, u.g, key) : -1;
+        at = key < u.n ? slot_word(c, u.s, u.g, key) : -1;
         old = at >= 0 && p.decay > 0.f ? c.weights[at] : 0.f;
       }
-      if (!all_wait(b_z_full(it), (it / kS) & 1) || !all_wait(b_s_full(it), (it / kS) & 1)) { fail = true; break; }
+      if (!all_wait(b_z_full(it), (it / kS) & 1) || !all_wait(b_s_full(it, half), (it / kS) & 1)) { fail = true; break; }
       tc_fence_after();
-      const float* z = s_z + it % kS * 128 + 64 * half;
-      // columns [cmin, cmax) of this half hold rows that see the key
+      const float* z = s_z + it % kS * 128;
+      // columns [cmin, cmax) hold rows that see the key
       const int past = u.kt * kBK + r - u.len - u.rt * TT;
-      const int cmin = (past > 0 ? min(past, TT) : 0) * G - 64 * half;
+      const int cmin = (past > 0 ? min(past, TT) : 0) * G;
       const bool part = (u.rt + 1) * TT > u.L;
-      const int cmax = (part ? (u.L - u.rt * TT) * G : 128) - 64 * half;
+      const int cmax = part ? (u.L - u.rt * TT) * G : 128;
       const bool edge = part || u.kt * kBK + kBK - 1 - u.len > u.rt * TT;  // the same for every thread
+      const uint32_t col = col0 + 256 * (it % kS);
       uint32_t v[2][32];
-      const uint32_t col = col0 + 128 * (it % kS);
       tmem_ld32(col, v[0]);
-      tmem_ld32(col + 32, v[1]);
-      tmem_wait_ld();
-      reg_fence32(v[0]);
-      reg_fence32(v[1]);
-      if (!edge) {
 #pragma unroll
-        for (int e = 0; e < 64; e += 4) {
-          const float4 zz = *reinterpret_cast<const float4*>(z + e);
-          float a0, a1, a2, a3;
-          f2_split(ffma2(f2_bits(v[e >> 5][e & 31], v[e >> 5][(e & 31) + 1]), scale2, f2_make(zz.x, zz.y)), a0, a1);
-          f2_split(ffma2(f2_bits(v[e >> 5][(e & 31) + 2], v[e >> 5][(e & 31) + 3]), scale2, f2_make(zz.z, zz.w)), a2, a3);
-          acc[(e >> 1) & 2] = fadd2(acc[(e >> 1) & 2], f2_make(ex2_approx(a0), ex2_approx(a1)));
-          acc[((e >> 1) & 2) + 1] = fadd2(acc[((e >> 1) & 2) + 1], f2_make(ex2_approx(a2), ex2_approx(a3)));
-        }
-      } else {
+      for (int b = 0; b < 4; ++b) {
+        tmem_wait_ld();
+        reg_fence32(v[b & 1]);
+        if (b < 3) tmem_ld32(col + 32 * (b + 1), v[(b + 1) & 1]);
+        if (!edge) {
 #pragma unroll
-        for (int e = 0; e < 64; e += 2) {
-          const float2 zz = *reinterpret_cast<const float2*>(z + e);
-          float a0, a1;
-          f2_split(ffma2(f2_bits(v[e >> 5][e & 31], v[e >> 5][(e & 31) + 1]), scale2, f2_make(zz.x, zz.y)), a0, a1);
-          a0 = e >= cmin && e < cmax ? ex2_approx(a0) : 0.f;
-          a1 = e + 1 >= cmin && e + 1 < cmax ? ex2_approx(a1) : 0.f;
-          acc[(e >> 1) & 3] = fadd2(acc[(e >> 1) & 3], f2_make(a0, a1));
+          for (int e = 0; e < 32; e += 4) {
+            const float4 zz = *reinterpret_cast<const float4*>(z + 32 * b + e);
+            float a0, a1, a2, a3;
+            f2_split(ffma2(f2_bits(v[b & 1][e], v[b & 1][e + 1]), scale2, f2_make(zz.x, zz.y)), a0, a1);
+            f2_split(ffma2(f2_bits(v[b & 1][e + 2], v[b & 1][e + 3]), scale2, f2_make(zz.z, zz.w)), a2, a3);
+            acc[(e >> 1) & 2] = fadd2(acc[(e >> 1) & 2], f2_make(ex2_approx(a0), ex2_approx(a1)));
+            acc[((e >> 1) & 2) + 1] = fadd2(acc[((e >> 1) & 2) + 1], f2_make(ex2_approx(a2), ex2_approx(a3)));
+          }
+        } else {
+#pragma unroll
+          for (int e = 0; e < 32; e += 2) {
+            const int col_e = 32 * b + e;
+            const float2 zz = *reinterpret_cast<const float2*>(z + col_e);
+            float a0, a1;
+            f2_split(ffma2(f2_bits(v[b & 1][e], v[b & 1][e + 1]), scale2, f2_make(zz.x, zz.y)), a0, a1);
+            a0 = col_e >= cmin && col_e < cmax ? ex2_approx(a0) : 0.f;
+            a1 = col_e + 1 >= cmin && col_e + 1 < cmax ? ex2_approx(a1) : 0.f;
+            acc[(e >> 1) & 3] = fadd2(acc[(e >> 1) & 3], f2_make(a0, a1));
+          }
         }
       }
       tc_fence_before();
-      mbar_arrive(b_s_empty(it));
+      mbar_arrive(b_s_empty(it, half));
       const bool ends = u.rt + 1 == u.R;
       if (ends || x + 1 == x1) {
         float a0, a1, b0, b1;
         f2_split(fadd2(acc[0], acc[1]), a0, a1);
         f2_split(fadd2(acc[2], acc[3]), b0, b1);
-        float w = (a0 + a1) + (b0 + b1);
+        const float w = (a0 + a1) + (b0 + b1);
         acc[0] = acc[1] = acc[2] = acc[3] = 0ull;
-        if (half != (int)(xc & 1)) {  // the warpgroups take turns in handing over and in writing
-          if (xc >= 2 && !all_wait(b_x_empty(xc), ((xc / 2) - 1) & 1)) { fail = true; break; }
-          s_x[xc % 2 * 128 + r] = w;
-          mbar_arrive(b_x_full(xc));
+        if (ends && !first_part) {
+          if (at >= 0) c.weights[at] = p.decay > 0.f ? fmaf(p.decay, old, w) : w;
         } else {
-          if (!all_wait(b_x_full(xc), (xc / 2) & 1)) { fail = true; break; }
-          const float v = s_x[xc % 2 * 128 + r];
-          w = half == 0 ? w + v : v + w;
-          mbar_arrive(b_x_empty(xc));
-          if (ends && !first_part) {
-            if (at >= 0) c.weights[at] = p.decay > 0.f ? fmaf(p.decay, old, w) : w;
-          } else {
-            p.part_ml[(2ll * me + (first_part ? 0 : 1)) * 128 + r] = w;
-          }
+          p.part_ml[(2ll * me + (first_part ? 0 : 1)) * kBK + r] = w;
         }
         first_part = false;
-        ++xc;
         fresh = true;
       }
       step_next(u, c, TT, x + 1 < x1);
@@ -434,8 +430,8 @@ __global__ void __launch_bounds__(kThreads, 1) cache_tiles_weights_kernel(const 
   if (warp == 1) tmem_dealloc(tmem, 512);
 }
 
-// Adds up the pieces of the key tiles that several CTAs share (places as in the attention's join).
-__global__ void __launch_bounds__(128) cache_weights_join_kernel(const __grid_constant__ CacheAttnParams p) {
+// Adds up the pieces of the items that several CTAs share (places as in the attention's join).
+__global__ void __launch_bounds__(kBK) cache_weights_join_kernel(const __grid_constant__ CacheAttnParams p) {
   pdl_wait();
   const int b = blockIdx.x + 1;
   const int32_t* meta = p.meta + (long long)b * kMetaWords;
@@ -447,7 +443,7 @@ __global__ void __launch_bounds__(128) cache_weights_join_kernel(const __grid_co
   const long long at = slot_word(c, s, meta[3], key);
   if (at < 0) return;
   float w = 0.f;
-  for (int k = b - 1; k <= last; ++k) w += p.part_ml[(2ll * k + (k == b - 1)) * 128 + threadIdx.x];
+  for (int k = b - 1; k <= last; ++k) w += p.part_ml[(2ll * k + (k == b - 1)) * kBK + threadIdx.x];
   c.weights[at] = p.decay > 0.f ? fmaf(p.decay, c.weights[at], w) : w;
 }
 
@@ -462,7 +458,7 @@ cudaError_t launch_cache_weights(const CacheAttnParams& p, int sms, cudaStream_t
   if (e == cudaSuccess)
     e = launch_pdl(cw::cache_tiles_weights_kernel, dim3(sms), cw::kThreads, cw::smem_bytes(p.c.num_seqs), st, p);
   if (e != cudaSuccess || sms < 2) return e;
-  return launch_pdl(cw::cache_weights_join_kernel, dim3(sms - 1), 128, 0, st, p);
+  return launch_pdl(cw::cache_weights_join_kernel, dim3(sms - 1), cw::kBK, 0, st, p);
 }
 
 }  // namespace fp
