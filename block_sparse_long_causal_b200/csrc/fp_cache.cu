@@ -78,6 +78,7 @@ constexpr int kSelThreads = 512, kSelWarps = kSelThreads / 32;
 constexpr int kSelCluster = 16;      // largest cluster
 constexpr int kSelSpan = 8192;       // slots a CTA is meant to take (16 a thread)
 constexpr int kSelKeysMax = 24576;   // keys kept in shared memory (96 KB: two CTAs fit an SM)
+constexpr int kSelRead = 10;         // slots a lane reads at once where that is all of them (8 otherwise)
 constexpr int kSelBins = 2048;
 constexpr int kSelCand = 6144;       // keys of the first digit's class that a CTA may list (24 KB)
 static_assert(kSelBins == 4 * kSelThreads, "a thread sums four bins");
@@ -107,6 +108,10 @@ __global__ void __launch_bounds__(kSelThreads, 2) select_kernel(const SelectPara
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int lo = __ldg(c.cu_seqlens + s), hi = __ldg(c.cu_seqlens + s + 1), len = c.lens[s], L = hi - lo;
   int32_t* moves = p.moves + (long long)sg * p.budget * 2;
+  auto fill = [&] {
+    for (int i = rank * kSelThreads + tid; i < p.budget; i += C * kSelThreads)
+      reinterpret_cast<int2*>(moves)[i] = make_int2(-1, -1);
+  };
   const bool bad_seq = L < 0 || len < 0 || len > c.max_len - L;
   const int n = bad_seq ? 0 : len + L;
   if (tid == 0 && rank == 0) {
@@ -115,7 +120,7 @@ __global__ void __launch_bounds__(kSelThreads, 2) select_kernel(const SelectPara
   }
   if (n <= p.budget) {  // nothing to evict (or a sequence that is skipped: no moves, lens as it was)
     if (tid == 0 && rank == 0) p.move_counts[sg] = 0;
-    for (long long i = rank * kSelThreads + tid; i < 2ll * p.budget; i += C * kSelThreads) moves[i] = -1;
+    fill();
     return;
   }
   // positions at or past `young` are protected (the difference cannot overflow: 64 bits)
@@ -124,20 +129,24 @@ __global__ void __launch_bounds__(kSelThreads, 2) select_kernel(const SelectPara
   // keys of slots u, u + 32, ... (K of them; past the last slot: anything), all their reads in flight together
   auto read_keys = [&](int u, uint32_t* out, auto count) {
     constexpr int K = decltype(count)::value;
-    long long w[K];
+    int page[K], pos[K];
     float val[K];
-    int pos[K];
 #pragma unroll
-    for (int i = 0; i < K; ++i) w[i] = slot_word(c, s, g, min(u + 32 * i, n - 1));
+    for (int i = 0; i < K; ++i)
+      page[i] = __ldg(c.block_table + (long long)s * c.max_pages + min(u + 32 * i, n - 1) / c.page_size);
 #pragma unroll
     for (int i = 0; i < K; ++i) {
-      val[i] = __ldg(c.weights + max(w[i], 0ll));
-      pos[i] = c.positions ? __ldg(c.positions + max(w[i], 0ll)) : u + 32 * i;
+      const int v = min(u + 32 * i, n - 1);
+      const bool bad = page[i] < 0 || page[i] >= c.num_pages;
+      const long long w = ((long long)(bad ? 0 : page[i]) * c.hkv + g) * c.page_size + v % c.page_size;
+      val[i] = __ldg(c.weights + w);
+      pos[i] = c.positions ? __ldg(c.positions + w) : v;
+      page[i] = bad;
     }
 #pragma unroll
     for (int i = 0; i < K; ++i) {
-      bad_page |= w[i] < 0;
-      out[i] = w[i] < 0 ? 0u : rank_key(val[i], pos[i] < p.sinks || pos[i] >= young);
+      bad_page |= page[i] != 0;
+      out[i] = page[i] ? 0u : rank_key(val[i], pos[i] < p.sinks || pos[i] >= young);
     }
   };
   const int wspan = (int)((((long long)n + C * kSelWarps - 1) / (C * kSelWarps) + 31) & ~31ll);  // slots a warp
@@ -148,15 +157,22 @@ __global__ void __launch_bounds__(kSelThreads, 2) select_kernel(const SelectPara
   *reinterpret_cast<uint4*>(&s_hist[4 * tid]) = make_uint4(0, 0, 0, 0);
   *reinterpret_cast<uint4*>(&s_sum[0][4 * tid]) = make_uint4(0, 0, 0, 0);
   if (kept) {
-    for (int u = u0 + lane; u < u1; u += 32 * 8) {
-      uint32_t k[8];
-      read_keys(u, k, std::integral_constant<int, 8>());
+    auto read_all = [&](auto count) {
+      constexpr int K = decltype(count)::value;
+      for (int u = u0 + lane; u < u1; u += 32 * K) {
+        uint32_t k[K];
+        read_keys(u, k, count);
+        if (u == u0 + lane) fill();  // the moves' places, while the reads are under way
 #pragma unroll
-      for (int i = 0; i < 8; ++i)
-        if (u + 32 * i < u1) s_keys[u + 32 * i - base] = k[i];
-    }
+        for (int i = 0; i < K; ++i)
+          if (u + 32 * i < u1) s_keys[u + 32 * i - base] = k[i];
+      }
+    };
+    if (wspan <= 32 * kSelRead) read_all(std::integral_constant<int, kSelRead>());  // one round of reads
+    else read_all(std::integral_constant<int, 8>());
     __syncwarp();  // a warp reads back its own keys only
   }
+  if (!kept || u0 >= u1) fill();
   // f(slot of lane 0, key) for the warp's slots, 32 at a time in ascending order; lanes past u1 get any key
   auto each = [&](auto f) {
     for (int u = u0; u < u1; u += 128) {
@@ -253,7 +269,7 @@ __global__ void __launch_bounds__(kSelThreads, 2) select_kernel(const SelectPara
     __syncthreads();
     prefix = (prefix << bits) | s_pick[0];
     need = s_pick[1];
-    if (pass == 0 && C > 1 && s_pick[2] <= kSelCand) {
+    if (pass == 0 && s_pick[2] <= kSelCand) {
       listed = true;
       each([&](int u, uint32_t k) {
         const bool match = u + lane < u1 && (k >> 21) == prefix;
@@ -263,7 +279,7 @@ __global__ void __launch_bounds__(kSelThreads, 2) select_kernel(const SelectPara
         at = __shfl_sync(kFullMask, at, 0);
         if (match) s_list[at + __popc(m & ((1u << lane) - 1u))] = k;
       });
-      cluster.sync();
+      sync_all();
     }
   }
   const uint32_t thr = prefix;  // keys above thr stay, and the first `need` slots whose key is thr
@@ -338,7 +354,6 @@ __global__ void __launch_bounds__(kSelThreads, 2) select_kernel(const SelectPara
     from += __popc(ms);
     eq_before += __popc(me);
   });
-  for (long long i = 2ll * total + rank * kSelThreads + tid; i < 2ll * p.budget; i += C * kSelThreads) moves[i] = -1;
   if (tid == 0 && rank == 0) p.move_counts[sg] = total;
   if (bad_page) dev_flag(p.dev_status, kDevBadProblem);
   if (C > 1) cluster.sync();  // no CTA ends while another still reads its counts
@@ -363,7 +378,7 @@ cudaError_t launch_select(const SelectParams& p, int sms, cudaStream_t st) {
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)(pairs * C));
   cfg.blockDim = dim3(kSelThreads);
-  cfg.dynamicSmemBytes = ((size_t)cap + (C > 1 ? kSelCand : 0)) * 4;
+  cfg.dynamicSmemBytes = ((size_t)cap + kSelCand) * 4;
   cfg.stream = st;
   cfg.attrs = at;
   cfg.numAttrs = 1;

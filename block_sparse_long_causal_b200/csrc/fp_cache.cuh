@@ -82,6 +82,26 @@ __device__ __forceinline__ bool cache_table(const CacheInfo& c, long long* tab, 
   return ok;
 }
 
+// A line of `total` tiles in equal shares, [at(i), at(i + 1)) for i < parts (at most `most`, and every one
+// has a tile): the first `rem` shares are one tile longer.
+struct Shares {
+  long long q = 0;
+  int rem = 0, parts = 0;
+  Shares() = default;
+  __device__ __forceinline__ Shares(long long total, int most) {
+    parts = (int)min((long long)most, total);
+    if (parts == 0) return;
+    if (total < 0x7fffffffll) {  // the 32-bit division is several times shorter
+      q = (unsigned)total / (unsigned)parts;
+      rem = (int)((unsigned)total % (unsigned)parts);
+    } else {
+      q = total / parts;
+      rem = (int)(total % parts);
+    }
+  }
+  __device__ __forceinline__ long long at(int i) const { return i * q + min(i, rem); }
+};
+
 // Largest s in [0, S) with tab[s] <= x < tab[s + 1] (sequences without work are passed over).
 __device__ __forceinline__ int find_seq64(const long long* tab, int S, long long x) {
   int lo = 0, hi = S - 1;

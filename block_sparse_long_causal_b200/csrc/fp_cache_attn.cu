@@ -86,12 +86,6 @@ __device__ __forceinline__ void cursor_next(Cursor& u, const CacheInfo& c, bool 
   do load_seq(u, c, ++s);
   while (u.kts == 0 && s + 1 < c.num_seqs);
 }
-// Share of CTA (or warp) i of `ctas`: [share(i), share(i + 1)), the first `rem` ones one tile longer.
-struct Shares {
-  long long q;
-  int rem, ctas;
-  __device__ __forceinline__ long long at(int i) const { return i * q + min(i, rem); }
-};
 // Every warp by itself: lane i sums the tiles of a contiguous run of sequences, a scan gives the total, and
 // the lane whose run holds the start of share `me` walks it. No shared memory and no barrier: this
 // chain is most of what a short call waits for. The device arrays are checked against the host's
@@ -119,15 +113,8 @@ __device__ __forceinline__ bool find_share(const CacheInfo& c, Shares& sh, Curso
     if (threadIdx.x == 0 && blockIdx.x == 0) dev_flag(dev_status, kDevBadProblem);
     return false;
   }
-  sh.ctas = (int)min((long long)parts, total);
-  if (me >= sh.ctas) return false;
-  if (total < 0x7fffffffll) {
-    sh.q = (unsigned)total / (unsigned)sh.ctas;
-    sh.rem = (int)((unsigned)total % (unsigned)sh.ctas);
-  } else {
-    sh.q = total / sh.ctas;
-    sh.rem = (int)(total % sh.ctas);
-  }
+  sh = Shares(total, parts);
+  if (me >= sh.parts) return false;
   const long long x0 = sh.at(me);
   const bool mine = incl - sum <= x0 && x0 < incl;
   if (mine) {
@@ -176,7 +163,7 @@ __global__ void __launch_bounds__(kRowThreads, kCtasSm) cache_rows_kernel(const 
     meta[0] = cur.kt > 0 && sh.at(me - 1) <= unit0;  // its first CTA but one: its pieces are joined in its name
     if (cur.kt > 0) {
       int last = me;  // the last CTA whose share begins inside the unit
-      while (last + 1 < sh.ctas && sh.at(last + 1) < end) ++last;
+      while (last + 1 < sh.parts && sh.at(last + 1) < end) ++last;
       meta[1] = last;
       meta[2] = cur.seq0;
       meta[3] = cur.g;
@@ -572,6 +559,12 @@ __global__ void __launch_bounds__(32 * kJoinWarps) cache_join_kernel(const __gri
           return k < P ? __ldcg(reinterpret_cast<const float2*>(p.part_ml + 2 * place(k))) : make_float2(-INFINITY, 0.f);
         };
         const float2 ml0 = ml_of(lane);
+        float4 few[4];  // up to four pieces are read beside their maxima (an unwritten one is not used)
+        const bool early = kTiled && P <= 4;
+        if (early)
+#pragma unroll
+          for (int j = 0; j < 4; ++j)
+            if (j < P) few[j] = __ldcg(reinterpret_cast<const float4*>(p.part_o + place(j) * kHeadDim) + lane);
         float m = ml0.x;
         for (int k = lane + 32; k < P; k += 32) m = fmaxf(m, ml_of(k).x);
 #pragma unroll
@@ -582,6 +575,15 @@ __global__ void __launch_bounds__(32 * kJoinWarps) cache_join_kernel(const __gri
           const float w = ml.y != 0.f ? ex2_approx(ml.x - mu) : 0.f;  // sum 0: nothing of the row in this piece
           if (ml.y != 0.f) l += w * ml.y;
           const unsigned use = __ballot_sync(kAll, ml.y != 0.f);      // its O may be unwritten
+          if (early) {
+#pragma unroll
+            for (int j = 0; j < 4; ++j)
+              if (j % wr == slice && ((use >> j) & 1)) {
+                const float wj = __shfl_sync(kAll, w, j);
+                acc.x += wj * few[j].x; acc.y += wj * few[j].y; acc.z += wj * few[j].z; acc.w += wj * few[j].w;
+              }
+            continue;
+          }
           const int top = min(32, P - k0);
 #pragma unroll 8
           for (int j = slice; j < top; j += wr) {

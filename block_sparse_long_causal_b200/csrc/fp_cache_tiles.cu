@@ -91,8 +91,11 @@ __device__ __forceinline__ long long unit_at(long long i, long long N, unsigned 
   if (N <= ctas || N > kOrderMax) return i;
   return (unsigned)i * ctas % (unsigned)N + (unsigned)i / ((unsigned)N / d);
 }
-// What a unit weighs on the line: its key tiles and what beginning and ending it costs, in key tiles.
-constexpr int kUnitCost = 3;
+// What a unit weighs on the line: its key tiles, more where two row tiles take part in each, and what
+// beginning and ending it costs.
+constexpr int kCost1 = 2, kCost2 = 3, kUnitCost = 6;
+__device__ __forceinline__ int tile_cost(const Unit& u, int TT) { return (2 * u.m + 1) * TT < u.L ? kCost2 : kCost1; }
+__device__ __forceinline__ int tiles_before(long long cost, int w) { return (int)((cost + w - 1) / w); }
 
 __device__ __forceinline__ void tma_load_3d(uint32_t dst, const void* tmap, uint32_t bar, int x, int y, int z) {
   asm volatile(
@@ -167,42 +170,46 @@ __global__ void __launch_bounds__(kThreads, 1) cache_tiles_kernel(const __grid_c
   // ---- this CTA's part [x0, x1) of the line, and the unit that x0 falls into
   const unsigned d = N > gridDim.x && N <= kOrderMax ? gcd32((unsigned)N, gridDim.x) : 1u;
   long long x0 = 0, x1 = 0;
-  int ctas = 0;
   {
-    const long long per = (N + kThreads - 1) / kThreads, a = min(N, tid * per), b = min(N, a + per);
+    int kts = 0, w = 1;
+    auto cost = [&](long long i, Unit& u) {
+      u = decode(c, tab, TT, unit_at(i, N, gridDim.x, d));
+      kts = key_tiles(u, (2 * u.m + 2) * TT);
+      w = tile_cost(u, TT);
+      return (long long)kts * w + kUnitCost;
+    };
+    const long long per = N <= kThreads ? 1 : (N + kThreads - 1) / kThreads, a = min(N, tid * per), b = min(N, a + per);
     long long sum = 0;
-    for (long long i = a; i < b; ++i) {
-      const Unit u = decode(c, tab, TT, unit_at(i, N, gridDim.x, d));
-      sum += key_tiles(u, (2 * u.m + 2) * TT) + kUnitCost;
-    }
+    Unit u;
+    for (long long i = a; i < b; ++i) sum += cost(i, u);
     const long long incl = warp_incl_scan(sum);
     __syncthreads();  // cache_table is done with the scratch
     if (lane == 31) s_scan[warp] = incl;
     __syncthreads();
     long long base = incl - sum, T = 0;
-    for (int w = 0; w < kThreads / 32; ++w) {
-      if (w < warp) base += s_scan[w];
-      T += s_scan[w];
+    for (int k = 0; k < kThreads / 32; ++k) {
+      if (k < warp) base += s_scan[k];
+      T += s_scan[k];
     }
-    ctas = (int)min((long long)gridDim.x, T);
+    // a share is no shorter than a tile, so that every piece between two shares has one
+    const Shares sh(T, (int)min((long long)gridDim.x, T / kCost2));
     const int me = blockIdx.x;
-    if (me < ctas) {
-      x0 = T * me / ctas;
-      x1 = T * (me + 1) / ctas;
+    int32_t* meta = p.meta + (long long)me * kMetaWords;
+    if (me < sh.parts) {
+      x0 = sh.at(me);
+      x1 = sh.at(me + 1);
       if (base <= x0 && x0 < base + sum) {
         for (long long i = a; i < b; ++i) {
-          const Unit u = decode(c, tab, TT, unit_at(i, N, gridDim.x, d));
-          const int kts = key_tiles(u, (2 * u.m + 2) * TT);
-          if (x0 < base + kts + kUnitCost) {
+          const long long all = per > 1 ? cost(i, u) : (long long)kts * w + kUnitCost;
+          if (x0 < base + all) {
             s_start[0] = i;
             s_start[1] = x0 - base;
-            int32_t* meta = p.meta + (long long)me * kMetaWords;
             // a part that begins inside a unit: the first such CTA of the unit has the pieces joined
-            const bool inside = x0 > base && x0 < base + kts;
-            meta[0] = inside && T * (me - 1) / ctas <= base;
+            const bool inside = x0 > base && tiles_before(x0 - base, w) < kts;
+            meta[0] = inside && sh.at(me - 1) <= base;
             if (inside) {
               int last = me;  // the last CTA whose part begins inside the unit
-              while (last + 1 < ctas && T * (last + 1) / ctas < base + kts) ++last;
+              while (last + 1 < sh.parts && tiles_before(sh.at(last + 1) - base, w) < kts) ++last;
               meta[1] = last;
               meta[2] = u.seq0;
               meta[3] = u.g;
@@ -211,11 +218,11 @@ __global__ void __launch_bounds__(kThreads, 1) cache_tiles_kernel(const __grid_c
             }
             break;
           }
-          base += kts + kUnitCost;
+          base += all;
         }
       }
     } else if (tid == 0) {
-      p.meta[(long long)me * kMetaWords] = 0;
+      meta[0] = 0;
     }
   }
   tc_fence_before();
@@ -239,14 +246,15 @@ __global__ void __launch_bounds__(kThreads, 1) cache_tiles_kernel(const __grid_c
       return __all_sync(kAll, mbar_wait(bar, parity, p.wait_limit_ns));
     };
     long long i = x0 < x1 ? s_start[0] : 0;
-    int kt = x0 < x1 ? (int)s_start[1] : 0;
-    for (long long x = x0; x < x1 && !fail; ++i, kt = 0) {
+    long long off = x0 < x1 ? s_start[1] : 0;
+    for (long long x = x0; x < x1 && !fail; ++i, off = 0) {
       const Unit u = decode(c, tab, TT, unit_at(i, N, gridDim.x, d));
+      const int w = tile_cost(u, TT);
       Piece pc;
       pc.kts = key_tiles(u, (2 * u.m + 2) * TT);
-      pc.kt0 = kt;
-      pc.kt1 = (int)min((long long)pc.kts, kt + (x1 - x));
-      x += pc.kts + kUnitCost - kt;
+      pc.kt0 = (int)min((long long)pc.kts, (long long)tiles_before(off, w));
+      pc.kt1 = (int)min((long long)pc.kts, (off + (x1 - x) + w - 1) / w);
+      x += (long long)pc.kts * w + kUnitCost - off;
       if (pc.kt0 >= pc.kts) continue;  // the part begins in what ending the unit costs
       pc.seq0 = u.seq0;
       pc.L = u.L;
@@ -255,7 +263,7 @@ __global__ void __launch_bounds__(kThreads, 1) cache_tiles_kernel(const __grid_c
       pc.tok0 = 2 * u.m * TT;
       pc.nslot = pc.tok0 + TT < u.L ? 2 : 1;
       pc.kts0 = key_tiles(u, (2 * u.m + 1) * TT);
-      pc.slot = kt == 0 && pc.kt1 == pc.kts ? -1 : 2 * (int)blockIdx.x + (kt == 0 ? 1 : 0);
+      pc.slot = pc.kt0 == 0 && pc.kt1 == pc.kts ? -1 : 2 * (int)blockIdx.x + (pc.kt0 == 0 ? 1 : 0);
       if (uc >= kUnitRing && !all_wait(b_u_empty(uc), ((uc / kUnitRing) - 1) & 1)) { fail = true; break; }
       if (lane == 0) {
         *unit_entry(uc) = pc;

@@ -172,8 +172,9 @@ __global__ void __launch_bounds__(kThreads, 1) cache_tiles_weights_kernel(const 
   const uint32_t tmem = *s_tmem;
   pdl_trigger();
   const long long T = ok ? tab[c.num_seqs] : 0;
-  const int ctas = (int)min((long long)gridDim.x, T), me = blockIdx.x;
-  const long long x0 = me < ctas ? T * me / ctas : 0, x1 = me < ctas ? T * (me + 1) / ctas : 0;
+  const Shares sh(T, gridDim.x);
+  const int me = blockIdx.x;
+  const long long x0 = me < sh.parts ? sh.at(me) : 0, x1 = me < sh.parts ? sh.at(me + 1) : 0;
   if (x0 >= x1) {
     if (tid == 0) p.meta[(long long)me * kMetaWords] = 0;
   }
@@ -189,10 +190,10 @@ __global__ void __launch_bounds__(kThreads, 1) cache_tiles_weights_kernel(const 
       int32_t* meta = p.meta + (long long)me * kMetaWords;
       const long long item0 = x0 - (u.rt - u.rt0), end = item0 + u.R - u.rt0;
       const bool inside = u.rt > u.rt0;
-      meta[0] = inside && T * (me - 1) / ctas <= item0;
+      meta[0] = inside && sh.at(me - 1) <= item0;
       if (inside) {
         int last = me;  // the last CTA whose share begins inside the item's steps
-        while (last + 1 < ctas && T * (last + 1) / ctas < end) ++last;
+        while (last + 1 < sh.parts && sh.at(last + 1) < end) ++last;
         meta[1] = last;
         meta[2] = u.s;
         meta[3] = u.g;
