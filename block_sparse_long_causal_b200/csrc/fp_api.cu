@@ -833,6 +833,8 @@ fp_status fp_cache_attn(const fp_problem* p, const fp_kv_cache* c, const void* q
   a.decay = decay;
   a.dev_status = dev_status;
   a.wait_limit_ns = wait_limit_ns();
+  const char* tw = getenv("FP_TEST_UNSIGNALLED_WAIT");
+  a.test_unsignalled_wait = (tw && tw[0] == '1') ? 1 : 0;
   if (tiled) {
     a.tile_tokens = 128 / group;
     a.box_rows = 128;

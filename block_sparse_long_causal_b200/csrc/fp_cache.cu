@@ -31,7 +31,7 @@ __global__ void __launch_bounds__(256) append_kernel(const AppendParams p) {
   long long row = -1;
   if (ok) {
     const int lo = __ldg(c.cu_seqlens + s), hi = __ldg(c.cu_seqlens + s + 1), len = c.lens[s];
-    ok = t < hi && len >= 0 && len <= c.max_len - (hi - lo);
+    ok = lo >= 0 && t >= lo && t < hi && len >= 0 && len <= c.max_len - (hi - lo);
     u = len + (int)(t - lo);
     if (ok) row = slot_row(c, s, u);
   }

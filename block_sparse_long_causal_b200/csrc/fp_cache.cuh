@@ -102,6 +102,10 @@ struct Shares {
   __device__ __forceinline__ long long at(int i) const { return i * q + min(i, rem); }
 };
 
+__device__ __forceinline__ bool nonfinite2(uint32_t x) {  // either of two bf16
+  return (x & 0x7f80u) == 0x7f80u || (x & 0x7f800000u) == 0x7f800000u;
+}
+
 // Largest s in [0, S) with tab[s] <= x < tab[s + 1] (sequences without work are passed over).
 __device__ __forceinline__ int find_seq64(const long long* tab, int S, long long x) {
   int lo = 0, hi = S - 1;

@@ -353,6 +353,37 @@ __global__ void __launch_bounds__(kRowThreads, kCtasSm) cache_rows_kernel(const 
       pf[t][0] = movmatrix(pack_bf16x2(e0, e1));
       pf[t][1] = movmatrix(pack_bf16x2(e2, e3));
     }
+    // 0 * NaN is NaN, so what is masked has to be finite in V as well: non-finite values of new tokens go to the
+    // rows that see them by themselves (p > 0) and become zeros for the product
+    if (cur.L > 1 && key0 + kKeysW - 1 > cur.len) {
+      unsigned char* v = smem + (sv - smem_u32(smem));
+      bool any = false;
+#pragma unroll 1
+      for (int e = lane; e < kKeysW * 16; e += 32) {
+        const uint4 y = *reinterpret_cast<const uint4*>(v + e * 16);
+        any |= nonfinite2(y.x) || nonfinite2(y.y) || nonfinite2(y.z) || nonfinite2(y.w);
+      }
+      if (__any_sync(kAll, any)) {
+        for (int k = 0; k < kKeysW; ++k)
+#pragma unroll
+          for (int j = 0; j < 16; ++j) {  // this thread's columns 8 j + kr: accumulators [j / 2][.][2 (j & 1)], [.. + 1]
+            const uint32_t y = *reinterpret_cast<const uint16_t*>(v + k * 256 + ((j ^ (k & 7)) << 4) + kr * 2);
+            if ((y & 0x7f80) != 0x7f80) continue;
+            const float f = __uint_as_float(y << 16);
+#pragma unroll
+            for (int t = 0; t < NT; ++t)
+#pragma unroll
+              for (int i = 0; i < 2; ++i)
+                if (key0 + k <= last[t][i]) o[j >> 1][t][2 * (j & 1) + i] += f;
+          }
+        __syncwarp();
+        for (int e = lane; e < kKeysW * kHeadDim; e += 32) {
+          uint16_t* y = reinterpret_cast<uint16_t*>(v) + e;
+          if ((*y & 0x7f80) == 0x7f80) *y = 0;
+        }
+        __syncwarp();
+      }
+    }
     {  // O^T += V^T P^T: 16 columns at a time
 #pragma unroll
       for (int j = 0; j < 8; ++j) {

@@ -30,14 +30,15 @@ constexpr float kFastSumLimit = 65536.f;  // largest row sum that an item withou
 constexpr uint32_t kTile = 128 * 128 * 2, kSlab = 128 * 128;
 constexpr uint32_t kOffQ = 0, kOffK = 2 * kTile, kOffV = kOffK + kStages * kTile, kOffBar = kOffV + kStages * kTile;
 // q_full, q_empty, k_full[], k_empty[], v_full[], v_empty[], s_full[2], p_full[2], o_final[2], x_full, x_done,
-// drain, v_tail[], unit_full[], unit_empty[]
-constexpr int kNumBars = 2 + 4 * kStages + 6 + 3 + kStages + 2 * kUnitRing;
+// drain, v_tail[], unit_full[], unit_empty[], never (the test hook's barrier that nothing arrives on)
+constexpr int kNumBars = 2 + 4 * kStages + 6 + 3 + kStages + 2 * kUnitRing + 1;
 constexpr uint32_t kOffMisc = kOffBar + kNumBars * 8;                   // tmem base, abort flag, bad flag
 constexpr uint32_t kOffScan = (kOffMisc + 16 + 15) & ~15u;              // int64[12]; the line's start (5 int64)
 constexpr uint32_t kOffUnit = kOffScan + 8 * 12 + 8 * 6;                // unit descriptors
 constexpr uint32_t kUnitBytes = 48;
 constexpr uint32_t kOffX = kOffUnit + kUnitRing * kUnitBytes;           // float max[2][128], sum[2][128]
-constexpr uint32_t kOffTab = (kOffX + 2 * 2 * 128 * 4 + 15) & ~15u;
+constexpr uint32_t kOffBad = kOffX + 2 * 2 * 128 * 4;                   // per unit entry: int key[3][128], then flags
+constexpr uint32_t kOffTab = (kOffBad + kUnitRing * (3 * 128 + 1) * 4 + 15) & ~15u;
 constexpr uint32_t smem_bytes(int S) { return kOffTab + 8 * (S + 1) + 1024; }
 static_assert(smem_bytes(kMaxSeqs) <= 227 * 1024, "shared memory per CTA");
 constexpr uint32_t kIdescQK = idesc_bf16_f32(128, kBK, 0, 0), kIdescPV = idesc_bf16_f32(128, kHeadDim, 0, 1);
@@ -119,12 +120,16 @@ __global__ void __launch_bounds__(kThreads, 1) cache_tiles_kernel(const __grid_c
   auto b_v_tail = [&](int i) { return b_drain + 8 + 8 * i; };
   auto b_u_full = [&](uint32_t i) { return b_drain + 8 + 8 * (kStages + i % kUnitRing); };
   auto b_u_empty = [&](uint32_t i) { return b_drain + 8 + 8 * (kStages + kUnitRing + i % kUnitRing); };
+  const uint32_t b_never = bar0 + 8 * (kNumBars - 1);
   uint32_t* s_tmem = reinterpret_cast<uint32_t*>(smem + kOffMisc);
   volatile int* s_abort = reinterpret_cast<volatile int*>(smem + kOffMisc + 4);
   int* s_bad = reinterpret_cast<int*>(smem + kOffMisc + 8);
   long long* s_scan = reinterpret_cast<long long*>(smem + kOffScan);
   long long* s_start = s_scan + 12;  // T, unit index, its tile, its line position
   long long* tab = reinterpret_cast<long long*>(smem + kOffTab);
+  // first key of the unit's unseen-by-some ones whose V is NaN, +inf, -inf in a column (see the tail warp)
+  auto bad_keys = [&](uint32_t i) { return reinterpret_cast<int*>(smem + kOffBad) + (i % kUnitRing) * 3 * 128; };
+  volatile int* s_bad_unit = reinterpret_cast<volatile int*>(smem + kOffBad + kUnitRing * 3 * 128 * 4);
   auto unit_entry = [&](uint32_t i) { return reinterpret_cast<Piece*>(smem + kOffUnit + (i % kUnitRing) * kUnitBytes); };
 
   const CacheInfo& c = p.c;
@@ -148,6 +153,7 @@ __global__ void __launch_bounds__(kThreads, 1) cache_tiles_kernel(const __grid_c
     mbar_init(b_x_full, 256);
     mbar_init(b_x_done, 256);
     mbar_init(b_drain, 1);
+    mbar_init(b_never, 1);
     for (int i = 0; i < kUnitRing; ++i) {
       mbar_init(b_u_full(i), 1);
       mbar_init(b_u_empty(i), kUnitReaders);
@@ -158,6 +164,8 @@ __global__ void __launch_bounds__(kThreads, 1) cache_tiles_kernel(const __grid_c
     tma_prefetch_desc(&p.tm_k);
     tma_prefetch_desc(&p.tm_v);
   }
+  for (int e = tid; e < kUnitRing * 3 * 128; e += kThreads) bad_keys(0)[e] = 0x7fffffff;
+  if (tid < kUnitRing) s_bad_unit[tid] = 0;
   if (warp == 1) {
     tmem_alloc(smem_u32(s_tmem), 512);
     tmem_relinquish();
@@ -296,11 +304,12 @@ __global__ void __launch_bounds__(kThreads, 1) cache_tiles_kernel(const __grid_c
           tma_load_2d(dst + kSlab + lane * bh * 128, tm, full, u.g * kHeadDim + 64, row);
         }
       };
-      // a tile that reaches past the sequence's last slot goes to the tail warp first
+      // a tile with keys that the unit's first token does not see goes to the tail warp first
+      const int tail0 = (u.len + pc.tok0 + 1) / kBK;
       auto load_v = [&](int t, int row) -> bool {
         const int vs = vit % kStages;
         if (!all_wait(b_v_empty(vs), ((vit / kStages) & 1) ^ 1)) return false;
-        load(sV + vs * kTile, &p.tm_v, (t + 1) * kBK > n ? b_v_tail(vs) : b_v_full(vs), row);
+        load(sV + vs * kTile, &p.tm_v, t >= tail0 ? b_v_tail(vs) : b_v_full(vs), row);
         ++vit;
         return true;
       };
@@ -433,8 +442,10 @@ __global__ void __launch_bounds__(kThreads, 1) cache_tiles_kernel(const __grid_c
     }
     __syncwarp();
   } else if (warp == 3) {
-    // =========================================================== V rows behind a sequence's last slot
-    // They may hold anything, and 0 * NaN is NaN: they become zeros before the product reads them.
+    // =========================================================== V rows that some row of the unit does not see
+    // 0 * NaN is NaN, so what is masked has to be finite in V as well. Slots behind the sequence's last one may
+    // hold anything: zeros. Non-finite values of new tokens become zeros too, and the first key that has one in
+    // a column is noted for the epilogue, which adds it to the rows that do see the key (p > 0).
     uint32_t vit = 0, tails[2] = {0, 0};
     static_assert(kStages == 2, "tail barriers' phases");
     bool fail = false;
@@ -445,21 +456,52 @@ __global__ void __launch_bounds__(kThreads, 1) cache_tiles_kernel(const __grid_c
       if (!all_wait(b_u_full(uc), (uc / kUnitRing) & 1)) { fail = true; break; }
       const Piece pc = *unit_entry(uc);
       __syncwarp();
-      if (lane == 0) mbar_arrive(b_u_empty(uc));
       if (pc.seq0 < 0) break;
-      vit += pc.kt1 - pc.kt0;
-      const int live = pc.len + pc.L - (pc.kt1 - 1) * kBK;
-      if (live >= kBK) continue;
-      const int vs = (vit - 1) % kStages;
-      const uint32_t phase = vs ? tails[1]++ : tails[0]++;
-      if (!all_wait(b_v_tail(vs), phase & 1)) { fail = true; break; }
-      for (int e = live * 8 + lane; e < kBK * 8; e += 32) {
-        *reinterpret_cast<uint4*>(smem + kOffV + vs * kTile + e * 16) = make_uint4(0, 0, 0, 0);
-        *reinterpret_cast<uint4*>(smem + kOffV + vs * kTile + kSlab + e * 16) = make_uint4(0, 0, 0, 0);
+      int* bad = bad_keys(uc);
+      if (s_bad_unit[uc % kUnitRing]) {  // left by an earlier unit of this entry
+        __syncwarp();
+        for (int e = lane; e < 3 * 128; e += 32) bad[e] = 0x7fffffff;
+        if (lane == 0) s_bad_unit[uc % kUnitRing] = 0;
+        __syncwarp();
       }
-      asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+      const int seen = pc.len + pc.tok0 + 1;  // keys below it are seen by every row
+      for (int t = pc.kt0; t < pc.kt1; ++t, ++vit) {
+        if (t < seen / kBK) continue;
+        const int vs = vit % kStages;
+        const uint32_t phase = vs ? tails[1]++ : tails[0]++;
+        if (!all_wait(b_v_tail(vs), phase & 1)) { fail = true; break; }
+        unsigned char* v = smem + kOffV + vs * kTile;
+        const int live = min(kBK, pc.len + pc.L - t * kBK);  // rows of the sequence
+        bool any = false;
+        for (int e = max(0, seen - t * kBK) * 8 + lane; e < live * 8; e += 32)
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {
+            const uint4 x = *reinterpret_cast<const uint4*>(v + h * kSlab + e * 16);
+            any |= nonfinite2(x.x) || nonfinite2(x.y) || nonfinite2(x.z) || nonfinite2(x.w);
+          }
+        if (__any_sync(kAll, any)) {
+          for (int e = max(0, seen - t * kBK) * 8 + lane; e < live * 8; e += 32)
+            for (int h = 0; h < 2; ++h)
+              for (int i = 0; i < 8; ++i) {
+                uint16_t* x = reinterpret_cast<uint16_t*>(v + h * kSlab + e * 16) + i;
+                if ((*x & 0x7f80) != 0x7f80) continue;
+                const int col = 64 * h + (((e & 7) ^ ((e >> 3) & 7)) << 3) + i;  // 128-byte swizzle
+                atomicMin(bad + ((*x & 0x7f) ? 0 : *x >> 15 ? 256 : 128) + col, t * kBK + (e >> 3));
+                *x = 0;
+              }
+          if (lane == 0) s_bad_unit[uc % kUnitRing] = 1;
+        }
+        for (int e = live * 8 + lane; e < kBK * 8; e += 32) {
+          *reinterpret_cast<uint4*>(v + e * 16) = make_uint4(0, 0, 0, 0);
+          *reinterpret_cast<uint4*>(v + kSlab + e * 16) = make_uint4(0, 0, 0, 0);
+        }
+        asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+        __threadfence_block();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(b_v_full(vs));
+      }
       __syncwarp();
-      if (lane == 0) mbar_arrive(b_v_full(vs));
+      if (lane == 0) mbar_arrive(b_u_empty(uc));
     }
     if (fail && lane == 0) {
       *s_abort = 1;
@@ -481,11 +523,11 @@ __global__ void __launch_bounds__(kThreads, 1) cache_tiles_kernel(const __grid_c
       return __all_sync(kAll, mbar_wait(bar, parity, p.wait_limit_ns));
     };
     const uint64_t scale2 = f2_make(p.scale_log2, p.scale_log2);
+    if (p.test_unsignalled_wait && x0 < x1) fail = !all_wait(b_never, 0);
     for (uint32_t uc = 0; !fail; ++uc) {
       if (!all_wait(b_u_full(uc), (uc / kUnitRing) & 1)) { fail = true; break; }
       const Piece pc = *unit_entry(uc);
       __syncwarp();
-      if (lane == 0) mbar_arrive(b_u_empty(uc));
       if (pc.seq0 < 0) break;
       const bool dual = pc.nslot == 1;  // both warpgroups share the row tile
       const int tok = pc.tok0 + (dual ? 0 : slot) * TT + r / G;
@@ -643,6 +685,8 @@ __global__ void __launch_bounds__(kThreads, 1) cache_tiles_kernel(const __grid_c
       }
       const long long part = ((long long)pc.slot * 2 + (dual ? 0 : slot)) * 128 + r;  // row of the partial results
       uint16_t* orow = p.out + (token * c.hq + h) * kHeadDim;
+      const int* bad = bad_keys(uc);
+      const bool odd = s_bad_unit[uc % kUnitRing] != 0;
       const uint32_t col0 = t_o(dual ? 0 : slot) + lane_off, col1 = t_o(1) + lane_off;
       const int cb = dual ? 64 * slot : 0, ce = dual ? cb + 64 : kHeadDim;
       if (use[0] || pc.slot < 0) {
@@ -665,6 +709,13 @@ __global__ void __launch_bounds__(kThreads, 1) cache_tiles_kernel(const __grid_c
             for (int e = 0; e < 32; ++e)
               o[e] = __float_as_uint(fmaf(__uint_as_float(o1[e]), w1, __uint_as_float(o[e])));
           }
+          if (odd)  // rare: non-finite V of a key that this row sees and others do not
+            for (int e = 0; e < 32; ++e) {
+              float add = last >= bad[b + e] ? NAN : 0.f;
+              if (last >= bad[128 + b + e]) add += INFINITY;
+              if (last >= bad[256 + b + e]) add -= INFINITY;
+              o[e] = __float_as_uint(__uint_as_float(o[e]) + add);
+            }
           if (!pad && pc.slot < 0) {
             uint32_t w[16];
 #pragma unroll
@@ -698,6 +749,8 @@ __global__ void __launch_bounds__(kThreads, 1) cache_tiles_kernel(const __grid_c
         ++xc;
         tc_fence_after();
       }
+      __syncwarp();
+      if (lane == 0) mbar_arrive(b_u_empty(uc));  // the entry and its noted keys may be used again
     }
     if (fail) {
       *s_abort = 1;

@@ -23,8 +23,9 @@ constexpr int kThreads = 384, kBK = 256;
 constexpr int kQ = 2, kK = 2, kS = 2;  // row tiles, items of keys, pairs of accumulators
 constexpr uint32_t kTile = 128 * 128 * 2, kSlab = 128 * 128;
 constexpr uint32_t kOffQ = 0, kOffK = kQ * kTile, kOffBar = kOffK + kK * 2 * kTile;
-// q_full[], q_empty[], k_full[], k_empty[], s_full[][2], s_empty[][2], z_full[], drain
-constexpr int kNumBars = 2 * kQ + 2 * kK + 5 * kS + 1;
+// q_full[], q_empty[], k_full[], k_empty[], s_full[][2], s_empty[][2], z_full[], drain, never (the test hook's
+// barrier that nothing arrives on)
+constexpr int kNumBars = 2 * kQ + 2 * kK + 5 * kS + 2;
 constexpr uint32_t kOffMisc = kOffBar + 8 * kNumBars;                // tmem base, abort flag, bad flag
 constexpr uint32_t kOffScan = (kOffMisc + 16 + 15) & ~15u;           // int64[12]
 constexpr uint32_t kOffZ = kOffScan + 8 * 12;                        // float -lse2[kS][128]
@@ -117,7 +118,7 @@ __global__ void __launch_bounds__(kThreads, 1) cache_tiles_weights_kernel(const 
   auto b_s_full = [&](uint32_t i, int h) { return bar0 + 8 * (2 * kQ + 2 * kK + 2 * (i % kS) + h); };
   auto b_s_empty = [&](uint32_t i, int h) { return bar0 + 8 * (2 * kQ + 2 * kK + 2 * kS + 2 * (i % kS) + h); };
   auto b_z_full = [&](uint32_t i) { return bar0 + 8 * (2 * kQ + 2 * kK + 4 * kS + i % kS); };
-  const uint32_t b_drain = bar0 + 8 * (kNumBars - 1);
+  const uint32_t b_drain = bar0 + 8 * (kNumBars - 2), b_never = b_drain + 8;
   uint32_t* s_tmem = reinterpret_cast<uint32_t*>(smem + kOffMisc);
   volatile int* s_abort = reinterpret_cast<volatile int*>(smem + kOffMisc + 4);
   int* s_bad = reinterpret_cast<int*>(smem + kOffMisc + 8);
@@ -144,6 +145,7 @@ __global__ void __launch_bounds__(kThreads, 1) cache_tiles_weights_kernel(const 
       mbar_init(b_z_full(i), 32);
     }
     mbar_init(b_drain, 1);
+    mbar_init(b_never, 1);
     *s_abort = 0;
     fence_mbar_init();
     tma_prefetch_desc(&p.tm_q);
@@ -354,7 +356,8 @@ __global__ void __launch_bounds__(kThreads, 1) cache_tiles_weights_kernel(const 
     bool fresh = true;
     long long at = -1;  // this thread's weight, looked up (and read) while the item's first step is under way
     float old = 0.f;
-    for (long long x = x0; x < x1; ++x, ++it) {
+    if (p.test_unsignalled_wait && x0 < x1) fail = !all_wait(b_never, 0);
+    for (long long x = x0; x < x1 && !fail; ++x, ++it) {
       if (fresh) {
         fresh = false;
         const int key = u.kt * kBK + r;

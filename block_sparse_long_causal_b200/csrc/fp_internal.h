@@ -156,6 +156,7 @@ struct __align__(64) CacheAttnParams {
   float decay;                // weights = decay * weights + this call's; < 0: weights are left alone
   int32_t* dev_status;
   uint64_t wait_limit_ns;
+  int32_t test_unsignalled_wait;  // tests only: as in AttnParams (128-row schedule)
 };
 
 struct SelectParams {

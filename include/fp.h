@@ -344,8 +344,8 @@ FP_API fp_status fp_paged_validate_lists(const fp_problem* p, const fp_paged_cac
  * the host's) set FP_DEV_BAD_PROBLEM: fp_cache_attn then does no work, the others skip that sequence.
  * A block-table entry outside [0, num_pages) sets it too; attention reads that page as zeros, and the
  * calls that write skip its slots (selection ranks them lowest). Slots past a sequence's last one may
- * hold anything, NaN included; the slots in use are read as numbers, so a non-finite value of one
- * reaches every row that attends it, and a non-finite V also the rows before it in its chunk. */
+ * hold anything, NaN included; a non-finite value in a slot in use reaches the rows that see the slot, and
+ * no others. */
 typedef struct fp_kv_cache {
   void* k;                    /* device bf16 [num_pages * page_size, Hkv, d], 16-byte aligned */
   void* v;
@@ -374,7 +374,10 @@ FP_API fp_status fp_cache_append(const fp_problem* p, const fp_kv_cache* c, cons
                                  const void* v, int64_t v_stride, const int32_t* next_pos, int32_t* dev_status,
                                  void* stream);
 
-/* Bytes of workspace that fp_cache_attn needs (for the current device). */
+/* Bytes of workspace that fp_cache_attn needs (for the current device). It depends on the problem's sizes, on
+ * max_new and, when the cache has weights, on max_len and num_pages (scores of single tokens and short
+ * drafts, 4 bytes per slot and q-head: fp_cache_attn with decay >= 0 flags FP_DEV_BAD_PROBLEM and does no work
+ * when sequences that share pages have more slots than the cache). */
 FP_API fp_status fp_cache_attn_workspace(const fp_problem* p, const fp_kv_cache* c, int64_t* bytes);
 
 /* Attention of the new tokens over the cache (dense: every slot 0 .. lens[s] + t), for one token per

@@ -69,6 +69,9 @@ ATTN = [
     ([77], [90], 8, 8, 16),                                 # one head a group
     ([100, 3], [2, 70], 64, 1, 128),                        # 64 heads a group
     ([511], [513], 16, 2, 128),
+    ([3000, 17, 512, 0, 90, 700, 5, 260], [200, 150, 1, 300, 64, 90, 33, 170], 32, 8, 48),  # more units than CTAs
+    ([6000], [20], 2, 2, 16),                               # one row tile, two warpgroups, split over many CTAs
+    ([128, 384, 383], [32, 128, 1], 4, 1, 64),              # keys and rows that fill their tiles exactly
 ]
 
 
@@ -243,6 +246,113 @@ def test_offsets_past_32_bits():
         assert torch.equal(bits(k[rr.cuda(), h]), bits(want))
     del k, v, w, pos
     torch.cuda.empty_cache()
+
+
+@pytest.mark.parametrize("lens,new,hq,hkv", [([40], [4], 8, 2), ([200], [12], 2, 2), ([70, 33], [200, 60], 8, 2),
+                                             ([300], [20], 4, 2)])
+@pytest.mark.parametrize("value", [math.nan, math.inf, -math.inf])
+def test_masked_values_reach_nobody(lens, new, hq, hkv, value):
+    """A non-finite V of a new token is seen by the rows from that token on, and by no row before it."""
+    x = make(lens, new, hq, hkv, 16, seed=23)
+    G = hq // hkv
+    clean, clean_lse = Dev(x).attn()
+    s, j, g, cols = 0, new[0] // 2, hkv - 1, [0, 5, 63, 64, 127]
+    y = dict(x, v=x["v"].clone())
+    r = int(rows(x["table"], 16, s, lens[s] + j + 1)[-1])
+    y["v"][r, g, cols] = value
+    d = Dev(y)
+    out, lse = d.attn()
+    assert d.status() == 0 and torch.equal(bits(lse.cpu()), bits(clean_lse.cpu()))
+    want = clean.clone()
+    for c in cols:
+        want[j:new[0], g * G:(g + 1) * G, c] = value
+    got, want = out.cpu(), want.cpu()
+    assert torch.equal(got.isnan(), want.isnan())
+    assert torch.equal(bits(got.nan_to_num(nan=1.0)), bits(want.nan_to_num(nan=1.0)))
+    # and a K of it: NaN rows from the token on, the others within their bounds
+    y = dict(x, k=x["k"].clone())
+    y["k"][r, g, 3] = math.nan
+    d = Dev(y)
+    out, lse = d.attn()
+    bad = torch.zeros(out.shape[:2], dtype=torch.bool)
+    bad[j:new[0], g * G:(g + 1) * G] = True
+    assert torch.equal(out.cpu().isnan().all(-1), bad) and torch.equal(lse.cpu().isnan(), bad.T)
+    o, z, _, bo, bz, _ = oracle_attn(x)
+    assert bool(((out.cpu().double() - o).abs() <= bo)[~bad].all())
+    assert bool(((lse.cpu().double() - z).abs() <= bz)[~bad.T].all())
+
+
+def test_prompt_pieces_capture_and_replay():
+    """A captured append + attention + selection + compaction of prompt pieces, replayed on other inputs."""
+    lens, new, hq, hkv, page, B = [30, 261], [70, 50], 8, 2, 16, 200
+    x = make(lens, new, hq, hkv, page, seed=5)
+    d = Dev(x)
+    T = sum(new)
+    mv = torch.empty((2, hkv, B, 2), dtype=torch.int32, device="cuda")
+    cnt, nl = (torch.empty(n, dtype=torch.int32, device="cuda") for n in ((2, hkv), (2,)))
+    q, out = torch.zeros((T, hq, D), dtype=torch.bfloat16, device="cuda"), torch.zeros((T, hq, D), dtype=torch.bfloat16, device="cuda")
+    k, v = (torch.zeros((T, hkv, D), dtype=torch.bfloat16, device="cuda") for _ in range(2))
+
+    def step():
+        fp.cache_append(d.p, d.c, k, v, None, d.st)
+        fp.cache_attn(d.p, d.c, q, 0.0, d.ws, out, None, 0.0, d.st)
+        fp.cache_select(d.p, d.c, B, 2, 60, None, mv, cnt, nl, d.st)
+        fp.cache_compact(d.p, d.c, B, mv, cnt, nl, d.st)
+
+    keep = [t.clone() for t in (d.k, d.v, d.w, d.pos, d.lens)]
+    step()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        step()
+    for seed in (1, 2):
+        g = torch.Generator().manual_seed(seed)
+        for t, src in zip((d.k, d.v, d.w, d.pos, d.lens), keep):
+            t.copy_(src)
+        for t in (q, k, v):
+            t.copy_(torch.randn(t.shape, generator=g).to(torch.bfloat16))
+        y = dict(x, q=q.cpu(), k=x["k"].clone(), v=x["v"].clone(), w=x["w"].clone())
+        t0 = 0
+        for s in range(2):
+            r = rows(x["table"], page, s, lens[s] + new[s])[lens[s]:]
+            y["k"][r], y["v"][r] = k.cpu()[t0:t0 + new[s]], v.cpu()[t0:t0 + new[s]]
+            t0 += new[s]
+        graph.replay()
+        assert d.status() == 0
+        check_attn(y, out, None)
+        assert d.lens.tolist() == [100, 200]
+        assert cnt[0].tolist() == [0] * hkv and min(cnt[1].tolist()) >= 50  # of 60 recent ones past slot 200
+
+
+def test_calls_of_two_streams_at_once():
+    """Two callers, each with its own workspace, on streams of their own."""
+    xs = [make([900, 40], [1, 1], 8, 2, 16, seed=1), make([500, 77], [90, 30], 8, 2, 32, seed=2)]
+    ds = [Dev(x) for x in xs]
+    qs = [x["q"].cuda() for x in xs]
+    outs = [torch.empty_like(q) for q in qs]
+    streams = [torch.cuda.Stream() for _ in xs]
+    torch.cuda.synchronize()
+    for _ in range(20):
+        for d, q, o, st in zip(ds, qs, outs, streams):
+            fp.cache_attn(d.p, d.c, q, 0.0, d.ws, o, None, 0.0, d.st, stream=st)
+    for x, d, o in zip(xs, ds, outs):
+        assert d.status() == 0
+        check_attn(x, o, None, d.w, 0.0)
+
+
+def test_wait_that_runs_out_is_flagged_and_the_context_survives(monkeypatch):
+    x = make([300], [70], 8, 2, 16, seed=3)
+    d = Dev(x)
+    good, _ = d.attn(decay=0.0)
+    assert d.status() == 0
+    monkeypatch.setenv("FP_TEST_UNSIGNALLED_WAIT", "1")
+    monkeypatch.setenv("FP_WAIT_LIMIT_MS", "50")
+    d.attn(decay=0.0)
+    assert d.status() & fp.FP_DEV_TIMEOUT
+    monkeypatch.delenv("FP_TEST_UNSIGNALLED_WAIT")
+    monkeypatch.delenv("FP_WAIT_LIMIT_MS")
+    d.st.zero_()
+    again, _ = d.attn(decay=0.0)
+    assert d.status() == 0 and torch.equal(bits(good), bits(again))
 
 
 def test_bad_tables_are_flagged_and_leave_the_outputs():
