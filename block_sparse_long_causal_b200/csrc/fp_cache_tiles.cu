@@ -345,39 +345,34 @@ __global__ void __launch_bounds__(kThreads, 1) cache_tiles_kernel(const __grid_c
     }
     __syncwarp();
   } else if (warp == 1) {
-    // =========================================================== tcgen05 issue (lane 0)
-    uint32_t kit = 0, vit = 0, cnt[2] = {0, 0};
-    bool fail = false;
-    auto all_wait = [&](uint32_t bar, uint32_t parity) {
-      return __all_sync(kAll, mbar_wait(bar, parity, p.wait_limit_ns));
-    };
-    for (uint32_t uc = 0; !fail; ++uc) {
-      if (!all_wait(b_u_full(uc), (uc / kUnitRing) & 1)) { fail = true; break; }
-      const Piece pc = *unit_entry(uc);
-      __syncwarp();
-      if (lane == 0) mbar_arrive(b_u_empty(uc));
-      if (pc.seq0 < 0) break;
-      if (!all_wait(b_q_full, uc & 1)) { fail = true; break; }
-      tc_fence_after();
-      int prev_part = 0;
-      bool had_pv[2] = {false, false};
-      auto pv = [&](int k) -> bool {  // O_k += P_k V of the tile before
-        if (!all_wait(b_p_full0 + 8 * k, (cnt[k] - 1) & 1)) return false;
-        const int vs = vit % kStages;
-        if (!all_wait(b_v_full(vs), (vit / kStages) & 1)) return false;
+    // =========================================================== tcgen05 issue (one thread)
+    if (lane == 0) {
+      uint32_t kit = 0, vit = 0, cnt[2] = {0, 0};
+      bool fail = false;
+      auto wait = [&](uint32_t bar, uint32_t parity) { return mbar_wait(bar, parity, p.wait_limit_ns); };
+      for (uint32_t uc = 0; !fail; ++uc) {
+        if (!wait(b_u_full(uc), (uc / kUnitRing) & 1)) { fail = true; break; }
+        const Piece pc = *unit_entry(uc);
+        mbar_arrive(b_u_empty(uc));
+        if (pc.seq0 < 0) break;
+        if (!wait(b_q_full, uc & 1)) { fail = true; break; }
         tc_fence_after();
-        if (lane == 0) {
+        int prev_part = 0;
+        bool had_pv[2] = {false, false};
+        auto pv = [&](int k) -> bool {  // O_k += P_k V of the tile before
+          if (!wait(b_p_full0 + 8 * k, (cnt[k] - 1) & 1)) return false;
+          const int vs = vit % kStages;
+          if (!wait(b_v_full(vs), (vit / kStages) & 1)) return false;
+          tc_fence_after();
           const uint64_t vdesc = sdesc_sw128(sV + vs * kTile, kSlab, 1024);
 #pragma unroll
           for (int kk = 0; kk < kBK / 16; ++kk)
             mma_ts(t_o(k), t_s(k) + kk * 8, desc_advance(vdesc, kk * (2048 >> 4)), kIdescPV,
                    had_pv[k] || kk > 0 ? 1u : 0u);
-        }
-        had_pv[k] = true;
-        return true;
-      };
-      auto qk = [&](int k, uint32_t kbase) {
-        if (lane == 0) {
+          had_pv[k] = true;
+          return true;
+        };
+        auto qk = [&](int k, uint32_t kbase) {
           const uint64_t qdesc = sdesc_sw128(sQ + (pc.nslot == 2 ? k : 0) * kTile, 16, 1024);
           const uint64_t kdesc = sdesc_sw128(kbase, 16, 1024);
 #pragma unroll
@@ -386,53 +381,47 @@ __global__ void __launch_bounds__(kThreads, 1) cache_tiles_kernel(const __grid_c
             mma_ss(t_s(k), desc_advance(qdesc, off), desc_advance(kdesc, off), kIdescQK, kk > 0 ? 1u : 0u);
           }
           mma_commit(b_s_full0 + 8 * k);
-        }
-        ++cnt[k];
-      };
-      for (int t = pc.kt0; t < pc.kt1; ++t) {
-        const int part = pc.nslot == 2 ? (t < pc.kts0 ? 3 : 2) : 1 << ((t - pc.kt0) & 1);
-        const int ks = kit % kStages;
-        if (!all_wait(b_k_full(ks), (kit / kStages) & 1)) { fail = true; break; }
-        tc_fence_after();
-        const uint32_t kbase = sK + ks * kTile;
-        // a slot that took part in the previous tile issues that tile's PV before this one's QK (S overwrites
-        // P); the QK of one that did not goes first, so that its softmax overlaps the other's
+          ++cnt[k];
+        };
+        for (int t = pc.kt0; t < pc.kt1; ++t) {
+          const int part = pc.nslot == 2 ? (t < pc.kts0 ? 3 : 2) : 1 << ((t - pc.kt0) & 1);
+          const int ks = kit % kStages;
+          if (!wait(b_k_full(ks), (kit / kStages) & 1)) { fail = true; break; }
+          tc_fence_after();
+          const uint32_t kbase = sK + ks * kTile;
+          // a slot that took part in the previous tile issues that tile's PV before this one's QK (S overwrites
+          // P); the QK of one that did not goes first, so that its softmax overlaps the other's
 #pragma unroll
-        for (int k = 0; k < 2; ++k)
-          if (((part & ~prev_part) >> k) & 1) qk(k, kbase);
+          for (int k = 0; k < 2; ++k)
+            if (((part & ~prev_part) >> k) & 1) qk(k, kbase);
 #pragma unroll
-        for (int k = 0; k < 2; ++k)
-          if (!fail && ((prev_part >> k) & 1)) {
-            if (!pv(k)) { fail = true; break; }
-            if ((part >> k) & 1) qk(k, kbase);
+          for (int k = 0; k < 2; ++k)
+            if (!fail && ((prev_part >> k) & 1)) {
+              if (!pv(k)) { fail = true; break; }
+              if ((part >> k) & 1) qk(k, kbase);
+            }
+          if (fail) break;
+          if (t > pc.kt0) {
+            mma_commit(b_v_empty(vit % kStages));
+            ++vit;
           }
-        if (fail) break;
-        if (t > pc.kt0) {
-          if (lane == 0) mma_commit(b_v_empty(vit % kStages));
-          ++vit;
-        }
-        if (lane == 0) {
           mma_commit(b_k_empty(ks));
           if (t + 1 == pc.kt1) mma_commit(b_q_empty);
+          ++kit;
+          prev_part = part;
+          if (*s_abort) { fail = true; break; }
         }
-        ++kit;
-        prev_part = part;
-        if (*s_abort) { fail = true; break; }
-      }
-      if (fail) break;
+        if (fail) break;
 #pragma unroll
-      for (int k = 0; k < 2; ++k)
-        if (!fail && ((prev_part >> k) & 1))
-          if (!pv(k)) fail = true;
-      if (fail) break;
-      if (lane == 0) {
+        for (int k = 0; k < 2; ++k)
+          if (!fail && ((prev_part >> k) & 1))
+            if (!pv(k)) fail = true;
+        if (fail) break;
         mma_commit(b_v_empty(vit % kStages));
         if (had_pv[0]) mma_commit(b_o_final0);
         if (had_pv[1]) mma_commit(b_o_final0 + 8);
+        ++vit;
       }
-      ++vit;
-    }
-    if (lane == 0) {
       if (fail) {
         *s_abort = 1;
         dev_flag(p.dev_status, kDevTimeout);
