@@ -386,18 +386,22 @@ cudaError_t launch_select(const SelectParams& p, int sms, cudaStream_t st) {
 }
 
 // ------------------------------------------------------------------------ compaction ------------
-// A warp takes eight moves at a time: their entries and page look-ups in eight lanes at once, then the rows
-// with all eight loads in flight, lanes 0..15 the K row and lanes 16..31 the V row, 16 bytes each. Sources
-// lie at or past the budget and destinations below it (checked), so no move reads what another one
-// writes and the order of the moves does not matter.
-constexpr int kMovesW = 8;
+// A CTA takes 64 moves at a time. Two warps look up their rows, a lane to a move, and move the weights and
+// positions, so that neighbouring slots of a head go together; then every warp moves the K and V rows of eight
+// of them with all its loads in flight, lanes 0..15 the K row and lanes 16..31 the V row, 16 bytes each. (Words
+// moved by the eight lanes of each warp that looked them up: 33.3 instead of 27.0 us for a cut from 128K to 16K
+// slots.) Sources lie at or past the budget and destinations below it (checked), so no move reads what another
+// one writes and the order of the moves does not matter.
+constexpr int kMovesW = 8, kMovesC = 8 * kMovesW;
 __global__ void __launch_bounds__(256, 4) compact_kernel(const CompactParams p) {
+  __shared__ longlong2 s_rows[2][kMovesC];  // source and destination rows; source -1: none
   const CacheInfo& c = p.c;
-  const int lane = threadIdx.x & 31, sg = blockIdx.x / p.parts, part = blockIdx.x % p.parts;
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int sg = blockIdx.x / p.parts, part = blockIdx.x % p.parts;
   const int s = sg / c.hkv, g = sg % c.hkv;
   const int cnt = p.move_counts[sg];
   const int slots = (int)min((long long)c.max_len, (long long)c.max_pages * c.page_size);
-  if (part == 0 && threadIdx.x == 0) {
+  if (part == 0 && tid == 0) {
     if (cnt < 0 || cnt > p.budget) dev_flag(p.dev_status, kDevBadList);
     if (g == 0) {
       const int nl = p.new_lens[s];
@@ -407,61 +411,54 @@ __global__ void __launch_bounds__(256, 4) compact_kernel(const CompactParams p) 
   }
   const int2* moves = reinterpret_cast<const int2*>(p.moves) + (long long)sg * p.budget;
   const int n = min(cnt, p.budget);
-  // lane m < kMovesW: rows of move i + m, or -1
-  auto entry = [&](long long i, long long& src, long long& dst) {
-    src = dst = -1;
-    if (lane >= kMovesW || i + lane >= n) return;
-    const int2 mv = moves[i + lane];
-    if (mv.x < p.budget || mv.x >= slots || mv.y < 0 || mv.y >= p.budget || mv.y >= slots) {
-      dev_flag(p.dev_status, kDevBadList);
-      return;
+  auto look_up = [&](long long i, int buf) {  // moves i .. i + 63, by the first 64 threads
+    longlong2 r = make_longlong2(-1, -1);
+    if (i + tid < n) {
+      const int2 mv = moves[i + tid];
+      if (mv.x < p.budget || mv.x >= slots || mv.y < 0 || mv.y >= p.budget || mv.y >= slots) {
+        dev_flag(p.dev_status, kDevBadList);
+      } else {
+        r = make_longlong2(slot_row(c, s, mv.x), slot_row(c, s, mv.y));
+        if (r.x < 0 || r.y < 0) {
+          dev_flag(p.dev_status, kDevBadProblem);
+          r.x = -1;
+        }
+      }
     }
-    src = slot_row(c, s, mv.x);
-    dst = slot_row(c, s, mv.y);
-    if (src < 0 || dst < 0) {
-      dev_flag(p.dev_status, kDevBadProblem);
-      src = -1;
-    }
-  };
-  const int step = p.parts * 8 * kMovesW;
-  long long i = (part * 8 + (threadIdx.x >> 5)) * kMovesW, src, dst;
-  if (i >= n) return;
-  entry(i, src, dst);
-  uint4* rows = reinterpret_cast<uint4*>(lane < 16 ? c.k : c.v) + (lane & 15);
-  for (;; i += step) {
-    uint4 v[kMovesW];
-#pragma unroll
-    for (int m = 0; m < kMovesW; ++m) {
-      const long long a = __shfl_sync(kFullMask, src, m);
-      if (a >= 0) v[m] = rows[(a * c.hkv + g) * 16];
-    }
-    const long long ps = src / c.page_size, pd = dst / c.page_size;
-    const long long ws = (ps * c.hkv + g) * c.page_size + (src - ps * c.page_size);
-    const long long wd = (pd * c.hkv + g) * c.page_size + (dst - pd * c.page_size);
+    s_rows[buf][tid] = r;
+    if (r.x < 0) return;
+    const long long ps = r.x / c.page_size, pd = r.y / c.page_size;
+    const long long ws = (ps * c.hkv + g) * c.page_size + (r.x - ps * c.page_size);
+    const long long wd = (pd * c.hkv + g) * c.page_size + (r.y - pd * c.page_size);
     float w = 0.f;
     int pos = 0;
-    if (src >= 0 && c.weights) w = c.weights[ws];
-    if (src >= 0 && c.positions) pos = c.positions[ws];
-    const bool more = i + step < n;
-    long long nsrc = -1, ndst = -1;
-    if (more) entry(i + step, nsrc, ndst);  // the next entries arrive while these rows do
+    if (c.weights) w = c.weights[ws];
+    if (c.positions) pos = c.positions[ws];
+    if (c.weights) c.weights[wd] = w;
+    if (c.positions) c.positions[wd] = pos;
+  };
+  long long i = (long long)part * kMovesC;
+  const int step = p.parts * kMovesC;
+  if (i < n && tid < kMovesC) look_up(i, 0);
+  uint4* rows = reinterpret_cast<uint4*>(lane < 16 ? c.k : c.v) + (lane & 15);
+  for (int buf = 0; i < n; i += step, buf ^= 1) {
+    __syncthreads();
+    uint4 v[kMovesW];
+    const longlong2* r = s_rows[buf] + warp * kMovesW;
 #pragma unroll
-    for (int m = 0; m < kMovesW; ++m) {
-      const long long a = __shfl_sync(kFullMask, src, m), b = __shfl_sync(kFullMask, dst, m);
-      if (a >= 0) rows[(b * c.hkv + g) * 16] = v[m];
-    }
-    if (src >= 0 && c.weights) c.weights[wd] = w;
-    if (src >= 0 && c.positions) c.positions[wd] = pos;
-    if (!more) break;
-    src = nsrc;
-    dst = ndst;
+    for (int m = 0; m < kMovesW; ++m)
+      if (r[m].x >= 0) v[m] = rows[(r[m].x * c.hkv + g) * 16];
+    if (i + step < n && tid < kMovesC) look_up(i + step, buf ^ 1);  // the next ones, while these rows arrive
+#pragma unroll
+    for (int m = 0; m < kMovesW; ++m)
+      if (r[m].x >= 0) rows[(r[m].y * c.hkv + g) * 16] = v[m];
   }
 }
 
 cudaError_t launch_compact(const CompactParams& in, int sms, cudaStream_t st) {
   CompactParams p = in;
-  // about four CTAs an SM over all pairs, and no more than one chunk a warp needs
-  const long long pairs = (long long)p.c.num_seqs * p.c.hkv, most = ((long long)p.budget + 8 * kMovesW - 1) / (8 * kMovesW);
+  // about four CTAs an SM over all pairs, and no more than there are chunks of moves
+  const long long pairs = (long long)p.c.num_seqs * p.c.hkv, most = ((long long)p.budget + kMovesC - 1) / kMovesC;
   const long long want = (4ll * sms + pairs - 1) / pairs;
   p.parts = (int)(want < most ? want : most);
   compact_kernel<<<(unsigned)(pairs * p.parts), 256, 0, st>>>(p);
