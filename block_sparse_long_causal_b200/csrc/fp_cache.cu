@@ -211,14 +211,20 @@ __global__ void __launch_bounds__(kSelThreads, 2) select_kernel(const SelectPara
       }
     } else {
       each([&](int u, uint32_t k) {
-        const bool match = u + lane < u1 && (pass == 0 || (k >> (shift + bits)) == prefix);
-        const unsigned act = __ballot_sync(kFullMask, match);
         // the warp's most likely run of equal digits (protected slots, ties) is added once: that of its first lane
+        // that matches
+        const bool match = u + lane < u1 && (pass == 0 || (k >> (shift + bits)) == prefix);
         const unsigned dig = (k >> shift) & mask;
-        const unsigned lead = __shfl_sync(kFullMask, dig, act ? __ffs(act) - 1 : 0);
+        int from = 0;
+        if (pass > 0) {
+          const unsigned act = __ballot_sync(kFullMask, match);
+          if (act == 0) return;
+          from = __ffs(act) - 1;
+        }
+        const unsigned lead = __shfl_sync(kFullMask, dig, from);
         const unsigned same = __ballot_sync(kFullMask, match && dig == lead);
         if (match && dig != lead) atomicAdd(&s_hist[dig], 1u);
-        if (lane == 0 && act) atomicAdd(&s_hist[lead], (unsigned)__popc(same));
+        if (lane == 0) atomicAdd(&s_hist[lead], (unsigned)__popc(same));
       });
     }
     __syncthreads();
@@ -286,8 +292,9 @@ __global__ void __launch_bounds__(kSelThreads, 2) select_kernel(const SelectPara
   int4 cnt = make_int4(0, 0, 0, 0);
   each([&](int u, uint32_t k) {
     const bool in = u + lane < u1;
-    const unsigned below = __ballot_sync(kFullMask, u + lane < p.budget);
     const unsigned mg = __ballot_sync(kFullMask, in && k > thr), me = __ballot_sync(kFullMask, in && k == thr);
+    // the lanes below the budget: all, none, or a run from lane 0
+    const unsigned below = u + 32 <= p.budget ? kFullMask : u >= p.budget ? 0u : (1u << (p.budget - u)) - 1u;
     cnt.x += __popc(mg & below);
     cnt.y += __popc(mg & ~below);
     cnt.z += __popc(me & below);
@@ -346,13 +353,18 @@ __global__ void __launch_bounds__(kSelThreads, 2) select_kernel(const SelectPara
     const unsigned me = __ballot_sync(kFullMask, in && k == thr);
     const unsigned lt = (1u << lane) - 1u;
     const bool keep = in && (k > thr || (k == thr && eq_before + __popc(me & lt) < (int)need));
-    const bool low = u + lane < p.budget;
-    const unsigned mh = __ballot_sync(kFullMask, in && low && !keep), ms = __ballot_sync(kFullMask, keep && !low);
-    if (in && low && !keep) moves[2ll * (hole + __popc(mh & lt)) + 1] = u + lane;
-    if (keep && !low) moves[2ll * (from + __popc(ms & lt))] = u + lane;
-    hole += __popc(mh);
-    from += __popc(ms);
     eq_before += __popc(me);
+    const bool low = u + lane < p.budget;
+    if (u < p.budget) {
+      const unsigned mh = __ballot_sync(kFullMask, in && low && !keep);
+      if (in && low && !keep) moves[2ll * (hole + __popc(mh & lt)) + 1] = u + lane;
+      hole += __popc(mh);
+    }
+    if (u + 32 > p.budget) {
+      const unsigned ms = __ballot_sync(kFullMask, keep && !low);
+      if (keep && !low) moves[2ll * (from + __popc(ms & lt))] = u + lane;
+      from += __popc(ms);
+    }
   });
   if (tid == 0 && rank == 0) p.move_counts[sg] = total;
   if (bad_page) dev_flag(p.dev_status, kDevBadProblem);
