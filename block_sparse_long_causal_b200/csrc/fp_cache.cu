@@ -92,7 +92,9 @@ static_assert(kSelBins == 4 * kSelThreads, "a thread sums four bins");
 // keys of it, and the other passes run in each CTA over all lists, without a barrier across the cluster
 // (128K slots: 44 -> 30 us). Then every warp counts its slots above and at the threshold, and after a scan over the cluster's warps writes its holes (evicted slots below
 // the budget) and sources (kept slots at or past it) in ascending order.
-// Bound by latency (a few thousand slots a CTA): the loops keep several slots a lane in flight.
+// Bound by latency (a few thousand slots a CTA): the loops keep several slots a lane in flight. Every write is
+// bounded by itself: the passes over a range that is read again would disagree if another stream changed the
+// weights meanwhile.
 __global__ void __launch_bounds__(kSelThreads, 2) select_kernel(const SelectParams p, const int keys_cap) {
   extern __shared__ uint32_t s_keys[];
   __shared__ __align__(16) unsigned s_hist[kSelBins], s_sum[2][kSelBins];
@@ -172,7 +174,7 @@ __global__ void __launch_bounds__(kSelThreads, 2) select_kernel(const SelectPara
     else read_all(std::integral_constant<int, 8>());
     __syncwarp();  // a warp reads back its own keys only
   }
-  if (!kept || u0 >= u1) fill();
+  if (!kept || u0 + lane >= u1) fill();  // the lanes that had nothing to read
   // f(slot of lane 0, key) for the warp's slots, 32 at a time in ascending order; lanes past u1 get any key
   auto each = [&](auto f) {
     for (int u = u0; u < u1; u += 128) {
@@ -194,7 +196,7 @@ __global__ void __launch_bounds__(kSelThreads, 2) select_kernel(const SelectPara
   };
   sync_all();  // every CTA's sums are zero before another adds to them
   bool listed = false;
-  if (tid == 0) s_listed = 0;
+  if (tid == 0) s_listed = s_pick[0] = s_pick[1] = s_pick[2] = 0;
   unsigned prefix = 0, need = (unsigned)p.budget;  // `need` keys of the current prefix class stay
 #pragma unroll 1
   for (int pass = 0; pass < 3; ++pass) {
@@ -202,7 +204,7 @@ __global__ void __launch_bounds__(kSelThreads, 2) select_kernel(const SelectPara
     const unsigned mask = (1u << bits) - 1u;
     if (listed) {
       const int per = kSelThreads / C, r = tid / per;  // threads per list, and this thread's list
-      const unsigned num = *cluster.map_shared_rank(&s_listed, r);
+      const unsigned num = min(*cluster.map_shared_rank(&s_listed, r), (unsigned)kSelCand);
       const uint32_t* list = cluster.map_shared_rank(s_list, r);
 #pragma unroll 4
       for (unsigned j = tid % per; j < num; j += per) {
@@ -283,7 +285,8 @@ __global__ void __launch_bounds__(kSelThreads, 2) select_kernel(const SelectPara
         unsigned at = 0;
         if (lane == 0 && m) at = atomicAdd(&s_listed, (unsigned)__popc(m));
         at = __shfl_sync(kFullMask, at, 0);
-        if (match) s_list[at + __popc(m & ((1u << lane) - 1u))] = k;
+        at += __popc(m & ((1u << lane) - 1u));
+        if (match && at < kSelCand) s_list[at] = k;
       });
       sync_all();
     }
@@ -357,12 +360,14 @@ __global__ void __launch_bounds__(kSelThreads, 2) select_kernel(const SelectPara
     const bool low = u + lane < p.budget;
     if (u < p.budget) {
       const unsigned mh = __ballot_sync(kFullMask, in && low && !keep);
-      if (in && low && !keep) moves[2ll * (hole + __popc(mh & lt)) + 1] = u + lane;
+      const int at = hole + __popc(mh & lt);
+      if (in && low && !keep && at < p.budget) moves[2ll * at + 1] = u + lane;
       hole += __popc(mh);
     }
     if (u + 32 > p.budget) {
       const unsigned ms = __ballot_sync(kFullMask, keep && !low);
-      if (keep && !low) moves[2ll * (from + __popc(ms & lt))] = u + lane;
+      const int at = from + __popc(ms & lt);
+      if (keep && !low && at < p.budget) moves[2ll * at] = u + lane;
       from += __popc(ms);
     }
   });

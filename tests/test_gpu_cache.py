@@ -445,6 +445,7 @@ SELECT = [
     ([3000], [1], 2, 64, 700, 4, 100),
     ([3000, 2000, 50], [30, 0, 1], 2, 32, 1999, 0, 0),
     ([9000], [0], 1, 128, 33, 1, 3),
+    ([70000, 12], [3, 1], 2, 32, 9001, 4, 500),  # several CTAs a head
 ]
 
 
@@ -476,6 +477,34 @@ def test_selection_and_compaction(lens, new, hkv, page, budget, sinks, recent, k
                 w[pb, h, b % page], pos[pb, h, b % page] = x["w"][pa, h, a % page], x["pos"][pa, h, a % page]
     assert torch.equal(bits(d.k.cpu()), bits(k)) and torch.equal(bits(d.v.cpu()), bits(v))
     assert torch.equal(bits(d.w.cpu()), bits(w)) and torch.equal(d.pos.cpu(), pos)
+
+
+@pytest.mark.parametrize("kind", ["ties", "tail"])
+def test_selection_of_more_slots_than_shared_memory_holds(kind):
+    """Many heads of a long sequence: one CTA a head, which reads its slots again in every pass."""
+    n, hkv, page, B, sinks, recent = 30001, 160, 256, 4000, 4, 900
+    pages = -(-n // page)
+    g = torch.Generator(device="cuda").manual_seed(9)
+    w = torch.rand((pages, hkv, page), generator=g, device="cuda")
+    w = (w * 50).floor() / 50 if kind == "ties" else torch.exp(8 * w)
+    pos = torch.stack([torch.randperm(pages * page, generator=g, device="cuda") for _ in range(hkv)]).to(torch.int32)
+    pos = pos.view(hkv, pages, page).transpose(0, 1).contiguous()
+    k = torch.zeros((pages * page, hkv, D), dtype=torch.bfloat16, device="cuda")
+    table = torch.randperm(pages, generator=g, device="cuda").to(torch.int32)[None]
+    lens, nxt = (torch.tensor([v], dtype=torch.int32, device="cuda") for v in (n, pages * page))
+    p = fp.problem([0, 0], hkv, hkv)
+    c = fp.kv_cache(p, k, k, lens, table, page, w, pos)
+    mv = torch.empty((1, hkv, B, 2), dtype=torch.int32, device="cuda")
+    cnt, nl = torch.empty((1, hkv), dtype=torch.int32, device="cuda"), torch.empty(1, dtype=torch.int32, device="cuda")
+    st = torch.zeros(1, dtype=torch.int32, device="cuda")
+    fp.cache_select(p, c, B, sinks, recent, nxt, mv, cnt, nl, st)
+    torch.cuda.synchronize()
+    assert int(st.item()) == 0 and nl.tolist() == [B]
+    for h in (0, 77, 159):
+        x = {"lens": [n], "new": [0], "hkv": 1, "page": page, "table": table.cpu(), "w": w[:, h:h + 1].cpu(),
+             "pos": pos[:, h:h + 1].cpu()}
+        m, cc, _ = oracle_select(x, B, sinks, recent, [pages * page])
+        assert torch.equal(mv[:, h:h + 1].cpu(), m) and int(cnt[0, h]) == int(cc)
 
 
 def test_selection_without_positions_ranks_slots():
