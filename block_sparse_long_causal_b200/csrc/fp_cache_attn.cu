@@ -542,12 +542,10 @@ __global__ void __launch_bounds__(32 * kJoinWarps) cache_join_kernel(const __gri
   constexpr int kRowsU = kTiled ? 2 * kTileM : kRowsMax;  // rows of a piece
   __shared__ float4 s_acc[kJoinWarps][32];
   __shared__ int4 s_meta[kJoinUnits][2];  // set entries; word 0: the CTA
-  __shared__ int s_num[kJoinWarps];
+  __shared__ int s_num[kJoinWarps], s_row0[kTiled ? kJoinUnits : 1];  // rows of the entries before an entry
   pdl_wait();
   const CacheInfo& c = p.c;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, G = c.group;
-  // the most rows that a piece of this call can have
-  const int rows = kTiled ? (c.max_new > p.tile_tokens ? kRowsU : kTileM) : min(kRowsU, c.max_new * G);
   for (int b0 = 0; b0 < ctas; b0 += kJoinUnits) {  // one round on devices of up to 256 SMs
     __syncthreads();
     int4 e0 = make_int4(0, 0, 0, 0), e1 = e0;
@@ -557,29 +555,50 @@ __global__ void __launch_bounds__(32 * kJoinWarps) cache_join_kernel(const __gri
       e1 = __ldcg(src + 1);
     }
     const unsigned set = __ballot_sync(kAll, e0.x != 0);
-    if (lane == 0) s_num[warp] = __popc(set);
+    // few rows: every unit gets the most rows that one can have. Row tiles: the rows from a unit's first token to its
+    // sequence's last (a batch of ragged pieces: 32.2 -> 31.2 us for the call)
+    int rows = 0, rows_incl = 0;
+    if (kTiled) {
+      const int toks = e1.y - e1.x, TT = p.tile_tokens;
+      if (e0.x != 0) rows = toks > TT ? kTileM + min(toks - TT, TT) * G : toks * G;
+      rows_incl = warp_incl_scan(rows);
+    }
+    if (lane == 31) s_num[warp] = rows_incl << 6 | __popc(set);  // at most 32 * 256 rows, 32 entries
     __syncthreads();
-    int at = __popc(set & ((1u << lane) - 1u)), num = 0;
+    int at = __popc(set & ((1u << lane) - 1u)), num = 0, row0 = rows_incl - rows, tasks = 0;
 #pragma unroll
     for (int w = 0; w < kJoinWarps; ++w) {
       const int x = s_num[w];
-      at += w < warp ? x : 0;
-      num += x;
+      at += w < warp ? x & 63 : 0;
+      num += x & 63;
+      row0 += w < warp ? x >> 6 : 0;
+      tasks += x >> 6;
     }
+    if (!kTiled) tasks = num * min(kRowsU, c.max_new * G);
     if (e0.x != 0) {
       e0.x = b0 + tid;
       s_meta[at][0] = e0;
       s_meta[at][1] = e1;
+      if (kTiled) s_row0[at] = row0;
     }
     __syncthreads();
     if (num == 0) continue;
-    const int tasks = num * rows;
     int wr = 1;  // warps that share a row
     while (wr < kJoinWarps && 2ll * wr * tasks <= (long long)gridDim.x * kJoinWarps) wr *= 2;
     const int per = kJoinWarps / wr, slice = warp % wr;  // rows a block takes at a time
     for (int task0 = blockIdx.x * per; task0 < tasks; task0 += gridDim.x * per) {
       const int task = task0 + warp / wr;
-      const int row = task / num, unit = task < tasks ? task - row * num : 0;
+      int unit = 0, row;
+      if (kTiled) {
+        for (int hi = num - 1; unit < hi;) {  // the entry that the row belongs to
+          const int mid = (unit + hi + 1) >> 1;
+          if (s_row0[mid] <= task) unit = mid; else hi = mid - 1;
+        }
+        row = task - s_row0[unit];
+      } else {
+        row = task / num;
+        unit = task < tasks ? task - row * num : 0;
+      }
       const int4 meta = s_meta[unit][0], meta2 = s_meta[unit][1];
       // meta2: first token and tokens of the sequence (tiled), first packed row and packed rows (not)
       const int b = meta.x, P = meta.y - b + 2, seq0 = meta.z, g = meta.w;
