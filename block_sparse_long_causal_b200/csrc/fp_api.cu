@@ -822,6 +822,7 @@ fp_status fp_cache_attn(const fp_problem* p, const fp_kv_cache* c, const void* q
   a.q = static_cast<const uint16_t*>(q);
   a.scale_log2 = scale * 1.4426950408889634f;
   a.out = static_cast<uint16_t*>(out);
+  a.out32 = (reinterpret_cast<uintptr_t>(out) & 31u) == 0;
   a.lse = lse;
   a.lse2 = decay >= 0.f ? reinterpret_cast<float*>(base + w.lse2) : nullptr;
   a.scores = decay >= 0.f && !tiled ? reinterpret_cast<float*>(base + w.scores) : nullptr;

@@ -537,12 +537,10 @@ __global__ void __launch_bounds__(256) cache_rows_weights_kernel(const __grid_co
 // block lists the set entries, and the rows of all listed units go round the grid's warps, 32 maxima at
 // once; where there are fewer rows than warps, up to 16 warps of a block share a row's pieces.
 constexpr int kJoinWarps = 16, kJoinUnits = 512;
-template <bool kTiled>
 __global__ void __launch_bounds__(32 * kJoinWarps) cache_join_kernel(const __grid_constant__ CacheAttnParams p, int ctas) {
-  constexpr int kRowsU = kTiled ? 2 * kTileM : kRowsMax;  // rows of a piece
   __shared__ float4 s_acc[kJoinWarps][32];
   __shared__ int4 s_meta[kJoinUnits][2];  // set entries; word 0: the CTA
-  __shared__ int s_num[kJoinWarps], s_row0[kTiled ? kJoinUnits : 1];  // rows of the entries before an entry
+  __shared__ int s_num[kJoinWarps];
   pdl_wait();
   const CacheInfo& c = p.c;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, G = c.group;
@@ -555,31 +553,20 @@ __global__ void __launch_bounds__(32 * kJoinWarps) cache_join_kernel(const __gri
       e1 = __ldcg(src + 1);
     }
     const unsigned set = __ballot_sync(kAll, e0.x != 0);
-    // few rows: every unit gets the most rows that one can have. Row tiles: the rows from a unit's first token to its
-    // sequence's last (a batch of ragged pieces: 32.2 -> 31.2 us for the call)
-    int rows = 0, rows_incl = 0;
-    if (kTiled) {
-      const int toks = e1.y - e1.x, TT = p.tile_tokens;
-      if (e0.x != 0) rows = toks > TT ? kTileM + min(toks - TT, TT) * G : toks * G;
-      rows_incl = warp_incl_scan(rows);
-    }
-    if (lane == 31) s_num[warp] = rows_incl << 6 | __popc(set);  // at most 32 * 256 rows, 32 entries
+    if (lane == 0) s_num[warp] = __popc(set);
     __syncthreads();
-    int at = __popc(set & ((1u << lane) - 1u)), num = 0, row0 = rows_incl - rows, tasks = 0;
+    int at = __popc(set & ((1u << lane) - 1u)), num = 0;
 #pragma unroll
     for (int w = 0; w < kJoinWarps; ++w) {
       const int x = s_num[w];
-      at += w < warp ? x & 63 : 0;
-      num += x & 63;
-      row0 += w < warp ? x >> 6 : 0;
-      tasks += x >> 6;
+      at += w < warp ? x : 0;
+      num += x;
     }
-    if (!kTiled) tasks = num * min(kRowsU, c.max_new * G);
+    const int tasks = num * min(kRowsMax, c.max_new * G);
     if (e0.x != 0) {
       e0.x = b0 + tid;
       s_meta[at][0] = e0;
       s_meta[at][1] = e1;
-      if (kTiled) s_row0[at] = row0;
     }
     __syncthreads();
     if (num == 0) continue;
@@ -588,47 +575,21 @@ __global__ void __launch_bounds__(32 * kJoinWarps) cache_join_kernel(const __gri
     const int per = kJoinWarps / wr, slice = warp % wr;  // rows a block takes at a time
     for (int task0 = blockIdx.x * per; task0 < tasks; task0 += gridDim.x * per) {
       const int task = task0 + warp / wr;
-      int unit = 0, row;
-      if (kTiled) {
-        for (int hi = num - 1; unit < hi;) {  // the entry that the row belongs to
-          const int mid = (unit + hi + 1) >> 1;
-          if (s_row0[mid] <= task) unit = mid; else hi = mid - 1;
-        }
-        row = task - s_row0[unit];
-      } else {
-        row = task / num;
-        unit = task < tasks ? task - row * num : 0;
-      }
+      // rows outermost: the rows that no unit has come last
+      const int row = task / num, unit = task < tasks ? task - row * num : 0;
       const int4 meta = s_meta[unit][0], meta2 = s_meta[unit][1];
-      // meta2: first token and tokens of the sequence (tiled), first packed row and packed rows (not)
+      // meta2: first packed row and packed rows
       const int b = meta.x, P = meta.y - b + 2, seq0 = meta.z, g = meta.w;
-      int tok, head;
-      bool in = task < tasks;
-      if (kTiled) {
-        const int r = row & 127, TT = p.tile_tokens;
-        tok = meta2.x + (row >> 7) * TT + r / G;
-        head = r % G;
-        in = in && r < TT * G && tok < meta2.y;
-      } else {
-        const int pr = meta2.x + row;
-        tok = pr / G;
-        head = pr % G;
-        in = in && pr < meta2.y;
-      }
+      const int pr = meta2.x + row, tok = pr / G, head = pr % G;
+      const bool in = task < tasks && pr < meta2.y;
       float l = 0.f, mu = 0.f;
       float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
       if (in) {
-        auto place = [&](int k) { return (2ll * (b - 1 + k) + (k == 0)) * kRowsU + row; };
+        auto place = [&](int k) { return (2ll * (b - 1 + k) + (k == 0)) * kRowsMax + row; };
         auto ml_of = [&](int k) {
           return k < P ? __ldcg(reinterpret_cast<const float2*>(p.part_ml + 2 * place(k))) : make_float2(-INFINITY, 0.f);
         };
         const float2 ml0 = ml_of(lane);
-        float4 few[4];  // up to four pieces are read beside their maxima (an unwritten one is not used)
-        const bool early = kTiled && P <= 4;
-        if (early)
-#pragma unroll
-          for (int j = 0; j < 4; ++j)
-            if (j < P) few[j] = __ldcg(reinterpret_cast<const float4*>(p.part_o + place(j) * kHeadDim) + lane);
         float m = ml0.x;
         for (int k = lane + 32; k < P; k += 32) m = fmaxf(m, ml_of(k).x);
 #pragma unroll
@@ -639,15 +600,6 @@ __global__ void __launch_bounds__(32 * kJoinWarps) cache_join_kernel(const __gri
           const float w = ml.y != 0.f ? ex2_approx(ml.x - mu) : 0.f;  // sum 0: nothing of the row in this piece
           if (ml.y != 0.f) l += w * ml.y;
           const unsigned use = __ballot_sync(kAll, ml.y != 0.f);      // its O may be unwritten
-          if (early) {
-#pragma unroll
-            for (int j = 0; j < 4; ++j)
-              if (j % wr == slice && ((use >> j) & 1)) {
-                const float wj = __shfl_sync(kAll, w, j);
-                acc.x += wj * few[j].x; acc.y += wj * few[j].y; acc.z += wj * few[j].z; acc.w += wj * few[j].w;
-              }
-            continue;
-          }
           const int top = min(32, P - k0);
 #pragma unroll 8
           for (int j = slice; j < top; j += wr) {
@@ -680,7 +632,7 @@ __global__ void __launch_bounds__(32 * kJoinWarps) cache_join_kernel(const __gri
           make_uint2(pack_bf16x2(acc.x * inv, acc.y * inv), pack_bf16x2(acc.z * inv, acc.w * inv));
       if (lane == 0) {
         const float z = any ? mu + log2f(l) : -INFINITY;
-        if (p.lse2) p.lse2[(long long)h * c.total_tokens + t] = kTiled ? -z : z;
+        if (p.lse2) p.lse2[(long long)h * c.total_tokens + t] = z;
         if (p.lse) p.lse[(long long)h * c.total_tokens + t] = z * 0.6931471805599453f;
       }
     }
@@ -712,17 +664,8 @@ CacheAttnLayout cache_attn_layout(int sms, bool tiled, const CacheInfo& c, bool 
 
 // Every kernel of a call asks for the same split of the SM's memory (the largest shared part): between
 // kernels that differ in it the SM has to drain first, which costs microseconds.
-cudaError_t launch_cache_join(const CacheAttnParams& p, bool tiled, int ctas, int sms, cudaStream_t st) {
-  if (ctas < 2) return cudaSuccess;
-  void (*fn)(const CacheAttnParams, int) = tiled ? cache_join_kernel<true> : cache_join_kernel<false>;
-  static unsigned long long attr[2][kMaxCachedDevices] = {};
-  const cudaError_t e = set_max_smem(reinterpret_cast<const void*>(fn), 0, attr[tiled], true);
-  if (e != cudaSuccess) return e;
-  return launch_pdl(fn, dim3(tiled ? 2 * sms : sms), 32 * kJoinWarps, 0, st, p, ctas);
-}
-
 cudaError_t launch_cache_attn(const CacheAttnParams& p, bool tiled, int sms, cudaStream_t st) {
-  static unsigned long long attr[3][kMaxCachedDevices] = {};
+  static unsigned long long attr[4][kMaxCachedDevices] = {};
   cudaError_t e;
   if (tiled) {
     if ((e = launch_cache_tiles(p, sms, st)) != cudaSuccess || !(p.decay >= 0.f)) return e;
@@ -732,7 +675,9 @@ cudaError_t launch_cache_attn(const CacheAttnParams& p, bool tiled, int sms, cud
   void (*fn)(const CacheAttnParams) = nt == 1 ? cache_rows_kernel<1> : cache_rows_kernel<2>;
   if ((e = set_max_smem(reinterpret_cast<const void*>(fn), kRowSmem, attr[nt - 1], true)) != cudaSuccess) return e;
   if ((e = launch_pdl(fn, dim3(grid), kRowThreads, kRowSmem, st, p)) != cudaSuccess) return e;
-  if ((e = launch_cache_join(p, false, grid, sms, st)) != cudaSuccess || !(p.decay >= 0.f)) return e;
+  if ((e = set_max_smem(reinterpret_cast<const void*>(cache_join_kernel), 0, attr[3], true)) != cudaSuccess) return e;
+  e = launch_pdl(cache_join_kernel, dim3(sms), 32 * kJoinWarps, 0, st, p, grid);
+  if (e != cudaSuccess || !(p.decay >= 0.f)) return e;
   if ((e = set_max_smem(reinterpret_cast<const void*>(cache_rows_weights_kernel), 0, attr[2], true)) != cudaSuccess)
     return e;
   return launch_pdl(cache_rows_weights_kernel, dim3(4 * sms), 256, 0, st, p);

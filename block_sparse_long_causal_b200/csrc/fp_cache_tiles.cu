@@ -672,7 +672,7 @@ __global__ void __launch_bounds__(kThreads, 1) cache_tiles_kernel(const __grid_c
         w0 *= inv;
         w1 *= inv;
       }
-      const long long part = ((long long)pc.slot * 2 + (dual ? 0 : slot)) * 128 + r;  // row of the partial results
+      const long long part0 = (long long)pc.slot * 2 + (dual ? 0 : slot);  // this row tile's partial results
       uint16_t* orow = p.out + (token * c.hq + h) * kHeadDim;
       const int* bad = bad_keys(uc);
       const bool odd = s_bad_unit[uc % kUnitRing] != 0;
@@ -709,13 +709,19 @@ __global__ void __launch_bounds__(kThreads, 1) cache_tiles_kernel(const __grid_c
             uint32_t w[16];
 #pragma unroll
             for (int e = 0; e < 16; ++e) w[e] = pack_bf16x2(__uint_as_float(o[2 * e]), __uint_as_float(o[2 * e + 1]));
-            uint4* dst = reinterpret_cast<uint4*>(orow + b);
+            if (p.out32) {  // a whole sector per thread
+              st_global_v8(orow + b, w);
+              st_global_v8(orow + b + 16, w + 8);
+            } else {
+              uint4* dst = reinterpret_cast<uint4*>(orow + b);
 #pragma unroll
-            for (int e = 0; e < 4; ++e) dst[e] = make_uint4(w[4 * e], w[4 * e + 1], w[4 * e + 2], w[4 * e + 3]);
+              for (int e = 0; e < 4; ++e) dst[e] = make_uint4(w[4 * e], w[4 * e + 1], w[4 * e + 2], w[4 * e + 3]);
+            }
           } else if (!pad) {
-            float* dst = p.part_o + part * kHeadDim + b;
+            // [eight columns][row]: a warp's store is 1 KB in a row (a row of 512 bytes per thread took 2 us longer)
+            float* dst = p.part_o + ((part0 * (kHeadDim / 8) + b / 8) * 128 + r) * 8;
 #pragma unroll
-            for (int e = 0; e < 32; e += 8) st_global_v8(dst + e, o + e);
+            for (int e = 0; e < 32; e += 8) st_global_v8(dst + e * 128, o + e);
           }
           __syncwarp();
         }
@@ -728,7 +734,7 @@ __global__ void __launch_bounds__(kThreads, 1) cache_tiles_kernel(const __grid_c
           if (p.lse2) p.lse2[at] = -z;
           if (p.lse) p.lse[at] = z * 0.6931471805599453f;
         } else {  // a row tile without a key tile in this piece: sum 0, and its O is not read
-          *reinterpret_cast<float2*>(p.part_ml + 2 * part) = make_float2(n > 0 || dual ? m_run : -INFINITY, l_run);
+          *reinterpret_cast<float2*>(p.part_ml + 2 * (part0 * 128 + r)) = make_float2(n > 0 || dual ? m_run : -INFINITY, l_run);
         }
       }
       tc_fence_before();
@@ -752,15 +758,137 @@ __global__ void __launch_bounds__(kThreads, 1) cache_tiles_kernel(const __grid_c
   if (warp == 1) tmem_dealloc(tmem, 512);
 }
 
+// Joins the pieces of the units that several CTAs share. Entry b of meta describes the unit inside of which
+// the part of CTA b begins and is set for the first such CTA of a unit: the unit's pieces are then the last
+// one of CTA b - 1 (place 1) and the first one (place 0) of every CTA from b to meta[1].
+// The time is one chain of dependent reads, so the work is laid out flat: every block lists the set entries, and a
+// warp takes 32 rows (a lane each) and 16 columns of a unit, four pieces in flight at a time.
+constexpr int kJoinThreads = 256, kJoinWarps = kJoinThreads / 32, kJoinBatch = 4;
+__global__ void __launch_bounds__(kJoinThreads) cache_tiles_join_kernel(const __grid_constant__ CacheAttnParams p, int ctas) {
+  __shared__ int4 s_meta[kJoinThreads][2];  // set entries; word 0: the CTA
+  __shared__ int s_first[kJoinThreads], s_num[kJoinWarps];  // tasks of the entries before an entry
+  pdl_wait();
+  const CacheInfo& c = p.c;
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, G = c.group, TT = p.tile_tokens;
+  for (int b0 = 0; b0 < ctas; b0 += kJoinThreads) {  // one round on devices of up to 256 SMs
+    __syncthreads();
+    int4 e0 = make_int4(0, 0, 0, 0), e1 = e0;
+    if (b0 + tid < ctas) {
+      const int4* src = reinterpret_cast<const int4*>(p.meta + (long long)(b0 + tid) * kMetaWords);
+      e0 = __ldcg(src);
+      e1 = __ldcg(src + 1);
+    }
+    const unsigned set = __ballot_sync(kAll, e0.x != 0);
+    int mine = 0;  // 32-row groups of the unit, times 8 column groups
+    if (e0.x != 0) {
+      const int toks = e1.y - e1.x, rows = toks > TT ? 128 + min(toks - TT, TT) * G : toks * G;
+      mine = (rows + 31) / 32 * 8;
+    }
+    const int incl = warp_incl_scan(mine);
+    if (lane == 31) s_num[warp] = incl << 6 | __popc(set);  // at most 32 * 64 tasks, 32 entries
+    __syncthreads();
+    int at = __popc(set & ((1u << lane) - 1u)), num = 0, first = incl - mine, tasks = 0;
+#pragma unroll
+    for (int w = 0; w < kJoinWarps; ++w) {
+      const int x = s_num[w];
+      at += w < warp ? x & 63 : 0;
+      num += x & 63;
+      first += w < warp ? x >> 6 : 0;
+      tasks += x >> 6;
+    }
+    if (e0.x != 0) {
+      e0.x = b0 + tid;
+      s_meta[at][0] = e0;
+      s_meta[at][1] = e1;
+      s_first[at] = first;
+    }
+    __syncthreads();
+    for (int task = blockIdx.x * kJoinWarps + warp; task < tasks; task += gridDim.x * kJoinWarps) {
+      int unit = 0;
+      for (int hi = num - 1; unit < hi;) {  // the entry that the task belongs to
+        const int mid = (unit + hi + 1) >> 1;
+        if (s_first[mid] <= task) unit = mid; else hi = mid - 1;
+      }
+      const int4 meta = s_meta[unit][0], meta2 = s_meta[unit][1];
+      const int b = meta.x, P = meta.y - b + 2, seq0 = meta.z, g = meta.w, tok0 = meta2.x, L = meta2.y;
+      const int cg = (task - s_first[unit]) & 7, row = ((task - s_first[unit]) >> 3) * 32 + lane;
+      const int half = row >> 7, r = row & 127, tok = tok0 + half * TT + r / G;
+      if (r >= TT * G || tok >= L) continue;
+      float m = -INFINITY, l = 0.f, acc[16];
+#pragma unroll
+      for (int e = 0; e < 16; ++e) acc[e] = 0.f;
+      for (int k0 = 0; k0 < P; k0 += kJoinBatch) {
+        float2 ml[kJoinBatch];
+        float4 o[kJoinBatch][4];
+#pragma unroll
+        for (int j = 0; j < kJoinBatch; ++j) {
+          ml[j] = make_float2(-INFINITY, 0.f);
+          if (k0 + j < P) {
+            const long long part0 = (2ll * (b - 1 + k0 + j) + (k0 + j == 0)) * 2 + half;
+            ml[j] = __ldcg(reinterpret_cast<const float2*>(p.part_ml) + part0 * 128 + r);
+            const float* src = p.part_o + ((part0 * (kHeadDim / 8) + 2 * cg) * 128 + r) * 8;
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+              o[j][e] = __ldcg(reinterpret_cast<const float4*>(src + (e >> 1) * 128 * 8) + (e & 1));
+          }
+        }
+        float mn = m;
+#pragma unroll
+        for (int j = 0; j < kJoinBatch; ++j) mn = fmaxf(mn, ml[j].x);
+        const float mu = mn == -INFINITY ? 0.f : mn, a = ex2_approx(m - mu);
+        l *= a;
+#pragma unroll
+        for (int e = 0; e < 16; ++e) acc[e] *= a;
+#pragma unroll
+        for (int j = 0; j < kJoinBatch; ++j)
+          if (ml[j].y != 0.f) {  // sum 0: nothing of the row in this piece, and its O may be unwritten
+            const float w = ex2_approx(ml[j].x - mu);
+            l += w * ml[j].y;
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+              acc[4 * e] += w * o[j][e].x;
+              acc[4 * e + 1] += w * o[j][e].y;
+              acc[4 * e + 2] += w * o[j][e].z;
+              acc[4 * e + 3] += w * o[j][e].w;
+            }
+          }
+        m = mn;
+      }
+      const bool any = l > 0.f || l != l;
+      const float inv = any ? 1.f / l : 0.f;
+      const long long t = (long long)seq0 + tok;
+      const int h = g * G + r % G;
+      uint32_t w[8];
+#pragma unroll
+      for (int e = 0; e < 8; ++e) w[e] = pack_bf16x2(acc[2 * e] * inv, acc[2 * e + 1] * inv);
+      uint16_t* dst = p.out + (t * c.hq + h) * kHeadDim + 16 * cg;
+      if (p.out32) {
+        st_global_v8(dst, w);
+      } else {
+        reinterpret_cast<uint4*>(dst)[0] = make_uint4(w[0], w[1], w[2], w[3]);
+        reinterpret_cast<uint4*>(dst)[1] = make_uint4(w[4], w[5], w[6], w[7]);
+      }
+      if (cg == 0) {
+        const float z = any ? (m == -INFINITY ? 0.f : m) + log2f(l) : -INFINITY;
+        const long long place = (long long)h * c.total_tokens + t;
+        if (p.lse2) p.lse2[place] = -z;
+        if (p.lse) p.lse[place] = z * 0.6931471805599453f;
+      }
+    }
+  }
+}
+
 }  // namespace tiles
 
 cudaError_t launch_cache_tiles(const CacheAttnParams& p, int sms, cudaStream_t st) {
-  static unsigned long long attr[kMaxCachedDevices] = {};
-  cudaError_t e = set_max_smem(reinterpret_cast<const void*>(tiles::cache_tiles_kernel), tiles::smem_bytes(kMaxSeqs), attr);
+  static unsigned long long attr[2][kMaxCachedDevices] = {};
+  cudaError_t e = set_max_smem(reinterpret_cast<const void*>(tiles::cache_tiles_kernel), tiles::smem_bytes(kMaxSeqs), attr[0]);
+  if (e == cudaSuccess)
+    e = set_max_smem(reinterpret_cast<const void*>(tiles::cache_tiles_join_kernel), 0, attr[1], true);
   if (e != cudaSuccess) return e;
   e = launch_pdl(tiles::cache_tiles_kernel, dim3(sms), tiles::kThreads, tiles::smem_bytes(p.c.num_seqs), st, p);
-  if (e != cudaSuccess) return e;
-  return launch_cache_join(p, true, sms, sms, st);
+  if (e != cudaSuccess || sms < 2) return e;
+  return launch_pdl(tiles::cache_tiles_join_kernel, dim3(2 * sms), tiles::kJoinThreads, 0, st, p, sms);
 }
 
 }  // namespace fp

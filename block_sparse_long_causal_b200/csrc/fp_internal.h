@@ -147,7 +147,8 @@ struct __align__(64) CacheAttnParams {
   uint16_t* out;              // [T, Hq, d] bf16 bits
   float* lse;                 // [Hq, T] or null (natural log)
   float* lse2;                // [Hq, T] workspace, log2 units (for the weights; negated by the 128-row schedule), or null
-  float* part_o;              // workspace: partial outputs [2 * grid][rows][128], not normalised
+  bool out32;                 // out is 32-byte aligned
+  float* part_o;              // workspace: partial outputs [2 * grid][rows][128] (row tiles: [..][16][128 rows][8])
   float* part_ml;             // workspace: their running max (log2 units) and row sum, 2 * grid * rows of each
   int32_t* meta;              // workspace: the unit that each CTA's range begins inside of [grid][kMetaWords]
   float* scores;              // workspace: scaled scores [tile of the line][64 keys][score_rows] (few rows), or null
@@ -222,8 +223,6 @@ CacheAttnLayout cache_attn_layout(int sms, bool tiled, const CacheInfo& c, bool 
 cudaError_t launch_cache_attn(const CacheAttnParams& p, bool tiled, int sms, cudaStream_t st);
 cudaError_t launch_cache_tiles(const CacheAttnParams& p, int sms, cudaStream_t st);
 cudaError_t launch_cache_weights(const CacheAttnParams& p, int sms, cudaStream_t st);
-// Joins the pieces of the units that several of `ctas` CTAs shared.
-cudaError_t launch_cache_join(const CacheAttnParams& p, bool tiled, int ctas, int sms, cudaStream_t st);
 cudaError_t launch_exp2_selftest(const float* x, float* y_poly, float* y_mufu, long long n, cudaStream_t st);
 
 }  // namespace fp
