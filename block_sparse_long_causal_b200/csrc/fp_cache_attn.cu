@@ -10,7 +10,8 @@
 // units form one line that the CTAs share out evenly, whatever the lengths: a CTA's share may begin or end
 // inside a unit, and the pieces of such a unit are joined from the workspace by a second kernel. Every
 // warp takes 16 keys of a tile with its own ring of cp.async stages, its own running maximum, row sum and
-// accumulator, so warps never wait for one another inside a unit.
+// accumulator, so warps never wait for one another inside a unit. (A loop of the same copies alone takes 80 us for
+// 537 MB on this GPU, in any order of the heads; this kernel takes 92 us for them, 4 of which find the share.)
 //
 // The products are formed transposed, keys and columns along the 16-row side of the matrix instruction and the
 // unit's rows along its 8-column side (S^T = K Q^T, O^T = V^T P^T): with the four rows of a token over
@@ -24,15 +25,21 @@ namespace fp {
 namespace {
 
 constexpr unsigned kAll = 0xffffffffu;
-constexpr int kRowsMax = 16;                // rows of a unit
+constexpr int kRowsMax = 32;                // rows of a unit
 constexpr int kKeysW = 16;                  // keys of a tile per warp
 constexpr int kWarps = 4, kRowThreads = 32 * kWarps;
 constexpr int kKeysT = kKeysW * kWarps;     // keys of a tile
-constexpr int kStages = 2, kCtasSm = 3;     // 12 warps an SM: fewer leave its schedulers waiting (see below)
 constexpr int kStageBytes = 2 * kKeysW * kHeadDim * 2;  // K then V of one warp's 16 keys
-constexpr int kOffMl = kWarps * kStages * kStageBytes;  // float m[warp][16], l[warp][16]
-constexpr int kRowSmem = kOffMl + 2 * kWarps * kRowsMax * 4;
-static_assert(kRowsMax * kHeadDim * 4 <= kStageBytes, "a consumed stage holds the warp's result when a unit is joined");
+// Up to 16 rows: twelve warps an SM with two stages each, Q in registers (fewer warps leave the schedulers waiting).
+// Up to 32: the accumulators take the registers of eight warps, with three stages, and Q stays in shared memory.
+constexpr int stages(int nt) { return nt <= 2 ? 2 : 3; }
+constexpr int ctas_sm(int nt) { return nt <= 2 ? 3 : 2; }
+constexpr bool q_shared(int nt) { return nt > 2; }
+constexpr int row_tiles(int64_t rows) { return rows <= 8 ? 1 : rows <= 16 ? 2 : 4; }  // of 8 rows: 1, 2 or 4 are built
+constexpr int off_q(int nt) { return kWarps * stages(nt) * kStageBytes; }
+constexpr int off_ml(int nt) { return off_q(nt) + (q_shared(nt) ? 8 * nt * 256 : 0); }  // float m[warp][32], l[warp][32]
+constexpr int row_smem(int nt) { return off_ml(nt) + 2 * kWarps * kRowsMax * 4; }
+static_assert(16 * kHeadDim * 4 <= kStageBytes, "a consumed stage holds 16 rows of the warp's result when a unit is joined");
 
 __device__ __forceinline__ void cp_async16(uint32_t dst, const void* src, bool valid) {
   asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(valid ? 16 : 0) : "memory");
@@ -141,7 +148,9 @@ __device__ __forceinline__ bool find_share(const CacheInfo& c, Shares& sh, Curso
 }
 
 template <int NT>
-__global__ void __launch_bounds__(kRowThreads, kCtasSm) cache_rows_kernel(const __grid_constant__ CacheAttnParams p) {
+__global__ void __launch_bounds__(kRowThreads, ctas_sm(NT)) cache_rows_kernel(const __grid_constant__ CacheAttnParams p) {
+  constexpr int kStages = stages(NT);
+  constexpr bool kQs = q_shared(NT);
   extern __shared__ __align__(1024) unsigned char smem[];
   pdl_wait();
   const CacheInfo& c = p.c;
@@ -221,17 +230,20 @@ __global__ void __launch_bounds__(kRowThreads, kCtasSm) cache_rows_kernel(const 
 #pragma unroll
   for (int i = 0; i < kStages - 1; ++i) load(x0 + i);
 
-  uint32_t qf[NT][8][2];
+  uint32_t qf[kQs ? 1 : NT][8][2];
   // m: the reference maximum; mu: the same, 0 while the row has seen no key; thr: how far above mu a score may lie
   float o[8][NT][4], l[NT][2], m[NT][2], mu[NT][2], thr[NT][2];
-  int last[NT][2];                                // the last key that a row sees
   const int kr = lane >> 2, rc = (lane & 3) * 2;  // this thread's keys kr, kr + 8 and rows rc, rc + 1 (+ 8 t)
-  float* s_m = reinterpret_cast<float*>(smem + kOffMl);
+  float* s_m = reinterpret_cast<float*>(smem + off_ml(NT));
   float* s_l = s_m + kWarps * kRowsMax;
   // ldmatrix rows of this lane: K [key][column] as it lies, V transposed
   const int rk = (lane & 7) + (((lane >> 3) & 1) << 3), rv = (lane & 7) + ((lane >> 4) << 3);
   const uint32_t get_k = rk * 256 + (((lane >> 4) ^ (rk & 7)) << 4);
   const uint32_t get_v = rv * 256 + ((((lane >> 3) & 1) ^ (rv & 7)) << 4);
+  // Q in shared memory: rows lane & 7 of two row tiles, both 8-column halves of a K step
+  const int rq = ((lane >> 4) << 3) + (lane & 7);
+  const uint32_t get_q = smem_u32(smem) + off_q(NT) + rq * 256 + ((((lane >> 3) & 1) ^ (rq & 7)) << 4);
+  auto last_of = [&](int t, int i) { return cur.len + (8 * t + rc + i) / c.group; };  // the last key that a row sees
   bool fresh = true;
   int first_kt = 0, get = 0;
   for (long long x = x0; x < x1; ++x) {
@@ -245,17 +257,28 @@ __global__ void __launch_bounds__(kRowThreads, kCtasSm) cache_rows_kernel(const 
         l[t][0] = l[t][1] = 0.f;
         m[t][0] = m[t][1] = thr[t][0] = thr[t][1] = -INFINITY;
         mu[t][0] = mu[t][1] = 0.f;
-        last[t][0] = cur.len + (8 * t + rc) / c.group;
-        last[t][1] = cur.len + (8 * t + rc + 1) / c.group;
-        const int r = 8 * t + kr;
-        const bool in = r < cur.L * c.group;
-        const uint16_t* q0 = p.q + (long long)(cur.seq0 + (in ? r / c.group : 0)) * p.q_stride +
-                             (cur.g * c.group + (in ? r % c.group : 0)) * kHeadDim + rc;
+        if (!kQs) {
+          const int r = 8 * t + kr;
+          const bool in = r < cur.L * c.group;
+          const uint16_t* q0 = p.q + (long long)(cur.seq0 + (in ? r / c.group : 0)) * p.q_stride +
+                               (cur.g * c.group + (in ? r % c.group : 0)) * kHeadDim + rc;
 #pragma unroll
-        for (int kk = 0; kk < 8; ++kk) {
-          qf[t][kk][0] = in ? __ldg(reinterpret_cast<const uint32_t*>(q0 + kk * 16)) : 0u;
-          qf[t][kk][1] = in ? __ldg(reinterpret_cast<const uint32_t*>(q0 + kk * 16 + 8)) : 0u;
+          for (int kk = 0; kk < 8; ++kk) {
+            qf[kQs ? 0 : t][kk][0] = in ? __ldg(reinterpret_cast<const uint32_t*>(q0 + kk * 16)) : 0u;
+            qf[kQs ? 0 : t][kk][1] = in ? __ldg(reinterpret_cast<const uint32_t*>(q0 + kk * 16 + 8)) : 0u;
+          }
         }
+      }
+      if (kQs) {  // the last unit's join has ended for every warp
+        for (int e = tid; e < 8 * NT * 16; e += kRowThreads) {
+          const int r = e >> 4, ch = e & 15;
+          uint4 y = make_uint4(0, 0, 0, 0);
+          if (r < cur.L * c.group)
+            y = __ldg(reinterpret_cast<const uint4*>(p.q + (long long)(cur.seq0 + r / c.group) * p.q_stride +
+                                                     (cur.g * c.group + r % c.group) * kHeadDim) + ch);
+          *reinterpret_cast<uint4*>(smem + off_q(NT) + r * 256 + ((ch ^ (r & 7)) << 4)) = y;
+        }
+        __syncthreads();
       }
     }
     load(x + kStages - 1);
@@ -275,10 +298,23 @@ __global__ void __launch_bounds__(kRowThreads, kCtasSm) cache_rows_kernel(const 
         uint32_t a[4], b[4];
         ldsm4((sk + get_k) ^ (kk << 5), a);
         ldsm4((sk + get_k) ^ ((kk + 1) << 5), b);
+        if (kQs) {
 #pragma unroll
-        for (int t = 0; t < NT; ++t) {
-          mma16816(sc[t], a, qf[t][kk][0], qf[t][kk][1]);
-          mma16816(s2[t], b, qf[t][kk + 1][0], qf[t][kk + 1][1]);
+          for (int t = 0; t < NT; t += 2) {
+            uint32_t q0[4], q1[4];
+            ldsm4((get_q ^ (kk << 5)) + t * 8 * 256, q0);
+            ldsm4((get_q ^ ((kk + 1) << 5)) + t * 8 * 256, q1);
+            mma16816(sc[t], a, q0[0], q0[1]);
+            mma16816(sc[t + 1], a, q0[2], q0[3]);
+            mma16816(s2[t], b, q1[0], q1[1]);
+            mma16816(s2[t + 1], b, q1[2], q1[3]);
+          }
+        } else {
+#pragma unroll
+          for (int t = 0; t < NT; ++t) {
+            mma16816(sc[t], a, qf[kQs ? 0 : t][kk][0], qf[kQs ? 0 : t][kk][1]);
+            mma16816(s2[t], b, qf[kQs ? 0 : t][kk + 1][0], qf[kQs ? 0 : t][kk + 1][1]);
+          }
         }
       }
 #pragma unroll
@@ -294,16 +330,16 @@ __global__ void __launch_bounds__(kRowThreads, kCtasSm) cache_rows_kernel(const 
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
           const int key = key0 + kr + (e >> 1) * 8;
-          if (key > last[t][e & 1] || key >= cur.n) sc[t][e] = -INFINITY;
+          if (key > last_of(t, e & 1) || key >= cur.n) sc[t][e] = -INFINITY;
         }
     }
-    if (p.scores) {  // for the weights pass: 64 keys x score_rows of a tile
-      float* dst = p.scores + (x * kKeysT + warp * kKeysW + kr) * p.score_rows;
+    if (p.scores) {  // for the weights pass: [four rows][64 keys][4] of a tile, so that both sides go 128 bytes at a time
+      float* dst = p.scores + (x * p.score_rows + rc / 4 * 4) * kKeysT + (warp * kKeysW + kr) * 4 + (rc & 2);
 #pragma unroll
       for (int t = 0; t < NT; ++t)
         if (8 * t + rc < p.score_rows) {
-          *reinterpret_cast<float2*>(dst + 8 * t + rc) = make_float2(sc[t][0] * p.scale_log2, sc[t][1] * p.scale_log2);
-          *reinterpret_cast<float2*>(dst + 8 * p.score_rows + 8 * t + rc) =
+          *reinterpret_cast<float2*>(dst + 8 * t * kKeysT) = make_float2(sc[t][0] * p.scale_log2, sc[t][1] * p.scale_log2);
+          *reinterpret_cast<float2*>(dst + 8 * t * kKeysT + 32) =
               make_float2(sc[t][2] * p.scale_log2, sc[t][3] * p.scale_log2);
         }
     }
@@ -374,7 +410,7 @@ __global__ void __launch_bounds__(kRowThreads, kCtasSm) cache_rows_kernel(const 
             for (int t = 0; t < NT; ++t)
 #pragma unroll
               for (int i = 0; i < 2; ++i)
-                if (key0 + k <= last[t][i]) o[j >> 1][t][2 * (j & 1) + i] += f;
+                if (key0 + k <= last_of(t, i)) o[j >> 1][t][2 * (j & 1) + i] += f;
           }
         __syncwarp();
         for (int e = lane; e < kKeysW * kHeadDim; e += 32) {
@@ -410,59 +446,62 @@ __global__ void __launch_bounds__(kRowThreads, kCtasSm) cache_rows_kernel(const 
           }
         }
       __syncthreads();
-      float* s_o = reinterpret_cast<float*>(smem + (sk - smem_u32(smem)));  // [row][128], columns swizzled
-#pragma unroll
-      for (int t = 0; t < NT; ++t)
-#pragma unroll
-        for (int i = 0; i < 2; ++i) {
-          const int r = 8 * t + rc + i;
-          float mt = s_m[r];
-          for (int k = 1; k < kWarps; ++k) mt = fmaxf(mt, s_m[k * kRowsMax + r]);
-          const float w = ex2_approx(m[t][i] - (mt == -INFINITY ? 0.f : mt));
-          const int swz = ((r >> 1) & 3) * 8;
-#pragma unroll
-          for (int j = 0; j < 8; ++j) {
-            s_o[r * kHeadDim + ((16 * j + kr) ^ swz)] = o[j][t][i] * w;
-            s_o[r * kHeadDim + ((16 * j + 8 + kr) ^ swz)] = o[j][t][2 + i] * w;
-          }
-        }
-      __syncthreads();
+      float* s_o = reinterpret_cast<float*>(smem + (sk - smem_u32(smem)));  // [row of 16][128], columns swizzled
       const bool whole = ends && first_kt == 0;
       const long long slot = 2ll * blockIdx.x + (first_kt == 0 ? 1 : 0);  // a piece from a unit's start: place 1
-      // thread: four columns of every fourth row
-      const int cc = lane * 4;
-      for (int r = warp; r < cur.L * c.group; r += kWarps) {
-        float mt = s_m[r];
-        for (int k = 1; k < kWarps; ++k) mt = fmaxf(mt, s_m[k * kRowsMax + r]);
-        const float mu = mt == -INFINITY ? 0.f : mt;
-        float lt = 0.f;
-        for (int k = 0; k < kWarps; ++k) lt += s_l[k * kRowsMax + r] * ex2_approx(s_m[k * kRowsMax + r] - mu);
-        const float* src = reinterpret_cast<const float*>(smem + get * kStageBytes) + r * kHeadDim +
-                           (cc ^ (((r >> 1) & 3) * 8));
-        float4 a = *reinterpret_cast<const float4*>(src);
-        for (int k = 1; k < kWarps; ++k) {
-          const float4 b = *reinterpret_cast<const float4*>(src + k * (kStages * kStageBytes / 4));
-          a.x += b.x; a.y += b.y; a.z += b.z; a.w += b.w;
-        }
-        if (!whole) {
-          *reinterpret_cast<float4*>(p.part_o + (slot * kRowsMax + r) * kHeadDim + cc) = a;
-          if (lane == 0) *reinterpret_cast<float2*>(p.part_ml + 2 * (slot * kRowsMax + r)) = make_float2(mt, lt);
-        } else {
-          const bool any = lt > 0.f || lt != lt;
-          const float inv = any ? 1.f / lt : 0.f;
-          const long long t = (long long)cur.seq0 + r / c.group;
-          const int h = cur.g * c.group + r % c.group;
-          *reinterpret_cast<uint2*>(p.out + (t * c.hq + h) * kHeadDim + cc) =
-              make_uint2(pack_bf16x2(a.x * inv, a.y * inv), pack_bf16x2(a.z * inv, a.w * inv));
-          if (lane == 0) {
-            const float z = any ? mu + log2f(lt) : -INFINITY;
-            const long long at = (long long)h * c.total_tokens + t;
-            if (p.lse2) p.lse2[at] = z;
-            if (p.lse) p.lse[at] = z * 0.6931471805599453f;
+#pragma unroll
+      for (int r0 = 0; r0 < 8 * NT; r0 += 16) {
+#pragma unroll
+        for (int t = r0 / 8; t < NT && t < r0 / 8 + 2; ++t)
+#pragma unroll
+          for (int i = 0; i < 2; ++i) {
+            const int r = 8 * t + rc + i;
+            float mt = s_m[r];
+            for (int k = 1; k < kWarps; ++k) mt = fmaxf(mt, s_m[k * kRowsMax + r]);
+            const float w = ex2_approx(m[t][i] - (mt == -INFINITY ? 0.f : mt));
+            const int swz = ((r >> 1) & 3) * 8;
+#pragma unroll
+            for (int j = 0; j < 8; ++j) {
+              s_o[(r - r0) * kHeadDim + ((16 * j + kr) ^ swz)] = o[j][t][i] * w;
+              s_o[(r - r0) * kHeadDim + ((16 * j + 8 + kr) ^ swz)] = o[j][t][2 + i] * w;
+            }
+          }
+        __syncthreads();
+        // thread: four columns of every fourth row
+        const int cc = lane * 4;
+        for (int r = r0 + warp; r < min(r0 + 16, cur.L * c.group); r += kWarps) {
+          float mt = s_m[r];
+          for (int k = 1; k < kWarps; ++k) mt = fmaxf(mt, s_m[k * kRowsMax + r]);
+          const float mu_r = mt == -INFINITY ? 0.f : mt;
+          float lt = 0.f;
+          for (int k = 0; k < kWarps; ++k) lt += s_l[k * kRowsMax + r] * ex2_approx(s_m[k * kRowsMax + r] - mu_r);
+          const float* src = reinterpret_cast<const float*>(smem + get * kStageBytes) + (r - r0) * kHeadDim +
+                             (cc ^ (((r >> 1) & 3) * 8));
+          float4 a = *reinterpret_cast<const float4*>(src);
+          for (int k = 1; k < kWarps; ++k) {
+            const float4 b = *reinterpret_cast<const float4*>(src + k * (kStages * kStageBytes / 4));
+            a.x += b.x; a.y += b.y; a.z += b.z; a.w += b.w;
+          }
+          if (!whole) {
+            *reinterpret_cast<float4*>(p.part_o + (slot * kRowsMax + r) * kHeadDim + cc) = a;
+            if (lane == 0) *reinterpret_cast<float2*>(p.part_ml + 2 * (slot * kRowsMax + r)) = make_float2(mt, lt);
+          } else {
+            const bool any = lt > 0.f || lt != lt;
+            const float inv = any ? 1.f / lt : 0.f;
+            const long long t = (long long)cur.seq0 + r / c.group;
+            const int h = cur.g * c.group + r % c.group;
+            *reinterpret_cast<uint2*>(p.out + (t * c.hq + h) * kHeadDim + cc) =
+                make_uint2(pack_bf16x2(a.x * inv, a.y * inv), pack_bf16x2(a.z * inv, a.w * inv));
+            if (lane == 0) {
+              const float z = any ? mu_r + log2f(lt) : -INFINITY;
+              const long long at = (long long)h * c.total_tokens + t;
+              if (p.lse2) p.lse2[at] = z;
+              if (p.lse) p.lse[at] = z * 0.6931471805599453f;
+            }
           }
         }
+        __syncthreads();
       }
-      __syncthreads();
       fresh = true;
     }
     get = get + 1 == kStages ? 0 : get + 1;
@@ -492,7 +531,7 @@ __global__ void __launch_bounds__(256) cache_rows_weights_kernel(const __grid_co
                                lane / c.group)
                       : INFINITY;
     }
-    const float* sc = p.scores + (x * kKeysT + lane) * rs;
+    const float4* sc = reinterpret_cast<const float4*>(p.scores) + x * (rs / 4) * kKeysT + lane;
     long long at[2];
     float old[2] = {0.f, 0.f}, w[2] = {0.f, 0.f};
 #pragma unroll
@@ -501,27 +540,18 @@ __global__ void __launch_bounds__(256) cache_rows_weights_kernel(const __grid_co
       at[i] = key < u.n ? slot_word(c, s, g, key) : -1;  // a bad page was flagged by the attention
       if (at[i] >= 0 && p.decay > 0.f) old[i] = c.weights[at[i]];
     }
-    if (rs == 4) {  // one token of a group of three or four heads: a key's scores are 16 bytes (128K keys: 0.8 us less)
-      const float4 v0 = __ldcg(reinterpret_cast<const float4*>(sc)), v1 = __ldcg(reinterpret_cast<const float4*>(sc + 128));
-      const float a[2][4] = {{v0.x, v0.y, v0.z, v0.w}, {v1.x, v1.y, v1.z, v1.w}};
+#pragma unroll 2
+    for (int r = 0; r < rows; r += 4, sc += kKeysT) {
+      float zr[4];
 #pragma unroll
-      for (int r = 0; r < 4; ++r) {
-        const float zr = __shfl_sync(kAll, z, r);
-        if (r < rows) {
-          w[0] += ex2_approx(a[0][r] - zr);
-          w[1] += ex2_approx(a[1][r] - zr);
-        }
-      }
-    } else {
-#pragma unroll 4
-      for (int r = 0; r < rows; r += 2) {
-        const float z0 = __shfl_sync(kAll, z, r), z1 = __shfl_sync(kAll, z, r + 1);
+      for (int j = 0; j < 4; ++j) zr[j] = __shfl_sync(kAll, z, r + j);
 #pragma unroll
-        for (int i = 0; i < 2; ++i) {
-          const float2 v = __ldcg(reinterpret_cast<const float2*>(sc + 32 * i * rs + r));
-          w[i] += ex2_approx(v.x - z0);
-          if (r + 1 < rows) w[i] += ex2_approx(v.y - z1);
-        }
+      for (int i = 0; i < 2; ++i) {
+        const float4 v = __ldcg(sc + 32 * i);
+        w[i] += ex2_approx(v.x - zr[0]);
+        if (r + 1 < rows) w[i] += ex2_approx(v.y - zr[1]);
+        if (r + 2 < rows) w[i] += ex2_approx(v.z - zr[2]);
+        if (r + 3 < rows) w[i] += ex2_approx(v.w - zr[3]);
       }
     }
 #pragma unroll
@@ -641,18 +671,23 @@ __global__ void __launch_bounds__(32 * kJoinWarps) cache_join_kernel(const __gri
 
 }  // namespace
 
+// Few rows: up to 32 packed rows a sequence. Where both schedules run, at 32 q-heads over 8 kv-heads, the call takes
+// (this one / the 128-row one, us): one sequence of 2K keys, 4 rows 10.5 / 19.0, 16 rows 13.8 / 19.7, 32 rows 15.5 / 21.2;
+// 32K keys, 16 rows 35.6 / 46.0, 32 rows 45.3 / 52.0; with weights 45.3 / 73.0 and 62.1 / 79.1; 32 sequences of 4K, 16 rows 97.9 /
+// 105.1, 32 rows 109.5 / 106.6.
 bool cache_attn_tiled(int32_t max_new, int32_t group) { return (int64_t)max_new * group > kRowsMax; }
 
 CacheAttnLayout cache_attn_layout(int sms, bool tiled, const CacheInfo& c, bool scores) {
   auto up = [](int64_t x) { return (x + 255) & ~(int64_t)255; };
-  const int64_t grid = tiled ? sms : kCtasSm * sms, rows = 2 * grid * (tiled ? 2 * kTileM : kRowsMax);
+  const int64_t grid = tiled ? sms : ctas_sm(row_tiles((int64_t)c.max_new * c.group)) * sms;
+  const int64_t rows = 2 * grid * (tiled ? 2 * kTileM : kRowsMax);
   CacheAttnLayout w;
   w.part_o = 0;
   w.part_ml = up(w.part_o + rows * kHeadDim * 4);
   w.meta = up(w.part_ml + rows * 2 * 4);
   w.lse2 = up(w.meta + grid * kMetaWords * 4);
   w.scores = up(w.lse2 + (int64_t)c.hq * c.total_tokens * 4);
-  w.score_rows = (c.max_new * c.group + 1) / 2 * 2;
+  w.score_rows = (c.max_new * c.group + 3) / 4 * 4;
   // tiles of a call that writes weights: by the longest sequence that there may be, and by the pages, which no
   // two sequences share then
   const int64_t by_len = (int64_t)c.num_seqs * ((c.max_len + kKeysT - 1) / kKeysT);
@@ -665,20 +700,20 @@ CacheAttnLayout cache_attn_layout(int sms, bool tiled, const CacheInfo& c, bool 
 // Every kernel of a call asks for the same split of the SM's memory (the largest shared part): between
 // kernels that differ in it the SM has to drain first, which costs microseconds.
 cudaError_t launch_cache_attn(const CacheAttnParams& p, bool tiled, int sms, cudaStream_t st) {
-  static unsigned long long attr[4][kMaxCachedDevices] = {};
+  static unsigned long long attr[2][kMaxCachedDevices] = {}, attr_rows[5][kMaxCachedDevices] = {};
   cudaError_t e;
   if (tiled) {
     if ((e = launch_cache_tiles(p, sms, st)) != cudaSuccess || !(p.decay >= 0.f)) return e;
     return launch_cache_weights(p, sms, st);
   }
-  const int nt = p.c.max_new * p.c.group <= 8 ? 1 : 2, grid = kCtasSm * sms;
-  void (*fn)(const CacheAttnParams) = nt == 1 ? cache_rows_kernel<1> : cache_rows_kernel<2>;
-  if ((e = set_max_smem(reinterpret_cast<const void*>(fn), kRowSmem, attr[nt - 1], true)) != cudaSuccess) return e;
-  if ((e = launch_pdl(fn, dim3(grid), kRowThreads, kRowSmem, st, p)) != cudaSuccess) return e;
-  if ((e = set_max_smem(reinterpret_cast<const void*>(cache_join_kernel), 0, attr[3], true)) != cudaSuccess) return e;
+  const int nt = row_tiles((int64_t)p.c.max_new * p.c.group), grid = ctas_sm(nt) * sms;
+  void (*fn)(const CacheAttnParams) = nt == 1 ? cache_rows_kernel<1> : nt == 2 ? cache_rows_kernel<2> : cache_rows_kernel<4>;
+  if ((e = set_max_smem(reinterpret_cast<const void*>(fn), row_smem(nt), attr_rows[nt], true)) != cudaSuccess) return e;
+  if ((e = launch_pdl(fn, dim3(grid), kRowThreads, row_smem(nt), st, p)) != cudaSuccess) return e;
+  if ((e = set_max_smem(reinterpret_cast<const void*>(cache_join_kernel), 0, attr[0], true)) != cudaSuccess) return e;
   e = launch_pdl(cache_join_kernel, dim3(sms), 32 * kJoinWarps, 0, st, p, grid);
   if (e != cudaSuccess || !(p.decay >= 0.f)) return e;
-  if ((e = set_max_smem(reinterpret_cast<const void*>(cache_rows_weights_kernel), 0, attr[2], true)) != cudaSuccess)
+  if ((e = set_max_smem(reinterpret_cast<const void*>(cache_rows_weights_kernel), 0, attr[1], true)) != cudaSuccess)
     return e;
   return launch_pdl(cache_rows_weights_kernel, dim3(4 * sms), 256, 0, st, p);
 }

@@ -151,7 +151,7 @@ struct __align__(64) CacheAttnParams {
   float* part_o;              // workspace: partial outputs [2 * grid][rows][128] (row tiles: [..][16][128 rows][8])
   float* part_ml;             // workspace: their running max (log2 units) and row sum, 2 * grid * rows of each
   int32_t* meta;              // workspace: the unit that each CTA's range begins inside of [grid][kMetaWords]
-  float* scores;              // workspace: scaled scores [tile of the line][64 keys][score_rows] (few rows), or null
+  float* scores;              // workspace: scaled scores [tile of the line][score_rows / 4][64 keys][4] (few rows), or null
   int32_t score_rows;
   int64_t score_tiles;        // tiles that fit
   float decay;                // weights = decay * weights + this call's; < 0: weights are left alone

@@ -375,9 +375,10 @@ FP_API fp_status fp_cache_append(const fp_problem* p, const fp_kv_cache* c, cons
                                  void* stream);
 
 /* Bytes of workspace that fp_cache_attn needs (for the current device). It depends on the problem's sizes, on
- * max_new and, when the cache has weights, on max_len and num_pages (scores of single tokens and short
- * drafts, 4 bytes per slot and q-head: fp_cache_attn with decay >= 0 flags FP_DEV_BAD_PROBLEM and does no work
- * when sequences that share pages have more slots than the cache). */
+ * max_new and, when the cache has weights and max_new * Hq / Hkv is at most 32, on max_len and num_pages: the
+ * scores of every slot, 4 bytes per new token and q-head (max_new * Hq / Hkv rounded up to a multiple of 4).
+ * fp_cache_attn with decay >= 0 flags FP_DEV_BAD_PROBLEM and does no work when sequences that share pages have
+ * more slots than the cache. */
 FP_API fp_status fp_cache_attn_workspace(const fp_problem* p, const fp_kv_cache* c, int64_t* bytes);
 
 /* Attention of the new tokens over the cache (dense: every slot 0 .. lens[s] + t), for one token per
