@@ -518,8 +518,8 @@ def cache_attn(p: Problem, c: KVCache, q, softmax_scale: float, workspace, out, 
     rows = c.tokens * c.hq
     op = _want(out, "out", torch.bfloat16, c.device, rows * c.d)
     lp = None if lse is None else _want(lse, "lse", torch.float32, c.device, rows)
-    if workspace.device != c.device or not workspace.is_contiguous():
-        raise ValueError(f"workspace must be contiguous on {c.device}")
+    if not isinstance(workspace, torch.Tensor) or workspace.device != c.device or not workspace.is_contiguous():
+        raise ValueError(f"workspace must be a contiguous tensor on {c.device}")
     if decay is None:
         decay = -1.0
     elif not 0.0 <= decay <= 1.0:

@@ -762,11 +762,13 @@ __global__ void __launch_bounds__(kThreads, 1) cache_tiles_kernel(const __grid_c
 // the part of CTA b begins and is set for the first such CTA of a unit: the unit's pieces are then the last
 // one of CTA b - 1 (place 1) and the first one (place 0) of every CTA from b to meta[1].
 // The time is one chain of dependent reads, so the work is laid out flat: every block lists the set entries, and a
-// warp takes 32 rows (a lane each) and 16 columns of a unit, four pieces in flight at a time.
+// warp takes 32 rows (a lane each) and 16 columns of a unit, four pieces in flight at a time; where there are fewer
+// such tasks than warps, up to eight warps of a block share a task's pieces.
 constexpr int kJoinThreads = 256, kJoinWarps = kJoinThreads / 32, kJoinBatch = 4;
 __global__ void __launch_bounds__(kJoinThreads) cache_tiles_join_kernel(const __grid_constant__ CacheAttnParams p, int ctas) {
   __shared__ int4 s_meta[kJoinThreads][2];  // set entries; word 0: the CTA
   __shared__ int s_first[kJoinThreads], s_num[kJoinWarps];  // tasks of the entries before an entry
+  __shared__ float s_acc[kJoinWarps][18][32];               // maximum, sum and columns of a warp's pieces
   pdl_wait();
   const CacheInfo& c = p.c;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, G = c.group, TT = p.tile_tokens;
@@ -803,7 +805,11 @@ __global__ void __launch_bounds__(kJoinThreads) cache_tiles_join_kernel(const __
       s_first[at] = first;
     }
     __syncthreads();
-    for (int task = blockIdx.x * kJoinWarps + warp; task < tasks; task += gridDim.x * kJoinWarps) {
+    int wr = 1;  // warps that share a task
+    while (wr < kJoinWarps && 2ll * wr * tasks <= (long long)gridDim.x * kJoinWarps) wr *= 2;
+    const int per = kJoinWarps / wr, slice = warp % wr;  // tasks a block takes at a time
+    for (int task0 = blockIdx.x * per; task0 < tasks; task0 += gridDim.x * per) {
+      const int task = min(task0 + warp / wr, tasks - 1);
       int unit = 0;
       for (int hi = num - 1; unit < hi;) {  // the entry that the task belongs to
         const int mid = (unit + hi + 1) >> 1;
@@ -813,18 +819,20 @@ __global__ void __launch_bounds__(kJoinThreads) cache_tiles_join_kernel(const __
       const int b = meta.x, P = meta.y - b + 2, seq0 = meta.z, g = meta.w, tok0 = meta2.x, L = meta2.y;
       const int cg = (task - s_first[unit]) & 7, row = ((task - s_first[unit]) >> 3) * 32 + lane;
       const int half = row >> 7, r = row & 127, tok = tok0 + half * TT + r / G;
-      if (r >= TT * G || tok >= L) continue;
+      const bool in = task0 + warp / wr < tasks && r < TT * G && tok < L;
       float m = -INFINITY, l = 0.f, acc[16];
 #pragma unroll
       for (int e = 0; e < 16; ++e) acc[e] = 0.f;
-      for (int k0 = 0; k0 < P; k0 += kJoinBatch) {
+      // pieces slice, slice + wr, ...
+      for (int k0 = in ? slice : P; k0 < P; k0 += kJoinBatch * wr) {
         float2 ml[kJoinBatch];
         float4 o[kJoinBatch][4];
 #pragma unroll
         for (int j = 0; j < kJoinBatch; ++j) {
           ml[j] = make_float2(-INFINITY, 0.f);
-          if (k0 + j < P) {
-            const long long part0 = (2ll * (b - 1 + k0 + j) + (k0 + j == 0)) * 2 + half;
+          const int k = k0 + j * wr;
+          if (k < P) {
+            const long long part0 = (2ll * (b - 1 + k) + (k == 0)) * 2 + half;
             ml[j] = __ldcg(reinterpret_cast<const float2*>(p.part_ml) + part0 * 128 + r);
             const float* src = p.part_o + ((part0 * (kHeadDim / 8) + 2 * cg) * 128 + r) * 8;
 #pragma unroll
@@ -854,6 +862,30 @@ __global__ void __launch_bounds__(kJoinThreads) cache_tiles_join_kernel(const __
           }
         m = mn;
       }
+      if (wr > 1) {
+        s_acc[warp][0][lane] = m;
+        s_acc[warp][1][lane] = l;
+#pragma unroll
+        for (int e = 0; e < 16; ++e) s_acc[warp][2 + e][lane] = acc[e];
+        __syncthreads();
+        if (slice == 0) {
+          float mt = m;
+          for (int q = 1; q < wr; ++q) mt = fmaxf(mt, s_acc[warp + q][0][lane]);
+          const float mu = mt == -INFINITY ? 0.f : mt, a = ex2_approx(m - mu);
+          l *= a;
+#pragma unroll
+          for (int e = 0; e < 16; ++e) acc[e] *= a;
+          for (int q = 1; q < wr; ++q) {
+            const float w = ex2_approx(s_acc[warp + q][0][lane] - mu);
+            l += w * s_acc[warp + q][1][lane];
+#pragma unroll
+            for (int e = 0; e < 16; ++e) acc[e] += w * s_acc[warp + q][2 + e][lane];
+          }
+          m = mt;
+        }
+        __syncthreads();
+      }
+      if (!in || slice != 0) continue;
       const bool any = l > 0.f || l != l;
       const float inv = any ? 1.f / l : 0.f;
       const long long t = (long long)seq0 + tok;
