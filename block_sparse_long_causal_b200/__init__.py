@@ -393,24 +393,29 @@ def paged_validate_lists(p: Problem, c: PagedCache, counts, indices, dev_status,
                                         _stream(stream)))
 
 
+# The cache calls are made once per token and layer: their checks are plain attribute reads, and names that are
+# looked up at every call are bound here.
+_Tensor, _BF16, _I32 = torch.Tensor, torch.bfloat16, torch.int32
+
+
 def _rows_of(t, name: str, tokens: int, heads: int, d: int, device):
     """Pointer and token-row stride of a bf16 [tokens, heads, head_dim] tensor whose rows may lie apart (a
     slice of a fused projection)."""
-    _want(t, name, torch.bfloat16, device)
+    if not isinstance(t, _Tensor) or t.dtype is not _BF16 or t.device != device:
+        _want(t, name, _BF16, device)  # says what is wrong
     if t.shape != (tokens, heads, d):
         raise ValueError(f"{name} must be [{tokens}, {heads}, {d}], got {list(t.shape)}")
     if tokens == 0:
         return None, 0
-    st = t.stride()
-    if st[2] != 1 or (heads > 1 and st[1] != d):
+    row, head, col = t.stride()
+    if col != 1 or (head != d and heads > 1):
         raise ValueError(f"{name}: the heads of a token must be contiguous")
-    return t.data_ptr(), st[0] if tokens > 1 else 0
+    return t.data_ptr(), row if tokens > 1 else 0
 
 
 def _want(t, name: str, dtype, device, numel=None) -> int:
-    """Check a tensor argument; its address. These calls are made once per token and layer: the checks are
-    plain attribute reads."""
-    if not isinstance(t, torch.Tensor):
+    """Check a tensor argument; its address."""
+    if not isinstance(t, _Tensor):
         raise ValueError(f"{name} must be a tensor")
     if t.dtype is not dtype:
         raise ValueError(f"{name} must be {dtype}, got {t.dtype}")
@@ -463,6 +468,7 @@ class KVCache:
         self.ref, self.p_ref = C.byref(self.c), p.ref
         self.tokens, self.seqs = int(p.total_tokens), int(p.num_seqs)
         self.hq, self.hkv, self.d = int(p.num_q_heads), hkv, d
+        self.index = dev.index if dev.type == "cuda" else -1
 
     def __getattr__(self, name):
         return getattr(self.__dict__["c"], name)
@@ -477,20 +483,19 @@ def _cache_args(p: Problem, c: KVCache, next_pos, dev_status):
     """Addresses of next_pos and dev_status (None: NULL)."""
     if p is not c.p:
         raise ValueError("the cache was described for another problem (kv_cache(p, ...))")
-    return (None if next_pos is None else _want(next_pos, "next_pos", torch.int32, c.device, c.seqs),
-            None if dev_status is None else _want(dev_status, "dev_status", torch.int32, c.device, 1))
+    return (None if next_pos is None else _want(next_pos, "next_pos", _I32, c.device, c.seqs),
+            None if dev_status is None else _want(dev_status, "dev_status", _I32, c.device, 1))
 
 
-def _call(c: KVCache, fn, *args, stream):
+def _call(c: KVCache, stream, fn, *args):
     """fn on the cache's device, on `stream` or that device's current one."""
-    dev = c.device
-    if dev.type != "cuda":
-        raise ValueError(f"the cache is on {dev}: the kernels run on a CUDA device only")
-    if torch.cuda.current_device() != dev.index:
-        with torch.cuda.device(dev):
-            return _call(c, fn, *args, stream=stream)
-    raw = torch._C._cuda_getCurrentRawStream(dev.index) if stream is None else _stream(stream)
-    st = fn(c.p_ref, c.ref, *args, raw)
+    index = c.index
+    if index < 0:
+        raise ValueError(f"the cache is on {c.device}: the kernels run on a CUDA device only")
+    if torch._C._cuda_getDevice() != index:
+        with torch.cuda.device(index):
+            return _call(c, stream, fn, *args)
+    st = fn(c.p_ref, c.ref, *args, torch._C._cuda_getCurrentRawStream(index) if stream is None else _stream(stream))
     if st != FP_OK:
         _check(st)
 
@@ -500,7 +505,7 @@ def cache_append(p: Problem, c: KVCache, k, v, next_pos=None, dev_status=None, s
     pos, status = _cache_args(p, c, next_pos, dev_status)
     kp, ks = _rows_of(k, "k", c.tokens, c.hkv, c.d, c.device)
     vp, vs = _rows_of(v, "v", c.tokens, c.hkv, c.d, c.device)
-    _call(c, _lib.fp_cache_append, kp, ks, vp, vs, pos, status, stream=stream)
+    _call(c, stream, _lib.fp_cache_append, kp, ks, vp, vs, pos, status)
 
 
 def cache_attn_workspace(p: Problem, c: KVCache) -> int:
@@ -516,7 +521,7 @@ def cache_attn(p: Problem, c: KVCache, q, softmax_scale: float, workspace, out, 
     _, status = _cache_args(p, c, None, dev_status)
     qp, qs = _rows_of(q, "q", c.tokens, c.hq, c.d, c.device)
     rows = c.tokens * c.hq
-    op = _want(out, "out", torch.bfloat16, c.device, rows * c.d)
+    op = _want(out, "out", _BF16, c.device, rows * c.d)
     lp = None if lse is None else _want(lse, "lse", torch.float32, c.device, rows)
     if not isinstance(workspace, torch.Tensor) or workspace.device != c.device or not workspace.is_contiguous():
         raise ValueError(f"workspace must be a contiguous tensor on {c.device}")
@@ -524,15 +529,15 @@ def cache_attn(p: Problem, c: KVCache, q, softmax_scale: float, workspace, out, 
         decay = -1.0
     elif not 0.0 <= decay <= 1.0:
         raise ValueError("decay must be in [0, 1]")
-    _call(c, _lib.fp_cache_attn, qp, qs, softmax_scale, workspace.data_ptr(),
-          workspace.numel() * workspace.element_size(), op, lp, decay, status, stream=stream)
+    _call(c, stream, _lib.fp_cache_attn, qp, qs, softmax_scale, workspace.data_ptr(),
+          workspace.numel() * workspace.element_size(), op, lp, decay, status)
 
 
 def _move_args(c: KVCache, budget: int, moves, move_counts, new_lens):
     n = c.seqs * c.hkv
-    return (_want(moves, "moves", torch.int32, c.device, 2 * n * budget),
-            _want(move_counts, "move_counts", torch.int32, c.device, n),
-            _want(new_lens, "new_lens", torch.int32, c.device, c.seqs))
+    return (_want(moves, "moves", _I32, c.device, 2 * n * budget),
+            _want(move_counts, "move_counts", _I32, c.device, n),
+            _want(new_lens, "new_lens", _I32, c.device, c.seqs))
 
 
 def cache_select(p: Problem, c: KVCache, budget: int, sinks: int, recent: int, next_pos, moves, move_counts, new_lens,
@@ -540,14 +545,14 @@ def cache_select(p: Problem, c: KVCache, budget: int, sinks: int, recent: int, n
     """fp_cache_select: the slots that stay, as moves int32 [num_seqs, Hkv, budget, 2]."""
     pos, status = _cache_args(p, c, next_pos, dev_status)
     out = _move_args(c, budget, moves, move_counts, new_lens)
-    _call(c, _lib.fp_cache_select, budget, sinks, recent, pos, *out, status, stream=stream)
+    _call(c, stream, _lib.fp_cache_select, budget, sinks, recent, pos, *out, status)
 
 
 def cache_compact(p: Problem, c: KVCache, budget: int, moves, move_counts, new_lens, dev_status=None, stream=None):
     """fp_cache_compact: apply the moves of cache_select and set lens."""
     _, status = _cache_args(p, c, None, dev_status)
     out = _move_args(c, budget, moves, move_counts, new_lens)
-    _call(c, _lib.fp_cache_compact, budget, *out, status, stream=stream)
+    _call(c, stream, _lib.fp_cache_compact, budget, *out, status)
 
 
 class SparsePrefill:

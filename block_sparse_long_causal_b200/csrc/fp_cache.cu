@@ -384,12 +384,12 @@ cudaError_t launch_select(const SelectParams& p, int sms, cudaStream_t st) {
   static unsigned long long attr[kMaxCachedDevices] = {};
   const void* fn = reinterpret_cast<const void*>(select_kernel);
   cudaError_t e = set_max_smem(fn, (kSelKeysMax + kSelCand) * 4, attr);
-  if (e == cudaSuccess) e = cudaFuncSetAttribute(fn, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
   if (e != cudaSuccess) return e;
   // clusters grow with the longest sequence that there may be, while one wave of two CTAs an SM holds them
   const long long pairs = (long long)p.c.num_seqs * p.c.hkv;
   int C = 1;
   while (C < kSelCluster && (long long)C * kSelSpan < p.c.max_len && pairs * C * 2 <= 2 * sms) C *= 2;
+  if (C > 8 && (e = cudaFuncSetAttribute(fn, cudaFuncAttributeNonPortableClusterSizeAllowed, 1)) != cudaSuccess) return e;
   const long long span = (((long long)p.c.max_len + C * kSelWarps - 1) / (C * kSelWarps) + 31) / 32 * 32 * kSelWarps;
   const int cap = (int)(span < kSelKeysMax ? span : kSelKeysMax);
   cudaLaunchAttribute at[1];
