@@ -17,7 +17,9 @@ constexpr unsigned kFullMask = 0xffffffffu;
 // a time, so that the look-up waits on one round trip and not on a chain), then copies the token's K
 // and V rows in 16-byte pieces and sets weight 0 and the position of its slot in every kv-head. Bound by the
 // copy: 39 thousand tokens of 8 kv-heads (318 MB moved) take 54 us, 5.9 TB/s; 64 single tokens 3.4 us.
-__global__ void __launch_bounds__(256) append_kernel(const AppendParams p) {
+__global__ void __launch_bounds__(256) append_kernel(const __grid_constant__ AppendParams p) {
+  pdl_wait();
+  pdl_trigger();
   const CacheInfo& c = p.c;
   const int lane = threadIdx.x & 31;
   const long long t = (long long)blockIdx.x * (blockDim.x >> 5) + (threadIdx.x >> 5);
@@ -61,8 +63,7 @@ __global__ void __launch_bounds__(256) append_kernel(const AppendParams p) {
 }
 
 cudaError_t launch_append(const AppendParams& p, cudaStream_t st) {
-  append_kernel<<<(p.c.total_tokens + 7) / 8, 256, 0, st>>>(p);
-  return cudaGetLastError();
+  return launch_pdl(append_kernel, dim3((p.c.total_tokens + 7) / 8), 256, 0, st, p);
 }
 
 // ------------------------------------------------------------------------ selection -------------
@@ -99,7 +100,7 @@ static_assert(kSelBins == 4 * kSelThreads, "a thread sums four bins");
 // 147 us where 16 took 44 (the range of a fourth does not fit shared memory). Every write is
 // bounded by itself: the passes over a range that is read again would disagree if another stream changed the
 // weights meanwhile.
-__global__ void __launch_bounds__(kSelThreads, 2) select_kernel(const SelectParams p, const int keys_cap) {
+__global__ void __launch_bounds__(kSelThreads, 2) select_kernel(const __grid_constant__ SelectParams p, const int keys_cap) {
   extern __shared__ uint32_t s_keys[];
   __shared__ __align__(16) unsigned s_hist[kSelBins], s_sum[2][kSelBins];
   __shared__ unsigned s_tot[kSelWarps], s_pick[3], s_listed;
@@ -112,6 +113,8 @@ __global__ void __launch_bounds__(kSelThreads, 2) select_kernel(const SelectPara
   const CacheInfo& c = p.c;
   const int sg = blockIdx.x / C, s = sg / c.hkv, g = sg % c.hkv;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  pdl_wait();
+  pdl_trigger();
   const int lo = __ldg(c.cu_seqlens + s), hi = __ldg(c.cu_seqlens + s + 1), len = c.lens[s], L = hi - lo;
   int32_t* moves = p.moves + (long long)sg * p.budget * 2;
   auto fill = [&] {
@@ -392,17 +395,19 @@ cudaError_t launch_select(const SelectParams& p, int sms, cudaStream_t st) {
   if (C > 8 && (e = cudaFuncSetAttribute(fn, cudaFuncAttributeNonPortableClusterSizeAllowed, 1)) != cudaSuccess) return e;
   const long long span = (((long long)p.c.max_len + C * kSelWarps - 1) / (C * kSelWarps) + 31) / 32 * 32 * kSelWarps;
   const int cap = (int)(span < kSelKeysMax ? span : kSelKeysMax);
-  cudaLaunchAttribute at[1];
-  at[0].id = cudaLaunchAttributeClusterDimension;
-  at[0].val.clusterDim.x = C;
-  at[0].val.clusterDim.y = at[0].val.clusterDim.z = 1;
+  cudaLaunchAttribute at[2];
+  at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  at[0].val.programmaticStreamSerializationAllowed = 1;
+  at[1].id = cudaLaunchAttributeClusterDimension;
+  at[1].val.clusterDim.x = C;
+  at[1].val.clusterDim.y = at[1].val.clusterDim.z = 1;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)(pairs * C));
   cfg.blockDim = dim3(kSelThreads);
   cfg.dynamicSmemBytes = ((size_t)cap + kSelCand) * 4;
   cfg.stream = st;
   cfg.attrs = at;
-  cfg.numAttrs = 1;
+  cfg.numAttrs = 2;
   return cudaLaunchKernelEx(&cfg, select_kernel, p, cap);
 }
 
@@ -414,12 +419,14 @@ cudaError_t launch_select(const SelectParams& p, int sms, cudaStream_t st) {
 // slots.) Sources lie at or past the budget and destinations below it (checked), so no move reads what another
 // one writes and the order of the moves does not matter.
 constexpr int kMovesW = 8, kMovesC = 8 * kMovesW;
-__global__ void __launch_bounds__(256, 4) compact_kernel(const CompactParams p) {
+__global__ void __launch_bounds__(256, 4) compact_kernel(const __grid_constant__ CompactParams p) {
   __shared__ longlong2 s_rows[2][kMovesC];  // source and destination rows; source -1: none
   const CacheInfo& c = p.c;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int sg = blockIdx.x / p.parts, part = blockIdx.x % p.parts;
   const int s = sg / c.hkv, g = sg % c.hkv;
+  pdl_wait();
+  pdl_trigger();
   const int cnt = p.move_counts[sg];
   const int slots = (int)min((long long)c.max_len, (long long)c.max_pages * c.page_size);
   if (part == 0 && tid == 0) {
@@ -482,8 +489,7 @@ cudaError_t launch_compact(const CompactParams& in, int sms, cudaStream_t st) {
   const long long pairs = (long long)p.c.num_seqs * p.c.hkv, most = ((long long)p.budget + kMovesC - 1) / kMovesC;
   const long long want = (4ll * sms + pairs - 1) / pairs;
   p.parts = (int)(want < most ? want : most);
-  compact_kernel<<<(unsigned)(pairs * p.parts), 256, 0, st>>>(p);
-  return cudaGetLastError();
+  return launch_pdl(compact_kernel, dim3((unsigned)(pairs * p.parts)), 256, 0, st, p);
 }
 
 }  // namespace fp

@@ -607,3 +607,51 @@ def test_prompt_then_budgeted_decode():
             assert len(set(have)) == budget and set(range(sinks)) <= set(have)
             assert set(range(L + i + 1 - recent, L + i + 1)) <= set(have)
     assert d.status() == 0
+
+
+@pytest.mark.parametrize("hq,hkv,page,B,L", [(8, 2, 16, 64, 1), (6, 2, 48, 200, 9), (4, 4, 64, 200, 40)])
+def test_chained_steps_equal_steps_that_wait(hq, hkv, page, B, L):
+    """Kernels of consecutive calls overlap at their ends: the same steps with a synchronisation after every
+    call leave the same bits."""
+    S, steps = 2, 20
+    need = -(-(B + L) // page)
+    g = torch.Generator().manual_seed(B + L)
+    table = torch.randperm(S * need, generator=g).view(S, need).to(torch.int32).cuda()
+    k, v = (torch.randn((S * need * page, hkv, D), generator=g).to(torch.bfloat16).cuda() for _ in range(2))
+    w = torch.rand((S * need, hkv, page), generator=g).cuda()
+    pos = torch.arange(need * page, dtype=torch.int32).view(1, need, 1, page).expand(S, need, hkv, page)
+    inv = torch.empty_like(table.flatten().long())
+    inv[table.flatten().long()] = torch.arange(S * need, device="cuda")
+    pos = pos.reshape(S * need, hkv, page).cuda()[inv].contiguous()
+    lens = torch.tensor([B - 5, B // 2], dtype=torch.int32, device="cuda")
+    nxt = lens.clone()
+    p = fp.problem([0, L, 2 * L], hq, hkv)
+    c = fp.kv_cache(p, k, v, lens, table, page, w, pos)
+    ws = torch.empty(fp.cache_attn_workspace(p, c), dtype=torch.uint8, device="cuda")
+    mv = torch.empty((S, hkv, B, 2), dtype=torch.int32, device="cuda")
+    cnt, nl = (torch.empty(n, dtype=torch.int32, device="cuda") for n in ((S, hkv), (S,)))
+    st = torch.zeros(1, dtype=torch.int32, device="cuda")
+    qs, ks, vs = (torch.randn((steps, S * L, n, D), generator=g).to(torch.bfloat16).cuda() for n in (hq, hkv, hkv))
+    state = (k, v, w, pos, lens, nxt)
+    start = [t.clone() for t in state]
+
+    def run(wait):
+        for t, a in zip(state, start):
+            t.copy_(a)
+        outs = torch.empty_like(qs)
+        for i in range(steps):
+            for call in (lambda: fp.cache_append(p, c, ks[i], vs[i], nxt, st),
+                         lambda: fp.cache_attn(p, c, qs[i], 0.0, ws, outs[i], None, 0.9, st),
+                         lambda: fp.cache_select(p, c, B, 2, B // 4, nxt, mv, cnt, nl, st),
+                         lambda: fp.cache_compact(p, c, B, mv, cnt, nl, st), lambda: nxt.add_(L)):
+                call()
+                if wait:
+                    torch.cuda.synchronize()
+        torch.cuda.synchronize()
+        return [bits(outs)] + [bits(t).clone() for t in state]
+
+    want = run(True)
+    assert int(st.item()) == 0 and lens.tolist() == [B, min(B, B // 2 + steps * L)]
+    for _ in range(2):
+        for a, b in zip(run(False), want):
+            assert torch.equal(a, b)
