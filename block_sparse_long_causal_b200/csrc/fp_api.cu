@@ -674,6 +674,13 @@ fp::CacheInfo cache_info(const fp_problem* p, const fp_kv_cache* c) {
   a.max_pages = c->max_pages;
   a.page_size = c->page_size;
   a.num_pages = c->num_pages;
+  // With 2^(n - 1) < page_size <= 2^n and m = ceil(2^(31 + n) / page_size) < 2^32, m * page_size exceeds 2^(31 + n) by
+  // e < page_size <= 2^n, so u * m / 2^(31 + n) exceeds u / page_size by u e / (2^(31 + n) page_size) < 1 / page_size
+  // for u < 2^31: the floors agree. page_size >= 16 (n >= 4).
+  int n = 4;
+  while ((int64_t)c->page_size > (int64_t)1 << n) ++n;
+  a.page_mul = (uint32_t)((((uint64_t)1 << (31 + n)) + c->page_size - 1) / (uint64_t)c->page_size);
+  a.page_shift = (uint32_t)(n - 1);
   a.max_len = c->max_len;
   a.max_new = c->max_new;
   a.hq = p->num_q_heads;

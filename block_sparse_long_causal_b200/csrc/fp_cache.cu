@@ -52,7 +52,7 @@ __global__ void __launch_bounds__(256) append_kernel(const __grid_constant__ App
     vd[i] = __ldg(vs + i);
   }
   if (c.weights || c.positions) {
-    const long long page = row / c.page_size, off = row - page * c.page_size;
+    const long long page = page_of(c, (int)row), off = row - page * c.page_size;  // a cache has less than 2^31 rows
     const int pos = (p.next_pos ? p.next_pos[s] : c.lens[s]) + (u - c.lens[s]);
     for (int g = lane; g < c.hkv; g += 32) {
       const long long w = (page * c.hkv + g) * c.page_size + off;
@@ -135,6 +135,7 @@ __global__ void __launch_bounds__(kSelThreads, 2) select_kernel(const __grid_con
   // positions at or past `young` are protected (the difference cannot overflow: 64 bits)
   const long long young = (long long)(p.next_pos ? p.next_pos[s] : len) + L - p.recent;
   bool bad_page = false;
+  const int32_t* table = c.block_table + (long long)s * c.max_pages;
   // keys of slots u, u + 32, ... (K of them; past the last slot: anything), all their reads in flight together
   auto read_keys = [&](int u, uint32_t* out, auto count) {
     constexpr int K = decltype(count)::value;
@@ -142,12 +143,12 @@ __global__ void __launch_bounds__(kSelThreads, 2) select_kernel(const __grid_con
     float val[K];
 #pragma unroll
     for (int i = 0; i < K; ++i)
-      page[i] = __ldg(c.block_table + (long long)s * c.max_pages + min(u + 32 * i, n - 1) / c.page_size);
+      page[i] = __ldg(table + page_of(c, min(u + 32 * i, n - 1)));
 #pragma unroll
     for (int i = 0; i < K; ++i) {
       const int v = min(u + 32 * i, n - 1);
       const bool bad = page[i] < 0 || page[i] >= c.num_pages;
-      const long long w = ((long long)(bad ? 0 : page[i]) * c.hkv + g) * c.page_size + v % c.page_size;
+      const long long w = ((long long)(bad ? 0 : page[i]) * c.hkv + g) * c.page_size + (v - page_of(c, v) * c.page_size);
       val[i] = __ldg(c.weights + w);
       pos[i] = c.positions ? __ldg(c.positions + w) : v;
       page[i] = bad;
@@ -455,7 +456,7 @@ __global__ void __launch_bounds__(256, 4) compact_kernel(const __grid_constant__
     }
     s_rows[buf][tid] = r;
     if (r.x < 0) return;
-    const long long ps = r.x / c.page_size, pd = r.y / c.page_size;
+    const long long ps = page_of(c, (int)r.x), pd = page_of(c, (int)r.y);  // a cache has less than 2^31 rows
     const long long ws = (ps * c.hkv + g) * c.page_size + (r.x - ps * c.page_size);
     const long long wd = (pd * c.hkv + g) * c.page_size + (r.y - pd * c.page_size);
     float w = 0.f;

@@ -27,18 +27,22 @@ cudaError_t launch_pdl(void (*kernel)(K...), dim3 grid, int threads, int smem, c
   return cudaLaunchKernelEx(&cfg, kernel, args...);
 }
 
+// u / page_size by a multiplication (a division by a run-time number is some twenty instructions).
+__device__ __forceinline__ int page_of(const CacheInfo& c, int u) {
+  return (int)(__umulhi((unsigned)u, c.page_mul) >> c.page_shift);
+}
 // Row of the cache that holds slot u of sequence s, or -1 when the block table points outside the
 // cache (callers flag FP_DEV_BAD_PROBLEM and treat the slot as not there). u < max_pages * page_size
 // is the caller's duty (n <= max_len is checked before any slot is used).
 __device__ __forceinline__ long long slot_row(const CacheInfo& c, int s, int u) {
-  const int lp = u / c.page_size;
+  const int lp = page_of(c, u);
   const int page = __ldg(c.block_table + (long long)s * c.max_pages + lp);
   if (page < 0 || page >= c.num_pages) return -1;
   return (long long)page * c.page_size + (u - lp * c.page_size);
 }
 // Index of (slot, kv-head) in the weights and positions arrays [num_pages, Hkv, page_size], or -1.
 __device__ __forceinline__ long long slot_word(const CacheInfo& c, int s, int g, int u) {
-  const int lp = u / c.page_size;
+  const int lp = page_of(c, u);
   const int page = __ldg(c.block_table + (long long)s * c.max_pages + lp);
   if (page < 0 || page >= c.num_pages) return -1;
   return ((long long)page * c.hkv + g) * c.page_size + (u - lp * c.page_size);

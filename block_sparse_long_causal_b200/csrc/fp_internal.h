@@ -116,6 +116,7 @@ struct CacheInfo {
   const int32_t* block_table; // device [S, max_pages]
   int32_t num_seqs, total_tokens;
   int32_t max_pages, page_size, num_pages;
+  uint32_t page_mul, page_shift;  // u / page_size = (u * page_mul) >> (32 + page_shift) for 0 <= u < 2^31
   int32_t max_len;            // bound of lens[s] + L_s
   int32_t max_new;            // bound of L_s
   int32_t hq, hkv, group;
