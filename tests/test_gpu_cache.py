@@ -72,6 +72,9 @@ ATTN = [
     ([3000, 17, 512, 0, 90, 700, 5, 260], [200, 150, 1, 300, 64, 90, 33, 170], 32, 8, 48),  # more units than CTAs
     ([6000], [20], 2, 2, 16),                               # one row tile, two warpgroups, split over many CTAs
     ([128, 384, 383], [32, 128, 1], 4, 1, 64),              # keys and rows that fill their tiles exactly
+    ([1000, 64, 0], [8, 1, 5], 8, 2, 16),                   # exactly 32 rows
+    ([63, 640], [31, 17], 2, 2, 48),                        # 31 rows, one head a group
+    ([4000, 5], [11, 2], 6, 2, 16),                         # one row more than 32
 ]
 
 
@@ -248,8 +251,8 @@ def test_offsets_past_32_bits():
     torch.cuda.empty_cache()
 
 
-@pytest.mark.parametrize("lens,new,hq,hkv", [([40], [4], 8, 2), ([200], [12], 2, 2), ([70, 33], [200, 60], 8, 2),
-                                             ([300], [20], 4, 2)])
+@pytest.mark.parametrize("lens,new,hq,hkv", [([40], [4], 8, 2), ([200], [12], 2, 2), ([90], [7], 8, 2),
+                                             ([70, 33], [200, 60], 8, 2), ([300], [20], 4, 2)])
 @pytest.mark.parametrize("value", [math.nan, math.inf, -math.inf])
 def test_masked_values_reach_nobody(lens, new, hq, hkv, value):
     """A non-finite V of a new token is seen by the rows from that token on, and by no row before it."""
