@@ -16,7 +16,7 @@ constexpr unsigned kFullMask = 0xffffffffu;
 // One warp per new token: it finds its sequence (the number of s with cu_seqlens[s] <= t, counted 32 at
 // a time, so that the look-up waits on one round trip and not on a chain), then copies the token's K
 // and V rows in 16-byte pieces and sets weight 0 and the position of its slot in every kv-head. Bound by the
-// copy: 39 thousand tokens of 8 kv-heads (318 MB moved) take 54 us, 5.9 TB/s; 64 single tokens 3.4 us.
+// copy: 39 thousand tokens of 8 kv-heads (318 MB moved) take 51.5 us, 6.2 TB/s; 64 single tokens 3.1 us.
 __global__ void __launch_bounds__(256) append_kernel(const __grid_constant__ AppendParams p) {
   pdl_wait();
   pdl_trigger();
@@ -95,7 +95,7 @@ static_assert(kSelBins == 4 * kSelThreads, "a thread sums four bins");
 // (128K slots and 8 heads: 43.6 -> 35.8 us). Then every warp counts its slots above and at the threshold, and
 // after a scan over the cluster's warps writes its holes (evicted slots below the budget) and sources (kept
 // slots at or past it) in ascending order.
-// Bound by latency, not by its 8 bytes a slot: of 16 us for 16 sequences of 4.1K slots 4 go to the reads, 2 to 3
+// Bound by latency, not by its 8 bytes a slot: of 15 us for 16 sequences of 4.1K slots 4 go to the reads, 2 to 3
 // to each pass, 2 to the list. The loops keep several slots a lane in flight. Clusters of 8 or 4 CTAs took 47 and
 // 147 us where 16 took 44 (the range of a fourth does not fit shared memory). Every write is
 // bounded by itself: the passes over a range that is read again would disagree if another stream changed the
