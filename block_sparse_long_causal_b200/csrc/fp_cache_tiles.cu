@@ -350,6 +350,9 @@ __global__ void __launch_bounds__(kThreads, 1) cache_tiles_kernel(const __grid_c
       uint32_t kit = 0, vit = 0, cnt[2] = {0, 0};
       bool fail = false;
       auto wait = [&](uint32_t bar, uint32_t parity) { return mbar_wait(bar, parity, p.wait_limit_ns); };
+      // descriptors are built once: every instruction of this thread lies on the critical path
+      const uint64_t q_desc = sdesc_sw128(sQ, 16, 1024), k_desc = sdesc_sw128(sK, 16, 1024);
+      const uint64_t v_desc = sdesc_sw128(sV, kSlab, 1024);
       for (uint32_t uc = 0; !fail; ++uc) {
         if (!wait(b_u_full(uc), (uc / kUnitRing) & 1)) { fail = true; break; }
         const Piece pc = *unit_entry(uc);
@@ -364,7 +367,7 @@ __global__ void __launch_bounds__(kThreads, 1) cache_tiles_kernel(const __grid_c
           const int vs = vit % kStages;
           if (!wait(b_v_full(vs), (vit / kStages) & 1)) return false;
           tc_fence_after();
-          const uint64_t vdesc = sdesc_sw128(sV + vs * kTile, kSlab, 1024);
+          const uint64_t vdesc = desc_advance(v_desc, vs * (kTile >> 4));
 #pragma unroll
           for (int kk = 0; kk < kBK / 16; ++kk)
             mma_ts(t_o(k), t_s(k) + kk * 8, desc_advance(vdesc, kk * (2048 >> 4)), kIdescPV,
@@ -372,9 +375,9 @@ __global__ void __launch_bounds__(kThreads, 1) cache_tiles_kernel(const __grid_c
           had_pv[k] = true;
           return true;
         };
-        auto qk = [&](int k, uint32_t kbase) {
-          const uint64_t qdesc = sdesc_sw128(sQ + (pc.nslot == 2 ? k : 0) * kTile, 16, 1024);
-          const uint64_t kdesc = sdesc_sw128(kbase, 16, 1024);
+        const uint64_t q_desc1 = pc.nslot == 2 ? desc_advance(q_desc, kTile >> 4) : q_desc;
+        auto qk = [&](int k, uint64_t kdesc) {
+          const uint64_t qdesc = k == 0 ? q_desc : q_desc1;
 #pragma unroll
           for (int kk = 0; kk < kHeadDim / 16; ++kk) {
             const uint32_t off = ((kk >> 2) * kSlab + (kk & 3) * 32) >> 4;
@@ -388,17 +391,17 @@ __global__ void __launch_bounds__(kThreads, 1) cache_tiles_kernel(const __grid_c
           const int ks = kit % kStages;
           if (!wait(b_k_full(ks), (kit / kStages) & 1)) { fail = true; break; }
           tc_fence_after();
-          const uint32_t kbase = sK + ks * kTile;
+          const uint64_t kdesc = desc_advance(k_desc, ks * (kTile >> 4));
           // a slot that took part in the previous tile issues that tile's PV before this one's QK (S overwrites
           // P); the QK of one that did not goes first, so that its softmax overlaps the other's
 #pragma unroll
           for (int k = 0; k < 2; ++k)
-            if (((part & ~prev_part) >> k) & 1) qk(k, kbase);
+            if (((part & ~prev_part) >> k) & 1) qk(k, kdesc);
 #pragma unroll
           for (int k = 0; k < 2; ++k)
             if (!fail && ((prev_part >> k) & 1)) {
               if (!pv(k)) { fail = true; break; }
-              if ((part >> k) & 1) qk(k, kbase);
+              if ((part >> k) & 1) qk(k, kdesc);
             }
           if (fail) break;
           if (t > pc.kt0) {
