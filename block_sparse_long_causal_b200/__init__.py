@@ -410,7 +410,11 @@ def _rows_of(t, name: str, tokens: int, heads: int, d: int, device):
     row, head, col = t.stride()
     if col != 1 or (head != d and heads > 1):
         raise ValueError(f"{name}: the heads of a token must be contiguous")
-    return t.data_ptr(), row if tokens > 1 else 0
+    if tokens == 1:
+        return t.data_ptr(), 0
+    if row < heads * d:  # an expanded tensor has stride 0, which the C call takes for packed rows
+        raise ValueError(f"{name}: the rows of its tokens overlap (stride {row}, at least {heads * d})")
+    return t.data_ptr(), row
 
 
 def _want(t, name: str, dtype, device, numel=None) -> int:

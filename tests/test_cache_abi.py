@@ -195,3 +195,26 @@ def test_binding_checks_the_calls_tensors():
             fp.cache_select(p, c, 8, 0, 0, None, *a)
         with pytest.raises(ValueError):
             fp.cache_compact(p, c, 8, *a)
+
+
+@pytest.mark.parametrize("heads", [1, 2, 8])
+def test_binding_refuses_rows_that_overlap(heads):
+    """An expanded tensor has a token stride of 0, which the C calls take for packed rows."""
+    one = torch.zeros((1, heads, 128), dtype=torch.bfloat16)
+    cpu = torch.device("cpu")
+    flat = torch.zeros(64 * heads * 128, dtype=torch.bfloat16)
+    for t in (one.expand(64, heads, 128), flat.as_strided((64, heads, 128), (heads * 128 - 8, 128, 1))):
+        with pytest.raises(ValueError, match="overlap"):
+            fp._rows_of(t, "q", 64, heads, 128, cpu)
+    # a single token has no neighbour; rows further apart than packed are a slice of a wider projection
+    assert fp._rows_of(one, "q", 1, heads, 128, cpu) == (one.data_ptr(), 0)
+    wide = torch.zeros((64, heads + 3, 128), dtype=torch.bfloat16)
+    assert fp._rows_of(wide[:, 1:1 + heads], "q", 64, heads, 128, cpu) == (wide.data_ptr() + 256, (heads + 3) * 128)
+    # and through the calls themselves
+    p, c = _py()
+    kv, q = torch.zeros((3, 2, 128), dtype=torch.bfloat16), torch.zeros((3, 8, 128), dtype=torch.bfloat16)
+    for k, v in ((kv[:1].expand(3, 2, 128), kv), (kv, kv[:1].expand(3, 2, 128))):
+        with pytest.raises(ValueError, match="overlap"):
+            fp.cache_append(p, c, k, v)
+    with pytest.raises(ValueError, match="overlap"):
+        fp.cache_attn(p, c, q[:1].expand(3, 8, 128), 0.0, torch.zeros(16, dtype=torch.uint8), q)
