@@ -273,6 +273,14 @@ __global__ void __launch_bounds__(kThreads, 1) cache_tiles_kernel(const __grid_c
       pc.kts0 = key_tiles(u, (2 * u.m + 1) * TT);
       pc.slot = pc.kt0 == 0 && pc.kt1 == pc.kts ? -1 : 2 * (int)blockIdx.x + (pc.kt0 == 0 ? 1 : 0);
       if (uc >= kUnitRing && !all_wait(b_u_empty(uc), ((uc / kUnitRing) - 1) & 1)) { fail = true; break; }
+      // keys that an earlier unit of this entry noted: cleared by the warp that hands the entry out, as the epilogue of a
+      // piece without a tail tile waits for nothing of the tail warp
+      if (s_bad_unit[uc % kUnitRing]) {
+        __syncwarp();
+        for (int e = lane; e < 3 * 128; e += 32) bad_keys(uc)[e] = 0x7fffffff;
+        if (lane == 0) s_bad_unit[uc % kUnitRing] = 0;
+        __syncwarp();
+      }
       if (lane == 0) {
         *unit_entry(uc) = pc;
         mbar_arrive(b_u_full(uc));
@@ -450,12 +458,6 @@ __global__ void __launch_bounds__(kThreads, 1) cache_tiles_kernel(const __grid_c
       __syncwarp();
       if (pc.seq0 < 0) break;
       int* bad = bad_keys(uc);
-      if (s_bad_unit[uc % kUnitRing]) {  // left by an earlier unit of this entry
-        __syncwarp();
-        for (int e = lane; e < 3 * 128; e += 32) bad[e] = 0x7fffffff;
-        if (lane == 0) s_bad_unit[uc % kUnitRing] = 0;
-        __syncwarp();
-      }
       const int seen = pc.len + pc.tok0 + 1;  // keys below it are seen by every row
       for (int t = pc.kt0; t < pc.kt1; ++t, ++vit) {
         if (t < seen / kBK) continue;

@@ -285,6 +285,34 @@ def test_masked_values_reach_nobody(lens, new, hq, hkv, value):
     assert bool(((lse.cpu().double() - z).abs() <= bz)[~bad.T].all())
 
 
+def test_noted_values_stay_with_their_unit():
+    """A CTA takes several units one after another, the last of them often in part and without the slots of its new
+    tokens: what an earlier unit noted of its non-finite V must not reach it."""
+    S, hq, hkv = 512, 8, 2
+    g = torch.Generator().manual_seed(41)
+    lens, new = torch.randint(100, 900, (S,), generator=g).tolist(), torch.randint(9, 21, (S,), generator=g).tolist()
+    x = make(lens, new, hq, hkv, 16, seed=42)
+    o, _, _, bound, _, _ = oracle_attn(x)
+    y = dict(x, v=x["v"].clone())
+    odd = torch.zeros(o.shape, dtype=torch.float64)  # what a row gets by itself
+    for s in range(S):
+        j, h, col = s % new[s], s % hkv, (37 * s) % D
+        value = (math.nan, math.inf, -math.inf)[s % 3]
+        y["v"][int(rows(x["table"], 16, s, lens[s] + j + 1)[-1]), h, col] = value
+        t0 = x["cu"][s]
+        odd[t0 + j:t0 + new[s], h * 4:(h + 1) * 4, col] = value
+    want = o + odd
+    d = Dev(y)
+    for _ in range(3):
+        out, _ = d.attn()
+        assert d.status() == 0
+        got = out.cpu().double()
+        fin = want.isfinite()
+        assert torch.equal(got.isnan(), want.isnan())
+        assert torch.equal(got[~fin].nan_to_num(nan=1.0), want[~fin].nan_to_num(nan=1.0))
+        assert bool(((got - o).abs() <= bound)[fin].all())
+
+
 def test_prompt_pieces_capture_and_replay():
     """A captured append + attention + selection + compaction of prompt pieces, replayed on other inputs."""
     lens, new, hq, hkv, page, B = [30, 261], [70, 50], 8, 2, 16, 200
