@@ -533,10 +533,12 @@ __global__ void __launch_bounds__(256) cache_rows_weights_kernel(const __grid_co
     }
     const float4* sc = reinterpret_cast<const float4*>(p.scores) + x * (rs / 4) * kKeysT + lane;
     long long at[2];
+    int rmin[2];  // the first row that sees the key: masked scores are -inf, but a row's lse may be NaN
     float old[2] = {0.f, 0.f}, w[2] = {0.f, 0.f};
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
       const int key = u.kt * kKeysT + 32 * i + lane;
+      rmin[i] = max(key - u.len, 0) * c.group;
       at[i] = key < u.n ? slot_word(c, s, g, key) : -1;  // a bad page was flagged by the attention
       if (at[i] >= 0 && p.decay > 0.f) old[i] = c.weights[at[i]];
     }
@@ -548,10 +550,10 @@ __global__ void __launch_bounds__(256) cache_rows_weights_kernel(const __grid_co
 #pragma unroll
       for (int i = 0; i < 2; ++i) {
         const float4 v = __ldcg(sc + 32 * i);
-        w[i] += ex2_approx(v.x - zr[0]);
-        if (r + 1 < rows) w[i] += ex2_approx(v.y - zr[1]);
-        if (r + 2 < rows) w[i] += ex2_approx(v.z - zr[2]);
-        if (r + 3 < rows) w[i] += ex2_approx(v.w - zr[3]);
+        if (r >= rmin[i]) w[i] += ex2_approx(v.x - zr[0]);
+        if (r + 1 < rows && r + 1 >= rmin[i]) w[i] += ex2_approx(v.y - zr[1]);
+        if (r + 2 < rows && r + 2 >= rmin[i]) w[i] += ex2_approx(v.z - zr[2]);
+        if (r + 3 < rows && r + 3 >= rmin[i]) w[i] += ex2_approx(v.w - zr[3]);
       }
     }
 #pragma unroll

@@ -313,6 +313,31 @@ def test_noted_values_stay_with_their_unit():
         assert bool(((got - o).abs() <= bound)[fin].all())
 
 
+# short drafts (few rows), longer pieces (row tiles, several of them), heads that fill a tile and that do not
+ODD_ROWS = [([40], [4], 8, 2), ([200, 17], [12, 1], 2, 2), ([130], [20], 4, 2), ([300], [90], 6, 2), ([70, 33], [200, 60], 8, 2)]
+
+
+@pytest.mark.parametrize("lens,new,hq,hkv", ODD_ROWS)
+def test_a_query_that_is_nan_reaches_the_weights_of_the_slots_it_sees(lens, new, hq, hkv):
+    x = make(lens, new, hq, hkv, 16, seed=29)
+    _, _, w, _, _, bound = oracle_attn(x, None, 0.5)
+    j, h = new[0] // 3, hq - 1
+    y = dict(x, q=x["q"].clone())
+    y["q"][j, h, 7] = math.nan
+    d = Dev(y)
+    _, lse = d.attn(decay=0.5)
+    assert d.status() == 0
+    nan_lse = torch.zeros(lse.shape, dtype=torch.bool)
+    nan_lse[h, j] = True
+    assert torch.equal(lse.cpu().isnan(), nan_lse)
+    seen = torch.zeros(w.shape, dtype=torch.bool)
+    r = rows(x["table"], 16, 0, lens[0] + j + 1)
+    seen[r // 16, hkv - 1, r % 16] = True
+    got, used = d.w.cpu().double(), bound > 0
+    assert torch.equal(got.isnan() & used, seen)
+    assert bool(((got - w).abs() <= bound)[used & ~seen].all())
+
+
 def test_prompt_pieces_capture_and_replay():
     """A captured append + attention + selection + compaction of prompt pieces, replayed on other inputs."""
     lens, new, hq, hkv, page, B = [30, 261], [70, 50], 8, 2, 16, 200
