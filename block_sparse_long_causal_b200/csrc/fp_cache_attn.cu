@@ -530,6 +530,7 @@ __global__ void __launch_bounds__(256) cache_rows_weights_kernel(const __grid_co
       z = lane < rows ? __ldcg(p.lse2 + (long long)(g * c.group + lane % c.group) * c.total_tokens + u.seq0 +
                                lane / c.group)
                       : INFINITY;
+      if (z == -INFINITY) z = INFINITY;  // a row without a finite score: 2^(-inf - z) is to be 0, not NaN
     }
     const float4* sc = reinterpret_cast<const float4*>(p.scores) + x * (rs / 4) * kKeysT + lane;
     long long at[2];

@@ -736,7 +736,7 @@ __global__ void __launch_bounds__(kThreads, 1) cache_tiles_kernel(const __grid_c
           const float mu = m_run == -INFINITY ? 0.f : m_run;
           const float z = any ? mu + log2f(l_run) : -INFINITY;
           const long long at = (long long)h * c.total_tokens + token;
-          if (p.lse2) p.lse2[at] = -z;
+          if (p.lse2) p.lse2[at] = any ? -z : -INFINITY;  // a row without a finite score adds no weight
           if (p.lse) p.lse[at] = z * 0.6931471805599453f;
         } else {  // a row tile without a key tile in this piece: sum 0, and its O is not read
           *reinterpret_cast<float2*>(p.part_ml + 2 * (part0 * 128 + r)) = make_float2(n > 0 || dual ? m_run : -INFINITY, l_run);
@@ -908,7 +908,7 @@ __global__ void __launch_bounds__(kJoinThreads) cache_tiles_join_kernel(const __
       if (cg == 0) {
         const float z = any ? (m == -INFINITY ? 0.f : m) + log2f(l) : -INFINITY;
         const long long place = (long long)h * c.total_tokens + t;
-        if (p.lse2) p.lse2[place] = -z;
+        if (p.lse2) p.lse2[place] = any ? -z : -INFINITY;  // as in a whole unit
         if (p.lse) p.lse[place] = z * 0.6931471805599453f;
       }
     }

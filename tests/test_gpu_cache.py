@@ -338,6 +338,26 @@ def test_a_query_that_is_nan_reaches_the_weights_of_the_slots_it_sees(lens, new,
     assert bool(((got - w).abs() <= bound)[used & ~seen].all())
 
 
+@pytest.mark.parametrize("lens,new,hq,hkv", ODD_ROWS)
+def test_a_row_without_a_finite_score_adds_no_weight(lens, new, hq, hkv):
+    """All scores of one row are -inf: its sum is 0, its lse -inf, and it leaves the slots' weights alone."""
+    x = make(lens, new, hq, hkv, 16, seed=30)
+    j, h = new[0] // 3, hq - 1
+    x["k"][:, hkv - 1, 0] = x["k"][:, hkv - 1, 0].abs() + 0.25
+    x["q"][j, h] = 0.0
+    _, _, w, _, _, bound = oracle_attn(x, None, 0.5)
+    r = rows(x["table"], 16, 0, lens[0] + j + 1)
+    w[r // 16, hkv - 1, r % 16] -= 1.0 / (lens[0] + j + 1)  # the row of zeros gave every slot the same
+    y = dict(x, q=x["q"].clone())
+    y["q"][j, h, 0] = -math.inf
+    d = Dev(y)
+    out, lse = d.attn(decay=0.5)
+    assert d.status() == 0
+    assert float(lse[h, j]) == -math.inf and not bool(out[j, h].any())
+    got, used = d.w.cpu().double(), bound > 0
+    assert bool(((got - w).abs() <= bound)[used].all())
+
+
 def test_prompt_pieces_capture_and_replay():
     """A captured append + attention + selection + compaction of prompt pieces, replayed on other inputs."""
     lens, new, hq, hkv, page, B = [30, 261], [70, 50], 8, 2, 16, 200
