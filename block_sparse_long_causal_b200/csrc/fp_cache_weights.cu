@@ -151,15 +151,6 @@ __global__ void __launch_bounds__(kThreads, 1) cache_tiles_weights_kernel(const 
     tma_prefetch_desc(&p.tm_q);
     tma_prefetch_desc(&p.tm_k);
   }
-  // the rows of a row tile past its last whole token are never loaded: zeros, so that their scores are finite
-  if (TT * G < 128) {
-    const int spare = 128 - TT * G;
-    for (int e = tid; e < kQ * 2 * spare * 8; e += kThreads)
-      *reinterpret_cast<uint4*>(smem + kOffQ + e / (spare * 8) * kSlab + TT * G * 128 + e % (spare * 8) * 16) =
-          make_uint4(0, 0, 0, 0);
-    asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
-  }
-  for (int e = tid; e < kS * 128; e += kThreads) s_z[e] = -INFINITY;  // theirs stay: 2^-inf
   if (warp == 1) {
     tmem_alloc(smem_u32(s_tmem), 512);
     tmem_relinquish();
@@ -371,8 +362,10 @@ __global__ void __launch_bounds__(kThreads, 1) cache_tiles_weights_kernel(const 
       const int past = u.kt * kBK + r - u.len - u.rt * TT;
       const int cmin = (past > 0 ? min(past, TT) : 0) * G;
       const bool part = (u.rt + 1) * TT > u.L;
-      const int cmax = part ? (u.L - u.rt * TT) * G : 128;
+      const int cmax = (part ? u.L - u.rt * TT : TT) * G;
       const bool edge = part || u.kt * kBK + kBK - 1 - u.len > u.rt * TT;  // the same for every thread
+      // columns below it need no mask; the spare ones of a row tile, which nothing loads, always do
+      const int plain = edge ? 0 : TT * G;
       const uint32_t col = col0 + 256 * (it % kS);
       uint32_t v[2][32];
       tmem_ld32(col, v[0]);
@@ -381,7 +374,7 @@ __global__ void __launch_bounds__(kThreads, 1) cache_tiles_weights_kernel(const 
         tmem_wait_ld();
         reg_fence32(v[b & 1]);
         if (b < 3) tmem_ld32(col + 32 * (b + 1), v[(b + 1) & 1]);
-        if (!edge) {
+        if (32 * (b + 1) <= plain) {
 #pragma unroll
           for (int e = 0; e < 32; e += 4) {
             const float4 zz = *reinterpret_cast<const float4*>(z + 32 * b + e);

@@ -358,6 +358,28 @@ def test_a_row_without_a_finite_score_adds_no_weight(lens, new, hq, hkv):
     assert bool(((got - w).abs() <= bound)[used].all())
 
 
+@pytest.mark.parametrize("lens,new,hq,hkv", [([40], [4], 8, 2), ([200], [70], 8, 2), ([300], [90], 6, 2), ([257], [130], 10, 2),
+                                             ([900], [6], 22, 2)])
+def test_an_infinite_key_that_every_row_scores_at_minus_infinity(lens, new, hq, hkv):
+    """Its slot is left with its decayed weight, also where the heads of a group do not fill a row tile."""
+    x = make(lens, new, hq, hkv, 16, seed=33)
+    G, u = hq // hkv, lens[0] // 2
+    x["q"][:, :G, 5] = x["q"][:, :G, 5].abs() + 1
+    r = int(rows(x["table"], 16, 0, u + 1)[-1])
+    # for the oracle a score so low that its exponential is nothing, in place of -inf
+    x["k"][r, 0, 5] = -1024.0
+    o, z, w, bo, bz, bw = oracle_attn(x, None, 0.5)
+    assert float(w[r // 16, 0, r % 16] - 0.5 * x["w"][r // 16, 0, r % 16].double()) < 2.0 ** -100
+    y = dict(x, k=x["k"].clone())
+    y["k"][r, 0, 5] = -math.inf
+    d = Dev(y)
+    out, lse = d.attn(decay=0.5)
+    assert d.status() == 0
+    assert bool(((out.cpu().double() - o).abs() <= bo).all()) and bool(((lse.cpu().double() - z).abs() <= bz).all())
+    used = bw > 0
+    assert bool(((d.w.cpu().double() - w).abs() <= bw)[used].all())
+
+
 def test_prompt_pieces_capture_and_replay():
     """A captured append + attention + selection + compaction of prompt pieces, replayed on other inputs."""
     lens, new, hq, hkv, page, B = [30, 261], [70, 50], 8, 2, 16, 200
