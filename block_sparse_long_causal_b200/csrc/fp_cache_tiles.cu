@@ -273,14 +273,6 @@ __global__ void __launch_bounds__(kThreads, 1) cache_tiles_kernel(const __grid_c
       pc.kts0 = key_tiles(u, (2 * u.m + 1) * TT);
       pc.slot = pc.kt0 == 0 && pc.kt1 == pc.kts ? -1 : 2 * (int)blockIdx.x + (pc.kt0 == 0 ? 1 : 0);
       if (uc >= kUnitRing && !all_wait(b_u_empty(uc), ((uc / kUnitRing) - 1) & 1)) { fail = true; break; }
-      // keys that an earlier unit of this entry noted: cleared by the warp that hands the entry out, as the epilogue of a
-      // piece without a tail tile waits for nothing of the tail warp
-      if (s_bad_unit[uc % kUnitRing]) {
-        __syncwarp();
-        for (int e = lane; e < 3 * 128; e += 32) bad_keys(uc)[e] = 0x7fffffff;
-        if (lane == 0) s_bad_unit[uc % kUnitRing] = 0;
-        __syncwarp();
-      }
       if (lane == 0) {
         *unit_entry(uc) = pc;
         mbar_arrive(b_u_full(uc));
@@ -458,6 +450,12 @@ __global__ void __launch_bounds__(kThreads, 1) cache_tiles_kernel(const __grid_c
       __syncwarp();
       if (pc.seq0 < 0) break;
       int* bad = bad_keys(uc);
+      if (s_bad_unit[uc % kUnitRing]) {  // left by an earlier unit of this entry
+        __syncwarp();
+        for (int e = lane; e < 3 * 128; e += 32) bad[e] = 0x7fffffff;
+        if (lane == 0) s_bad_unit[uc % kUnitRing] = 0;
+        __syncwarp();
+      }
       const int seen = pc.len + pc.tok0 + 1;  // keys below it are seen by every row
       for (int t = pc.kt0; t < pc.kt1; ++t, ++vit) {
         if (t < seen / kBK) continue;
@@ -680,7 +678,9 @@ __global__ void __launch_bounds__(kThreads, 1) cache_tiles_kernel(const __grid_c
       const long long part0 = (long long)pc.slot * 2 + (dual ? 0 : slot);  // this row tile's partial results
       uint16_t* orow = p.out + (token * c.hq + h) * kHeadDim;
       const int* bad = bad_keys(uc);
-      const bool odd = s_bad_unit[uc % kUnitRing] != 0;
+      // the notes are this unit's only where the piece has a tail tile: its V, and so its products, then waited for the
+      // tail warp; in a piece without one the tail warp may still be clearing an earlier unit's
+      const bool odd = pc.kt1 > (pc.len + pc.tok0 + 1) / kBK && s_bad_unit[uc % kUnitRing] != 0;
       const uint32_t col0 = t_o(dual ? 0 : slot) + lane_off, col1 = t_o(1) + lane_off;
       const int cb = dual ? 64 * slot : 0, ce = dual ? cb + 64 : kHeadDim;
       if (use[0] || pc.slot < 0) {
