@@ -17,6 +17,7 @@ constexpr unsigned kFullMask = 0xffffffffu;
 // a time, so that the look-up waits on one round trip and not on a chain), then copies the token's K
 // and V rows in 16-byte pieces and sets weight 0 and the position of its slot in every kv-head. Bound by the
 // copy: 39 thousand tokens of 8 kv-heads (318 MB moved) take 51.5 us, 6.2 TB/s; 64 single tokens 3.1 us.
+constexpr int kAppend = 4;  // 16-byte pieces of K and of V that a lane has in flight
 __global__ void __launch_bounds__(256) append_kernel(const __grid_constant__ AppendParams p) {
   pdl_wait();
   pdl_trigger();
@@ -27,13 +28,13 @@ __global__ void __launch_bounds__(256) append_kernel(const __grid_constant__ App
   int s = -1;
   for (int b = 0; b < c.num_seqs; b += 32) {
     const int x = b + lane;
-    s += __popc(__ballot_sync(kFullMask, x < c.num_seqs && __ldg(c.cu_seqlens + x) <= t));
+    s += __popc(__ballot_sync(kFullMask, x < c.num_seqs && c.cu_seqlens[x] <= t));
   }
   bool ok = s >= 0;
   int u = 0;
   long long row = -1;
   if (ok) {
-    const int lo = __ldg(c.cu_seqlens + s), hi = __ldg(c.cu_seqlens + s + 1), len = c.lens[s];
+    const int lo = c.cu_seqlens[s], hi = c.cu_seqlens[s + 1], len = c.lens[s];
     ok = lo >= 0 && t >= lo && t < hi && len >= 0 && len <= c.max_len - (hi - lo);
     u = len + (int)(t - lo);
     if (ok) row = slot_row(c, s, u);
@@ -47,9 +48,20 @@ __global__ void __launch_bounds__(256) append_kernel(const __grid_constant__ App
   const uint4* vs = reinterpret_cast<const uint4*>(p.v + t * p.v_stride);
   uint4* kd = reinterpret_cast<uint4*>(c.k) + row * chunks;
   uint4* vd = reinterpret_cast<uint4*>(c.v) + row * chunks;
-  for (int i = lane; i < chunks; i += 32) {
-    kd[i] = __ldg(ks + i);
-    vd[i] = __ldg(vs + i);
+  for (int i0 = lane; i0 < chunks; i0 += 32 * kAppend) {  // eight kv-heads at once, all their reads in flight
+    uint4 x[kAppend], y[kAppend];
+#pragma unroll
+    for (int j = 0; j < kAppend; ++j)
+      if (i0 + 32 * j < chunks) {
+        x[j] = ks[i0 + 32 * j];
+        y[j] = vs[i0 + 32 * j];
+      }
+#pragma unroll
+    for (int j = 0; j < kAppend; ++j)
+      if (i0 + 32 * j < chunks) {
+        kd[i0 + 32 * j] = x[j];
+        vd[i0 + 32 * j] = y[j];
+      }
   }
   if (c.weights || c.positions) {
     const long long page = page_of(c, (int)row), off = row - page * c.page_size;  // a cache has less than 2^31 rows
@@ -115,7 +127,7 @@ __global__ void __launch_bounds__(kSelThreads, 2) select_kernel(const __grid_con
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   pdl_wait();
   pdl_trigger();
-  const int lo = __ldg(c.cu_seqlens + s), hi = __ldg(c.cu_seqlens + s + 1), len = c.lens[s], L = hi - lo;
+  const int lo = c.cu_seqlens[s], hi = c.cu_seqlens[s + 1], len = c.lens[s], L = hi - lo;
   int32_t* moves = p.moves + (long long)sg * p.budget * 2;
   auto fill = [&] {
     for (int i = rank * kSelThreads + tid; i < p.budget; i += C * kSelThreads)
@@ -143,14 +155,14 @@ __global__ void __launch_bounds__(kSelThreads, 2) select_kernel(const __grid_con
     float val[K];
 #pragma unroll
     for (int i = 0; i < K; ++i)
-      page[i] = __ldg(table + page_of(c, min(u + 32 * i, n - 1)));
+      page[i] = table[page_of(c, min(u + 32 * i, n - 1))];
 #pragma unroll
     for (int i = 0; i < K; ++i) {
       const int v = min(u + 32 * i, n - 1);
       const bool bad = page[i] < 0 || page[i] >= c.num_pages;
       const long long w = ((long long)(bad ? 0 : page[i]) * c.hkv + g) * c.page_size + (v - page_of(c, v) * c.page_size);
-      val[i] = __ldg(c.weights + w);
-      pos[i] = c.positions ? __ldg(c.positions + w) : v;
+      val[i] = c.weights[w];
+      pos[i] = c.positions ? c.positions[w] : v;
       page[i] = bad;
     }
 #pragma unroll

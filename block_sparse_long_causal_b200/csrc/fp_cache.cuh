@@ -10,6 +10,8 @@ namespace fp {
 // Programmatic dependent launch: a kernel that was launched with launch_pdl may start while the one before
 // it on the stream still runs; pdl_wait returns once that one has ended and its writes are visible.
 // pdl_trigger, in the earlier kernel, allows the start (at its end without it).
+// So nothing here reads through ld.global.nc (__ldg), which is for data that no one writes while the kernel runs: a
+// line that the SM holds from the kernel before would do for it. Plain loads see what pdl_wait waited for.
 __device__ __forceinline__ void pdl_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
 __device__ __forceinline__ void pdl_trigger() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
 template <typename... K, typename... A>
@@ -36,14 +38,14 @@ __device__ __forceinline__ int page_of(const CacheInfo& c, int u) {
 // is the caller's duty (n <= max_len is checked before any slot is used).
 __device__ __forceinline__ long long slot_row(const CacheInfo& c, int s, int u) {
   const int lp = page_of(c, u);
-  const int page = __ldg(c.block_table + (long long)s * c.max_pages + lp);
+  const int page = c.block_table[(long long)s * c.max_pages + lp];
   if (page < 0 || page >= c.num_pages) return -1;
   return (long long)page * c.page_size + (u - lp * c.page_size);
 }
 // Index of (slot, kv-head) in the weights and positions arrays [num_pages, Hkv, page_size], or -1.
 __device__ __forceinline__ long long slot_word(const CacheInfo& c, int s, int g, int u) {
   const int lp = page_of(c, u);
-  const int page = __ldg(c.block_table + (long long)s * c.max_pages + lp);
+  const int page = c.block_table[(long long)s * c.max_pages + lp];
   if (page < 0 || page >= c.num_pages) return -1;
   return ((long long)page * c.hkv + g) * c.page_size + (u - lp * c.page_size);
 }
@@ -61,9 +63,9 @@ __device__ __forceinline__ bool cache_table(const CacheInfo& c, long long* tab, 
   if (tid == 0) *s_bad = 0;
   __syncthreads();
   long long sum = 0;
-  bool bad = tid == 0 && (__ldg(c.cu_seqlens) != 0 || __ldg(c.cu_seqlens + S) != c.total_tokens);
+  bool bad = tid == 0 && (c.cu_seqlens[0] != 0 || c.cu_seqlens[S] != c.total_tokens);
   for (int s = a; s < b; ++s) {
-    const int lo = __ldg(c.cu_seqlens + s), hi = __ldg(c.cu_seqlens + s + 1), len = c.lens[s];
+    const int lo = c.cu_seqlens[s], hi = c.cu_seqlens[s + 1], len = c.lens[s];
     const bool ok = lo >= 0 && hi >= lo && hi <= c.total_tokens && len >= 0 && len <= c.max_len - (hi - lo);
     bad |= !ok;
     tab[s] = sum;

@@ -77,8 +77,8 @@ struct Cursor {
 __device__ __forceinline__ int unit_tiles(int L, int n) { return L > 0 ? (n + kKeysT - 1) / kKeysT : 0; }
 __device__ __forceinline__ void load_seq(Cursor& u, const CacheInfo& c, int s) {
   u.s = s;
-  u.seq0 = __ldg(c.cu_seqlens + s);
-  u.L = __ldg(c.cu_seqlens + s + 1) - u.seq0;
+  u.seq0 = c.cu_seqlens[s];
+  u.L = c.cu_seqlens[s + 1] - u.seq0;
   u.len = c.lens[s];
   u.n = u.len + u.L;
   u.kts = unit_tiles(u.L, u.n);
@@ -102,10 +102,10 @@ __device__ __forceinline__ bool find_share(const CacheInfo& c, Shares& sh, Curso
   const int lane = threadIdx.x & 31, S = c.num_seqs, per = (S + 31) / 32;
   const int a = min(S, lane * per), b = min(S, a + per);
   long long sum = 0;
-  bool bad = lane == 0 && (__ldg(c.cu_seqlens) != 0 || __ldg(c.cu_seqlens + S) != c.total_tokens);
+  bool bad = lane == 0 && (c.cu_seqlens[0] != 0 || c.cu_seqlens[S] != c.total_tokens);
 #pragma unroll 4
   for (int s = a; s < b; ++s) {
-    const int lo = __ldg(c.cu_seqlens + s), hi = __ldg(c.cu_seqlens + s + 1), len = c.lens[s];
+    const int lo = c.cu_seqlens[s], hi = c.cu_seqlens[s + 1], len = c.lens[s];
     const bool ok = lo >= 0 && hi >= lo && hi <= c.total_tokens && hi - lo <= c.max_new && len >= 0 &&
                     len <= c.max_len - (hi - lo);
     bad |= !ok;
@@ -264,8 +264,8 @@ __global__ void __launch_bounds__(kRowThreads, ctas_sm(NT)) cache_rows_kernel(co
                                (cur.g * c.group + (in ? r % c.group : 0)) * kHeadDim + rc;
 #pragma unroll
           for (int kk = 0; kk < 8; ++kk) {
-            qf[kQs ? 0 : t][kk][0] = in ? __ldg(reinterpret_cast<const uint32_t*>(q0 + kk * 16)) : 0u;
-            qf[kQs ? 0 : t][kk][1] = in ? __ldg(reinterpret_cast<const uint32_t*>(q0 + kk * 16 + 8)) : 0u;
+            qf[kQs ? 0 : t][kk][0] = in ? *reinterpret_cast<const uint32_t*>(q0 + kk * 16) : 0u;
+            qf[kQs ? 0 : t][kk][1] = in ? *reinterpret_cast<const uint32_t*>(q0 + kk * 16 + 8) : 0u;
           }
         }
       }
@@ -274,8 +274,8 @@ __global__ void __launch_bounds__(kRowThreads, ctas_sm(NT)) cache_rows_kernel(co
           const int r = e >> 4, ch = e & 15;
           uint4 y = make_uint4(0, 0, 0, 0);
           if (r < cur.L * c.group)
-            y = __ldg(reinterpret_cast<const uint4*>(p.q + (long long)(cur.seq0 + r / c.group) * p.q_stride +
-                                                     (cur.g * c.group + r % c.group) * kHeadDim) + ch);
+            y = reinterpret_cast<const uint4*>(p.q + (long long)(cur.seq0 + r / c.group) * p.q_stride +
+                                               (cur.g * c.group + r % c.group) * kHeadDim)[ch];
           *reinterpret_cast<uint4*>(smem + off_q(NT) + r * 256 + ((ch ^ (r & 7)) << 4)) = y;
         }
         __syncthreads();

@@ -66,8 +66,8 @@ __device__ __forceinline__ int key_tiles(const Unit& u, int tokens) {
 __device__ __forceinline__ Unit decode(const CacheInfo& c, const long long* tab, int TT, long long x) {
   Unit u;
   u.s = find_seq64(tab, c.num_seqs, x);
-  u.seq0 = __ldg(c.cu_seqlens + u.s);
-  u.L = __ldg(c.cu_seqlens + u.s + 1) - u.seq0;
+  u.seq0 = c.cu_seqlens[u.s];
+  u.L = c.cu_seqlens[u.s + 1] - u.seq0;
   u.len = c.lens[u.s];
   const int pairs = ((u.L + TT - 1) / TT + 1) / 2;
   const int local = (int)(x - tab[u.s]);

@@ -56,8 +56,8 @@ __device__ __forceinline__ long long head_steps(int L, int n, int TT) {
 }
 __device__ __forceinline__ void load_seq(Step& u, const CacheInfo& c, int s, int TT) {
   u.s = s;
-  u.seq0 = __ldg(c.cu_seqlens + s);
-  u.L = __ldg(c.cu_seqlens + s + 1) - u.seq0;
+  u.seq0 = c.cu_seqlens[s];
+  u.L = c.cu_seqlens[s + 1] - u.seq0;
   u.len = c.lens[s];
   u.n = u.len + u.L;
   u.R = (u.L + TT - 1) / TT;
@@ -435,7 +435,7 @@ __global__ void __launch_bounds__(kBK) cache_weights_join_kernel(const __grid_co
   if (meta[0] == 0) return;
   const CacheInfo& c = p.c;
   const int last = meta[1], s = meta[2], key = meta[4] * kBK + (int)threadIdx.x;
-  const int n = c.lens[s] + __ldg(c.cu_seqlens + s + 1) - __ldg(c.cu_seqlens + s);
+  const int n = c.lens[s] + c.cu_seqlens[s + 1] - c.cu_seqlens[s];
   if (key >= n) return;
   const long long at = slot_word(c, s, meta[3], key);
   if (at < 0) return;

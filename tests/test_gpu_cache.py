@@ -753,3 +753,45 @@ def test_chained_steps_equal_steps_that_wait(hq, hkv, page, B, L):
     for _ in range(2):
         for a, b in zip(run(False), want):
             assert torch.equal(a, b)
+
+
+def test_chained_evictions_equal_evictions_that_wait():
+    """Append, selection and compaction one after another without an attention between them: a selection reads
+    the weights and positions that the compaction before it has just moved, the next append the lengths."""
+    S, hkv, page, n0, steps = 4, 8, 16, 4000, 24
+    need = n0 // page + 2
+    g = torch.Generator().manual_seed(51)
+    table = torch.randperm(S * need, generator=g).view(S, need).to(torch.int32).cuda()
+    k, v = (torch.randn((S * need * page, hkv, D), generator=g).to(torch.bfloat16).cuda() for _ in range(2))
+    w = torch.rand((S * need, hkv, page), generator=g).cuda()
+    pos = torch.randint(0, n0, w.shape, generator=g, dtype=torch.int32).cuda()
+    lens = torch.tensor([n0, n0 - 1, n0 - 700, 1500], dtype=torch.int32, device="cuda")
+    nxt = torch.full((S,), n0, dtype=torch.int32, device="cuda")
+    p = fp.problem(list(range(S + 1)), hkv, hkv)
+    c = fp.kv_cache(p, k, v, lens, table, page, w, pos)
+    budgets = [n0 - 150 * i for i in range(1, steps + 1)]
+    bufs = [(torch.empty((S, hkv, B, 2), dtype=torch.int32, device="cuda"),
+             torch.empty((S, hkv), dtype=torch.int32, device="cuda"), torch.empty(S, dtype=torch.int32, device="cuda"))
+            for B in budgets]
+    st = torch.zeros(1, dtype=torch.int32, device="cuda")
+    ks, vs = (torch.randn((steps, S, hkv, D), generator=g).to(torch.bfloat16).cuda() for _ in range(2))
+    state = (k, v, w, pos, lens)
+    start = [t.clone() for t in state]
+
+    def run(wait):
+        for t, a in zip(state, start):
+            t.copy_(a)
+        for i, (B, b) in enumerate(zip(budgets, bufs)):
+            for call in (lambda: fp.cache_append(p, c, ks[i], vs[i], nxt, st),
+                         lambda: fp.cache_select(p, c, B, 4, 40, nxt, *b, st), lambda: fp.cache_compact(p, c, B, *b, st)):
+                call()
+                if wait:
+                    torch.cuda.synchronize()
+        torch.cuda.synchronize()
+        return [bits(t).clone() for t in state] + [t.clone() for b in bufs for t in b]
+
+    want = run(True)
+    assert int(st.item()) == 0 and lens.tolist() == [budgets[-1]] * S and min(int(b[1].min()) for b in bufs[-8:]) > 0
+    for _ in range(3):
+        for a, b in zip(run(False), want):
+            assert torch.equal(a, b)
