@@ -717,6 +717,11 @@ fp_status make_q_tmap(CUtensorMap* m, const void* base, int64_t tokens, int64_t 
   return FP_OK;
 }
 
+bool overlap(const void* a, int64_t a_bytes, const void* b, int64_t b_bytes) {
+  const uintptr_t x = reinterpret_cast<uintptr_t>(a), y = reinterpret_cast<uintptr_t>(b);
+  return a && b && x < y + (uintptr_t)b_bytes && y < x + (uintptr_t)a_bytes;
+}
+
 fp_status check_budget(int32_t budget, const int32_t* moves, const int32_t* counts, const int32_t* new_lens) {
   if (budget < 1) return fail(FP_ERR_INVALID_ARG, "budget=%d must be >= 1", budget);
   if (!moves || !counts || !new_lens)
@@ -867,6 +872,11 @@ fp_status fp_cache_select(const fp_problem* p, const fp_kv_cache* c, int32_t bud
     return fail(FP_ERR_INVALID_ARG, "sinks=%d and recent=%d must be non-negative with a sum of at most budget=%d",
                 sinks, recent, budget);
   if (!c->weights) return fail(FP_ERR_INVALID_ARG, "selection needs cache.weights");
+  // every (sequence, kv-head) reads lens and next_pos while others already write
+  const int64_t seqs = 4ll * p->num_seqs;
+  for (const int32_t* in : {(const int32_t*)c->lens, next_pos})
+    if (overlap(new_lens, seqs, in, seqs) || overlap(move_counts, seqs * p->num_kv_heads, in, seqs))
+      return fail(FP_ERR_INVALID_ARG, "new_lens and move_counts must not overlap cache.lens or next_pos");
   fp::SelectParams a;
   memset(&a, 0, sizeof a);
   a.c = cache_info(p, c);

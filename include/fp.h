@@ -405,7 +405,8 @@ FP_API fp_status fp_cache_attn(const fp_problem* p, const fp_kv_cache* c, const 
  * slot at or past the budget goes to the i-th evicted slot below it (both ascending).
  * moves: device int32 [num_seqs, Hkv, budget, 2], (source, destination), entries past the count are -1;
  * move_counts: device int32 [num_seqs, Hkv]; new_lens: device int32 [num_seqs], min(lens + L, budget).
- * Reads the cache's weights (required) and positions (if any); changes nothing of the cache. */
+ * Reads the cache's weights (required) and positions (if any); changes nothing of the cache: new_lens and
+ * move_counts must not overlap cache.lens or next_pos (FP_ERR_INVALID_ARG). */
 FP_API fp_status fp_cache_select(const fp_problem* p, const fp_kv_cache* c, int32_t budget, int32_t sinks,
                                  int32_t recent, const int32_t* next_pos, int32_t* moves, int32_t* move_counts,
                                  int32_t* new_lens, int32_t* dev_status, void* stream);

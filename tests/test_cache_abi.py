@@ -110,6 +110,24 @@ def test_calls_refuse_bad_arguments_before_launch():
     assert attn() == fp.FP_ERR_UNSUPPORTED
 
 
+def test_selection_refuses_results_that_overlap_what_it_reads():
+    """Other heads of a sequence still read its length and position when the first one writes its results."""
+    st, p, c = _cache(lens=C.c_void_p(1 << 20))
+    assert st == fp.FP_OK
+    c.weights = 4096
+
+    def select(cnt, nl, nxt=NULL):
+        return fp._lib.fp_cache_select(C.byref(p), C.byref(c), 64, 4, 8, nxt, OK, C.c_void_p(cnt), C.c_void_p(nl), NULL,
+                                       NULL)
+    lens, nxt, far = 1 << 20, 1 << 21, 1 << 22  # 3 sequences of 2 kv-heads: 12 and 24 bytes
+    for nl in (lens, lens + 8, lens - 8):
+        assert select(far, nl) == fp.FP_ERR_INVALID_ARG and "overlap" in _err()
+    for cnt in (lens, lens + 8, lens - 20):
+        assert select(cnt, far) == fp.FP_ERR_INVALID_ARG and "overlap" in _err()
+    assert select(far, nxt, C.c_void_p(nxt)) == fp.FP_ERR_INVALID_ARG and "overlap" in _err()
+    assert select(nxt - 20, far, C.c_void_p(nxt)) == fp.FP_ERR_INVALID_ARG and "overlap" in _err()
+
+
 def test_calls_without_new_tokens_need_no_tensors():
     st, p, c = _cache(cu=(0, 0, 0, 0))
     assert st == fp.FP_OK and c.max_new == 0
