@@ -818,6 +818,10 @@ fp_status fp_cache_attn(const fp_problem* p, const fp_kv_cache* c, const void* q
   if (p->total_tokens == 0) return FP_OK;
   if (!q || !out) return fail(FP_ERR_INVALID_ARG, "q and out must be non-NULL");
   if (!aligned16(q) || !aligned16(out)) return fail(FP_ERR_INVALID_ARG, "q and out must be 16-byte aligned");
+  const int64_t out_bytes = (int64_t)p->total_tokens * p->num_q_heads * p->head_dim * 2;
+  const int64_t q_bytes = (p->total_tokens - 1) * a.q_stride * 2 + (int64_t)p->num_q_heads * p->head_dim * 2;
+  if (decay >= 0.f && overlap(out, out_bytes, q, q_bytes))  // the weights are summed after out was written
+    return fail(FP_ERR_INVALID_ARG, "out must not overlap q when weights are collected");
   const int sms = sm_count();
   const int group = p->num_q_heads / p->num_kv_heads;
   const bool tiled = fp::cache_attn_tiled(c->max_new, group);

@@ -390,6 +390,7 @@ FP_API fp_status fp_cache_attn_workspace(const fp_problem* p, const fp_kv_cache*
  *   weights[u, g] = decay * weights[u, g] + sum over the new tokens t and q-heads h of g that see u of
  *                   exp(softmax_scale * q_th . k_u - lse_th)
  * (1: the weight collected so far; 0: that of this call alone, the old value is not read).
+ * q is read again for the weights: out must not overlap it then (FP_ERR_INVALID_ARG).
  * A row none of whose scores is above -infinity gives zeros and an lse of -infinity and adds no weight.
  * workspace: device, 256-byte aligned, scratch (calls that may run at the same time must not share it).
  * The result of a call does not depend on timing: the work's split is a function of the lengths. */

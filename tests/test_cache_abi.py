@@ -128,6 +128,22 @@ def test_selection_refuses_results_that_overlap_what_it_reads():
     assert select(nxt - 20, far, C.c_void_p(nxt)) == fp.FP_ERR_INVALID_ARG and "overlap" in _err()
 
 
+def test_collected_weights_refuse_an_output_over_the_queries():
+    """The weights of long pieces are summed from q after out was written."""
+    st, p, c = _cache()
+    assert st == fp.FP_OK
+    c.weights = 4096
+    n = C.c_int64(0)
+    assert fp._lib.fp_cache_attn_workspace(C.byref(p), C.byref(c), C.byref(n)) == fp.FP_OK
+
+    def attn(out, stride=0):
+        return fp._lib.fp_cache_attn(C.byref(p), C.byref(c), C.c_void_p(q), stride, C.c_float(0.0), OK, n.value,
+                                     C.c_void_p(out), NULL, C.c_float(0.5), NULL, NULL)
+    q, row = 1 << 24, 8 * 128 * 2  # 10 tokens of 8 heads
+    for out, stride in ((q, 0), (q + 9 * row, 0), (q - 9 * row, 0), (q + 9 * 2 * row, 2 * 8 * 128), (q + row, 2 * 8 * 128)):
+        assert attn(out, stride) == fp.FP_ERR_INVALID_ARG and "overlap" in _err()
+
+
 def test_calls_without_new_tokens_need_no_tensors():
     st, p, c = _cache(cu=(0, 0, 0, 0))
     assert st == fp.FP_OK and c.max_new == 0
