@@ -648,6 +648,10 @@ fp_status fp_paged_validate_lists(const fp_problem* p, const fp_paged_cache* c, 
 
 // ---- serving from a paged key/value cache
 namespace {
+// Slots of a sequence (2^30 of them are 256 GiB of keys a kv-head) and of a budget: the kernels step past the last one
+// by less than a tile or a grid's width in int32.
+constexpr int32_t kMaxSlots = 1 << 30;
+
 fp_status check_kv(const fp_problem* p, const fp_kv_cache* c) {
   fp_status st = check_problem(p);
   if (st != FP_OK) return st;
@@ -657,7 +661,7 @@ fp_status check_kv(const fp_problem* p, const fp_kv_cache* c) {
   if (!aligned16(c->k) || !aligned16(c->v) || !aligned16(c->weights) || !aligned16(c->positions))
     return fail(FP_ERR_INVALID_ARG, "cache.k, v, weights and positions must be 16-byte aligned");
   if (c->page_size < 16 || c->page_size % 16 || c->max_pages < 1 || c->num_pages < 1 || c->max_new < 0 ||
-      c->max_len < c->max_new || (int64_t)c->max_pages * c->page_size < c->max_len ||
+      c->max_len < c->max_new || c->max_len > kMaxSlots || (int64_t)c->max_pages * c->page_size < c->max_len ||
       (int64_t)c->num_pages * c->page_size > (int64_t)INT32_MAX)
     return fail(FP_ERR_INVALID_ARG, "inconsistent key/value cache (use fp_kv_cache_init)");
   return FP_OK;
@@ -723,7 +727,7 @@ bool overlap(const void* a, int64_t a_bytes, const void* b, int64_t b_bytes) {
 }
 
 fp_status check_budget(int32_t budget, const int32_t* moves, const int32_t* counts, const int32_t* new_lens) {
-  if (budget < 1) return fail(FP_ERR_INVALID_ARG, "budget=%d must be >= 1", budget);
+  if (budget < 1 || budget > kMaxSlots) return fail(FP_ERR_INVALID_ARG, "budget=%d outside [1, 2^30]", budget);
   if (!moves || !counts || !new_lens)
     return fail(FP_ERR_INVALID_ARG, "moves, move_counts and new_lens must be non-NULL");
   if ((reinterpret_cast<uintptr_t>(moves) & 7u) != 0)
@@ -745,6 +749,7 @@ fp_status fp_kv_cache_init(fp_kv_cache* c, const fp_problem* p, const int32_t* h
   if ((int64_t)num_pages * page_size > (int64_t)INT32_MAX)
     return fail(FP_ERR_INVALID_ARG, "num_pages * page_size exceeds 2^31 - 1 rows");
   const int64_t room = (int64_t)max_pages * page_size;
+  if (max_len > kMaxSlots) return fail(FP_ERR_INVALID_ARG, "max_len=%d exceeds 2^30", max_len);
   if (max_len < 0 || max_len > room)
     return fail(FP_ERR_INVALID_ARG, "max_len=%d outside [0, max_pages * page_size = %lld]", max_len, (long long)room);
   if (host_cu_seqlens[p->num_seqs] != p->total_tokens)
@@ -755,8 +760,7 @@ fp_status fp_kv_cache_init(fp_kv_cache* c, const fp_problem* p, const int32_t* h
     if (L < 0) return fail(FP_ERR_INVALID_ARG, "cu_seqlens must be non-decreasing (sequence %d)", s);
     if (L > max_new) max_new = L;
   }
-  // rooms past 2^30 slots are never filled (num_pages bounds the rows), and key positions stay in int32
-  const int64_t bound = max_len ? max_len : (room < (1 << 30) ? room : (1 << 30));
+  const int64_t bound = max_len ? max_len : (room < kMaxSlots ? room : kMaxSlots);
   if (max_new > bound)
     return fail(FP_ERR_INVALID_ARG, "%lld new tokens exceed max_len=%lld", (long long)max_new, (long long)bound);
   fp_kv_cache n;

@@ -337,7 +337,8 @@ FP_API fp_status fp_paged_validate_lists(const fp_problem* p, const fp_paged_cac
  *     next_pos[s] (device, optional) is the position of the sequence's first new token; NULL: slot and
  *     position are the same.
  *   - lens lives on the device so that a captured graph can be replayed as the sequences grow; the host
- *     promises max_len >= lens[s] + L_s (0 in fp_kv_cache_init: max_pages * page_size).
+ *     promises max_len >= lens[s] + L_s (0 in fp_kv_cache_init: max_pages * page_size; at most 2^30, and so
+ *     are budgets).
  * A step is: fp_cache_append, fp_cache_attn, then either fp_cache_select + fp_cache_compact (which sets
  * lens) or lens[s] += L_s by the caller; next_pos[s] += L_s by the caller.
  * Device arrays that disagree with this description (lens[s] + L_s > max_len, cu_seqlens other than

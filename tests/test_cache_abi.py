@@ -144,6 +144,28 @@ def test_collected_weights_refuse_an_output_over_the_queries():
         assert attn(out, stride) == fp.FP_ERR_INVALID_ARG and "overlap" in _err()
 
 
+def test_sizes_past_two_to_the_thirty_are_refused():
+    """Slot and list indices step past the last one in int32."""
+    top = 1 << 30
+    wide = dict(max_pages=(1 << 27) + 1, page_size=16)
+    st, _, c = _cache(max_len=top, **wide)
+    assert st == fp.FP_OK and c.max_len == top
+    st, _, c = _cache(**wide)
+    assert st == fp.FP_OK and c.max_len == top  # the room of the table is larger
+    assert _cache(max_len=top + 1, **wide)[0] == fp.FP_ERR_INVALID_ARG
+    st, p, c = _cache(max_len=top, **wide)
+    c.weights = 4096
+    P, K, L, far = C.byref(p), C.byref(c), fp._lib, C.c_void_p(1 << 40)
+    for budget in (top + 1, (1 << 31) - 1):
+        assert L.fp_cache_select(P, K, budget, 0, 0, NULL, far, OK, OK, NULL, NULL) == fp.FP_ERR_INVALID_ARG
+        assert "budget" in _err()
+        assert L.fp_cache_compact(P, K, budget, far, OK, OK, NULL, NULL) == fp.FP_ERR_INVALID_ARG and "budget" in _err()
+    c.max_len = top + 1  # edited past it: refused by every call
+    n = C.c_int64(0)
+    assert L.fp_cache_attn_workspace(P, K, C.byref(n)) == fp.FP_ERR_INVALID_ARG
+    assert L.fp_cache_append(P, K, OK, 0, OK, 0, NULL, NULL, NULL) == fp.FP_ERR_INVALID_ARG
+
+
 def test_calls_without_new_tokens_need_no_tensors():
     st, p, c = _cache(cu=(0, 0, 0, 0))
     assert st == fp.FP_OK and c.max_new == 0
