@@ -6,6 +6,7 @@
 #include <cstring>
 #include <mutex>
 
+#include "fp_cache.h"
 #include "fp_internal.h"
 
 namespace {
@@ -226,7 +227,7 @@ unsigned long long context_id() {
   return id;
 }
 
-cudaError_t set_max_smem(const void* func, int bytes, unsigned long long (&done)[kMaxCachedDevices], bool carveout) {
+static cudaError_t set_smem(const void* func, int bytes, unsigned long long (&done)[kMaxCachedDevices], bool carveout) {
   static std::mutex mu;
   int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);
@@ -242,6 +243,12 @@ cudaError_t set_max_smem(const void* func, int bytes, unsigned long long (&done)
     e = cudaFuncSetAttribute(func, cudaFuncAttributePreferredSharedMemoryCarveout, cudaSharedmemCarveoutMaxShared);
   if (e == cudaSuccess && cached) done[dev] = context_id();  // the call above made the context current
   return e;
+}
+cudaError_t set_max_smem(const void* func, int bytes, unsigned long long (&done)[kMaxCachedDevices]) {
+  return set_smem(func, bytes, done, false);
+}
+cudaError_t set_max_smem_carveout(const void* func, int bytes, unsigned long long (&done)[kMaxCachedDevices]) {
+  return set_smem(func, bytes, done, true);
 }
 }  // namespace fp
 

@@ -1,8 +1,8 @@
 // fp_cache.cuh -- what the key/value cache kernels share: the launch description of a cache, page
 // look-up and the per-launch tables that turn a work index into (sequence, unit).
 #pragma once
+#include "fp_cache.h"
 #include "fp_dev.cuh"
-#include "fp_internal.h"
 #include "fp_seq.cuh"
 
 namespace fp {

@@ -711,12 +711,12 @@ cudaError_t launch_cache_attn(const CacheAttnParams& p, bool tiled, int sms, cud
   }
   const int nt = row_tiles((int64_t)p.c.max_new * p.c.group), grid = ctas_sm(nt) * sms;
   void (*fn)(const CacheAttnParams) = nt == 1 ? cache_rows_kernel<1> : nt == 2 ? cache_rows_kernel<2> : cache_rows_kernel<4>;
-  if ((e = set_max_smem(reinterpret_cast<const void*>(fn), row_smem(nt), attr_rows[nt], true)) != cudaSuccess) return e;
+  if ((e = set_max_smem_carveout(reinterpret_cast<const void*>(fn), row_smem(nt), attr_rows[nt])) != cudaSuccess) return e;
   if ((e = launch_pdl(fn, dim3(grid), kRowThreads, row_smem(nt), st, p)) != cudaSuccess) return e;
-  if ((e = set_max_smem(reinterpret_cast<const void*>(cache_join_kernel), 0, attr[0], true)) != cudaSuccess) return e;
+  if ((e = set_max_smem_carveout(reinterpret_cast<const void*>(cache_join_kernel), 0, attr[0])) != cudaSuccess) return e;
   e = launch_pdl(cache_join_kernel, dim3(sms), 32 * kJoinWarps, 0, st, p, grid);
   if (e != cudaSuccess || !(p.decay >= 0.f)) return e;
-  if ((e = set_max_smem(reinterpret_cast<const void*>(cache_rows_weights_kernel), 0, attr[1], true)) != cudaSuccess)
+  if ((e = set_max_smem_carveout(reinterpret_cast<const void*>(cache_rows_weights_kernel), 0, attr[1])) != cudaSuccess)
     return e;
   return launch_pdl(cache_rows_weights_kernel, dim3(4 * sms), 256, 0, st, p);
 }

@@ -921,7 +921,7 @@ cudaError_t launch_cache_tiles(const CacheAttnParams& p, int sms, cudaStream_t s
   static unsigned long long attr[2][kMaxCachedDevices] = {};
   cudaError_t e = set_max_smem(reinterpret_cast<const void*>(tiles::cache_tiles_kernel), tiles::smem_bytes(kMaxSeqs), attr[0]);
   if (e == cudaSuccess)
-    e = set_max_smem(reinterpret_cast<const void*>(tiles::cache_tiles_join_kernel), 0, attr[1], true);
+    e = set_max_smem_carveout(reinterpret_cast<const void*>(tiles::cache_tiles_join_kernel), 0, attr[1]);
   if (e != cudaSuccess) return e;
   e = launch_pdl(tiles::cache_tiles_kernel, dim3(sms), tiles::kThreads, tiles::smem_bytes(p.c.num_seqs), st, p);
   if (e != cudaSuccess || sms < 2) return e;

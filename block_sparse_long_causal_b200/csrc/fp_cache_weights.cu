@@ -451,7 +451,7 @@ cudaError_t launch_cache_weights(const CacheAttnParams& p, int sms, cudaStream_t
   cudaError_t e = set_max_smem(reinterpret_cast<const void*>(cw::cache_tiles_weights_kernel), cw::smem_bytes(kMaxSeqs),
                                attr[0]);
   if (e == cudaSuccess)
-    e = set_max_smem(reinterpret_cast<const void*>(cw::cache_weights_join_kernel), 0, attr[1], true);
+    e = set_max_smem_carveout(reinterpret_cast<const void*>(cw::cache_weights_join_kernel), 0, attr[1]);
   if (e == cudaSuccess)
     e = launch_pdl(cw::cache_tiles_weights_kernel, dim3(sms), cw::kThreads, cw::smem_bytes(p.c.num_seqs), st, p);
   if (e != cudaSuccess || sms < 2) return e;

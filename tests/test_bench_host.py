@@ -80,3 +80,10 @@ def test_measured_traffic_follows_the_source_hash(tmp_path, monkeypatch):
     assert bench.measured_traffic("attn_kernel<128>", "w128k") is None      # sources changed
     os.remove(tmp_path / "a.cu")
     assert bench.measured_traffic("attn_kernel<128>", "w128k") is None      # a source is missing
+
+
+def test_the_committed_traffic_record_is_of_these_sources():
+    with open(os.path.join(bench.ROOT, "profiles", "attn_kernel_traffic.json")) as f:
+        rec = json.load(f)
+    got = bench.measured_traffic(rec["kernel"], rec["workload"])
+    assert got == rec["dram_bytes_read"] + rec["dram_bytes_write"] > 4.0e9
