@@ -29,6 +29,14 @@ cudaError_t launch_pdl(void (*kernel)(K...), dim3 grid, int threads, int smem, c
   return cudaLaunchKernelEx(&cfg, kernel, args...);
 }
 
+// 3-D tiled load global -> shared (Q as tokens x heads x columns); tma_load_2d's rules.
+__device__ __forceinline__ void tma_load_3d(uint32_t dst, const void* tmap, uint32_t bar, int x, int y, int z) {
+  asm volatile(
+      "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%3, %4, %5}], [%2];"
+      ::"r"(dst), "l"(reinterpret_cast<uint64_t>(tmap)), "r"(bar), "r"(x), "r"(y), "r"(z)
+      : "memory");
+}
+
 // u / page_size by a multiplication (a division by a run-time number is some twenty instructions).
 __device__ __forceinline__ int page_of(const CacheInfo& c, int u) {
   return (int)(__umulhi((unsigned)u, c.page_mul) >> c.page_shift);

@@ -1,6 +1,6 @@
 // fp_cache_attn.cu -- attention of new tokens over a paged key/value cache, with the attention weight
-// that every cached slot collects: the schedule for few rows (single tokens, short drafts), the join of
-// split units for both schedules, and the entry that picks one.
+// that every cached slot collects: the schedule for few rows (single tokens, short drafts) with the join of
+// its split units, and the entry that picks a schedule.
 //
 //   o_th = sum_u p_thu v_u,  p_thu = exp(scale q_th . k_u - lse_th),  u <= lens[s] + t
 //   w_ug = decay * w_ug + sum_{t, h in group g} p_thu

@@ -1,5 +1,5 @@
 // fp_cache_tiles.cu -- attention of new tokens over a paged key/value cache on the tcgen05 tensor cores:
-// the schedule for calls whose sequences bring more packed rows than the 16-row kernel's tile holds.
+// the schedule for calls whose longest piece has more packed rows than the few-row kernel takes (32).
 //
 // A row tile is 128 / G whole tokens with the G q-heads of one kv-head (row r: token r / G, head r % G),
 // so that a K/V tile is read once for all heads of its group. A unit is two neighbouring row tiles of one
@@ -97,13 +97,6 @@ __device__ __forceinline__ long long unit_at(long long i, long long N, unsigned 
 constexpr int kCost1 = 2, kCost2 = 3, kUnitCost = 6;
 __device__ __forceinline__ int tile_cost(const Unit& u, int TT) { return (2 * u.m + 1) * TT < u.L ? kCost2 : kCost1; }
 __device__ __forceinline__ int tiles_before(long long cost, int w) { return (int)((cost + w - 1) / w); }
-
-__device__ __forceinline__ void tma_load_3d(uint32_t dst, const void* tmap, uint32_t bar, int x, int y, int z) {
-  asm volatile(
-      "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%3, %4, %5}], [%2];"
-      ::"r"(dst), "l"(reinterpret_cast<uint64_t>(tmap)), "r"(bar), "r"(x), "r"(y), "r"(z)
-      : "memory");
-}
 
 __global__ void __launch_bounds__(kThreads, 1) cache_tiles_kernel(const __grid_constant__ CacheAttnParams p) {
   extern __shared__ __align__(1024) unsigned char smem_raw[];

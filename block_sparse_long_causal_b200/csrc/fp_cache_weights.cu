@@ -100,13 +100,6 @@ __device__ __forceinline__ void step_next(Step& u, const CacheInfo& c, int TT, b
   u.rt = u.rt0 = first_row_tile(u.len, u.kt, TT);
 }
 
-__device__ __forceinline__ void tma_load_3d(uint32_t dst, const void* tmap, uint32_t bar, int x, int y, int z) {
-  asm volatile(
-      "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%3, %4, %5}], [%2];"
-      ::"r"(dst), "l"(reinterpret_cast<uint64_t>(tmap)), "r"(bar), "r"(x), "r"(y), "r"(z)
-      : "memory");
-}
-
 __global__ void __launch_bounds__(kThreads, 1) cache_tiles_weights_kernel(const __grid_constant__ CacheAttnParams p) {
   extern __shared__ __align__(1024) unsigned char smem_raw[];
   unsigned char* smem = (unsigned char*)(((uintptr_t)smem_raw + 1023) & ~(uintptr_t)1023);
