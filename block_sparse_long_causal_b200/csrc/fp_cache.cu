@@ -92,7 +92,6 @@ constexpr int kSelThreads = 512, kSelWarps = kSelThreads / 32;
 constexpr int kSelCluster = 16;      // largest cluster
 constexpr int kSelSpan = 8192;       // slots a CTA is meant to take (16 a thread)
 constexpr int kSelKeysMax = 24576;   // keys kept in shared memory (96 KB: two CTAs fit an SM)
-constexpr int kSelRead = 10;         // slots a lane reads at once where that is all of them (8 otherwise)
 constexpr int kSelBins = 2048;
 constexpr int kSelCand = 6144;       // keys of the first digit's class that a CTA may list (24 KB)
 static_assert(kSelBins == 4 * kSelThreads, "a thread sums four bins");
@@ -147,6 +146,8 @@ __global__ void __launch_bounds__(kSelThreads, 2) select_kernel(const __grid_con
   // positions at or past `young` are protected (the difference cannot overflow: 64 bits)
   const long long young = (long long)(p.next_pos ? p.next_pos[s] : len) + L - p.recent;
   bool bad_page = false;
+  const bool with_pos = c.positions != nullptr;  // (a branch in front of every read took 0.3 us)
+  const int32_t* positions = with_pos ? c.positions : reinterpret_cast<const int32_t*>(c.weights);
   const int32_t* table = c.block_table + (long long)s * c.max_pages;
   // keys of slots u, u + 32, ... (K of them; past the last slot: anything), all their reads in flight together
   auto read_keys = [&](int u, uint32_t* out, auto count) {
@@ -162,13 +163,14 @@ __global__ void __launch_bounds__(kSelThreads, 2) select_kernel(const __grid_con
       const bool bad = page[i] < 0 || page[i] >= c.num_pages;
       const long long w = ((long long)(bad ? 0 : page[i]) * c.hkv + g) * c.page_size + (v - page_of(c, v) * c.page_size);
       val[i] = c.weights[w];
-      pos[i] = c.positions ? c.positions[w] : v;
+      pos[i] = positions[w];  // (the weights where the cache has no positions)
       page[i] = bad;
     }
 #pragma unroll
     for (int i = 0; i < K; ++i) {
       bad_page |= page[i] != 0;
-      out[i] = page[i] ? 0u : rank_key(val[i], pos[i] < p.sinks || pos[i] >= young);
+      const int at = with_pos ? pos[i] : u + 32 * i;
+      out[i] = page[i] ? 0u : rank_key(val[i], at < p.sinks || at >= young);
     }
   };
   const int wspan = (int)((((long long)n + C * kSelWarps - 1) / (C * kSelWarps) + 31) & ~31ll);  // slots a warp
@@ -190,8 +192,12 @@ __global__ void __launch_bounds__(kSelThreads, 2) select_kernel(const __grid_con
           if (u + 32 * i < u1) s_keys[u + 32 * i - base] = k[i];
       }
     };
-    if (wspan <= 32 * kSelRead) read_all(std::integral_constant<int, kSelRead>());  // one round of reads
-    else read_all(std::integral_constant<int, 8>());
+    // slots a lane reads at once: of four and five what leaves the fewer look-ups past the range's end (16 sequences of
+    // 4.1K slots, 9 a lane: 15.9 and 15.3 us; of 0.3K, 1 a lane: 8.6 and 8.9; 128K slots of 8 heads, 16 a lane: 35.2 and
+    // 36.0; eight or ten at once 9.2 to 9.7 for 0.3K)
+    const int per = wspan / 32;
+    if ((per + 3) / 4 * 4 < (per + 4) / 5 * 5) read_all(std::integral_constant<int, 4>());
+    else read_all(std::integral_constant<int, 5>());
     __syncwarp();  // a warp reads back its own keys only
   }
   if (!kept || u0 + lane >= u1) fill();  // the lanes that had nothing to read
