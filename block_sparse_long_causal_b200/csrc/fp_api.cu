@@ -903,7 +903,7 @@ fp_status fp_cache_select(const fp_problem* p, const fp_kv_cache* c, int32_t bud
   a.move_counts = move_counts;
   a.new_lens = new_lens;
   a.dev_status = dev_status;
-  return cuda_status(fp::launch_select(a, sm_count(), static_cast<cudaStream_t>(stream)), "selection launch");
+  return cuda_status(fp::launch_select(a, static_cast<cudaStream_t>(stream)), "selection launch");
 }
 
 fp_status fp_cache_compact(const fp_problem* p, const fp_kv_cache* c, int32_t budget, const int32_t* moves,

@@ -2,6 +2,7 @@
 // of the slots that stay by collected attention weight, compaction.
 #include <cooperative_groups.h>
 
+#include <mutex>
 #include <type_traits>
 
 #include "fp_cache.cuh"
@@ -91,14 +92,16 @@ __device__ __forceinline__ uint32_t rank_key(float w, bool safe) {
 constexpr int kSelThreads = 512, kSelWarps = kSelThreads / 32;
 constexpr int kSelCluster = 16;      // largest cluster
 constexpr int kSelSpan = 8192;       // slots a CTA is meant to take (16 a thread)
-constexpr int kSelKeysMax = 24576;   // keys kept in shared memory (96 KB: two CTAs fit an SM)
+// Keys that a CTA keeps in shared memory: with 36 KB of other arrays 226 KB where an SM holds one CTA, 112 KB where
+// it holds two
+constexpr int kSelKeys1 = 48640, kSelKeys2 = 19456;
 constexpr int kSelBins = 2048;
 constexpr int kSelCand = 6144;       // keys of the first digit's class that a CTA may list (24 KB)
 static_assert(kSelBins == 4 * kSelThreads, "a thread sums four bins");
 
 // One cluster per (sequence, kv-head); each of its CTAs takes a contiguous range of the slots, a
 // contiguous part of it per warp. The slots are read once: their keys stay in shared memory (a range
-// longer than kSelKeysMax is read again in every pass). The key of rank `budget` is found by a radix select,
+// that they do not fit is read again in every pass). The key of rank `budget` is found by a radix select,
 // three passes of 11, 11 and 10 bits over the keys that match the prefix so far; a CTA adds its
 // occupied bins (few: weights cluster) to every CTA's sums through distributed shared memory, one cluster
 // barrier a pass. After the first digit its class is usually small (a few percent): every CTA lists its
@@ -107,15 +110,20 @@ static_assert(kSelBins == 4 * kSelThreads, "a thread sums four bins");
 // after a scan over the cluster's warps writes its holes (evicted slots below the budget) and sources (kept
 // slots at or past it) in ascending order.
 // Bound by latency, not by its 8 bytes a slot: of 15 us for 16 sequences of 4.1K slots 4 go to the reads, 2 to 3
-// to each pass, 2 to the list. The loops keep several slots a lane in flight. Clusters of 8 or 4 CTAs took 47 and
-// 147 us where 16 took 44 (the range of a fourth does not fit shared memory). Every write is
+// to each pass, 2 to the list. The loops keep several slots a lane in flight. Clusters of 8 CTAs take 39 us for 128K
+// slots of 8 heads where 16 take 36. Every write is
 // bounded by itself: the passes over a range that is read again would disagree if another stream changed the
 // weights meanwhile.
 __global__ void __launch_bounds__(kSelThreads, 2) select_kernel(const __grid_constant__ SelectParams p, const int keys_cap) {
   extern __shared__ uint32_t s_keys[];
-  __shared__ __align__(16) unsigned s_hist[kSelBins], s_sum[2][kSelBins];
+  // the list is written once every CTA has added to the first pass's sums and this one has read them; from then on
+  // no sums of the cluster are formed
+  __shared__ __align__(16) union {
+    unsigned sum[2][kSelBins];
+    uint32_t list[kSelCand];
+  } s_u;
+  __shared__ __align__(16) unsigned s_hist[kSelBins];
   __shared__ unsigned s_tot[kSelWarps], s_pick[3], s_listed;
-  uint32_t* s_list = s_keys + keys_cap;
   __shared__ int4 s_cnt[kSelWarps];                // slots above / at the threshold, below / past the budget
   __shared__ int s_eq[kSelCluster * kSelWarps + 1], s_hole[kSelCluster * kSelWarps + 1], s_from[kSelCluster * kSelWarps + 1];
   __shared__ int s_part[3][8];
@@ -179,7 +187,7 @@ __global__ void __launch_bounds__(kSelThreads, 2) select_kernel(const __grid_con
   const int u0 = (int)min((long long)n, first + warp * wspan), u1 = min(n, u0 + wspan);
   const bool kept = kSelWarps * wspan <= keys_cap;
   *reinterpret_cast<uint4*>(&s_hist[4 * tid]) = make_uint4(0, 0, 0, 0);
-  *reinterpret_cast<uint4*>(&s_sum[0][4 * tid]) = make_uint4(0, 0, 0, 0);
+  *reinterpret_cast<uint4*>(&s_u.sum[0][4 * tid]) = make_uint4(0, 0, 0, 0);
   if (kept) {
     auto read_all = [&](auto count) {
       constexpr int K = decltype(count)::value;
@@ -231,7 +239,7 @@ __global__ void __launch_bounds__(kSelThreads, 2) select_kernel(const __grid_con
     if (listed) {
       const int per = kSelThreads / C, r = tid / per;  // threads per list, and this thread's list
       const unsigned num = min(*cluster.map_shared_rank(&s_listed, r), (unsigned)kSelCand);
-      const uint32_t* list = cluster.map_shared_rank(s_list, r);
+      const uint32_t* list = cluster.map_shared_rank(s_u.list, r);
 #pragma unroll 4
       for (unsigned j = tid % per; j < num; j += per) {
         const uint32_t k = list[j];
@@ -261,9 +269,9 @@ __global__ void __launch_bounds__(kSelThreads, 2) select_kernel(const __grid_con
     uint4 cnt = *reinterpret_cast<const uint4*>(&s_hist[bin]);
     *reinterpret_cast<uint4*>(&s_hist[bin]) = make_uint4(0, 0, 0, 0);
     if (C > 1 && !listed) {
-      unsigned* sums = s_sum[pass & 1];
+      unsigned* sums = s_u.sum[pass & 1];
       // the other buffer is zeroed for the next pass, which no CTA begins before the barrier below
-      *reinterpret_cast<uint4*>(&s_sum[(pass + 1) & 1][bin]) = make_uint4(0, 0, 0, 0);
+      *reinterpret_cast<uint4*>(&s_u.sum[(pass + 1) & 1][bin]) = make_uint4(0, 0, 0, 0);
       if (cnt.x | cnt.y | cnt.z | cnt.w)
         for (int r = 0; r < C; ++r) {
           unsigned* dst = cluster.map_shared_rank(&sums[bin], r);
@@ -312,7 +320,7 @@ __global__ void __launch_bounds__(kSelThreads, 2) select_kernel(const __grid_con
         if (lane == 0 && m) at = atomicAdd(&s_listed, (unsigned)__popc(m));
         at = __shfl_sync(kFullMask, at, 0);
         at += __popc(m & ((1u << lane) - 1u));
-        if (match && at < kSelCand) s_list[at] = k;
+        if (match && at < kSelCand) s_u.list[at] = k;
       });
       sync_all();
     }
@@ -402,32 +410,100 @@ __global__ void __launch_bounds__(kSelThreads, 2) select_kernel(const __grid_con
   if (C > 1) cluster.sync();  // no CTA ends while another still reads its counts
 }
 
-cudaError_t launch_select(const SelectParams& p, int sms, cudaStream_t st) {
-  static unsigned long long attr[kMaxCachedDevices] = {};
-  const void* fn = reinterpret_cast<const void*>(select_kernel);
-  cudaError_t e = set_max_smem(fn, (kSelKeysMax + kSelCand) * 4, attr);
-  if (e != cudaSuccess) return e;
-  // clusters grow with the longest sequence that there may be, while one wave of two CTAs an SM holds them
-  const long long pairs = (long long)p.c.num_seqs * p.c.hkv;
-  int C = 1;
-  while (C < kSelCluster && (long long)C * kSelSpan < p.c.max_len && pairs * C * 2 <= 2 * sms) C *= 2;
-  if (C > 8 && (e = cudaFuncSetAttribute(fn, cudaFuncAttributeNonPortableClusterSizeAllowed, 1)) != cudaSuccess) return e;
-  const long long span = (((long long)p.c.max_len + C * kSelWarps - 1) / (C * kSelWarps) + 31) / 32 * 32 * kSelWarps;
-  const int cap = (int)(span < kSelKeysMax ? span : kSelKeysMax);
-  cudaLaunchAttribute at[2];
-  at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  at[0].val.programmaticStreamSerializationAllowed = 1;
-  at[1].id = cudaLaunchAttributeClusterDimension;
-  at[1].val.clusterDim.x = C;
-  at[1].val.clusterDim.y = at[1].val.clusterDim.z = 1;
+// Clusters of 1, 2, 4, 8 and 16 CTAs that the device holds at once, with kSelKeys1 and with kSelKeys2 keys a CTA.
+struct SelFit {
+  int n[5][2];
+};
+static cudaLaunchConfig_t select_config(cudaLaunchAttribute (&at)[2], int grid, int C, int keys, cudaStream_t st) {
+  at[0].id = cudaLaunchAttributeClusterDimension;
+  at[0].val.clusterDim.x = C;
+  at[0].val.clusterDim.y = at[0].val.clusterDim.z = 1;
+  at[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  at[1].val.programmaticStreamSerializationAllowed = 1;
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3((unsigned)(pairs * C));
+  cfg.gridDim = dim3((unsigned)grid);
   cfg.blockDim = dim3(kSelThreads);
-  cfg.dynamicSmemBytes = ((size_t)cap + kSelCand) * 4;
+  cfg.dynamicSmemBytes = (size_t)keys * 4;
   cfg.stream = st;
   cfg.attrs = at;
+  cfg.numAttrs = 1;  // the cluster; the launch adds the other
+  return cfg;
+}
+// Asked once per device and context (the kernel's attributes are set with it).
+static cudaError_t select_fit(SelFit& fit) {
+  static std::mutex mu;
+  static unsigned long long known[kMaxCachedDevices] = {};
+  static SelFit fits[kMaxCachedDevices];
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  std::lock_guard<std::mutex> lock(mu);
+  const bool cached = dev >= 0 && dev < kMaxCachedDevices;
+  unsigned long long id = cached ? context_id() : 0;
+  if (id != 0 && known[dev] == id) {
+    fit = fits[dev];
+    return cudaSuccess;
+  }
+  const void* fn = reinterpret_cast<const void*>(select_kernel);
+  e = cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, kSelKeys1 * 4);
+  if (e == cudaSuccess) e = cudaFuncSetAttribute(fn, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
+  if (e != cudaSuccess) return e;
+  for (int i = 0; i < 5; ++i)
+    for (int two = 0; two < 2; ++two) {
+      cudaLaunchAttribute at[2];
+      const cudaLaunchConfig_t cfg = select_config(at, 1 << i, 1 << i, two ? kSelKeys2 : kSelKeys1, nullptr);
+      if (cudaOccupancyMaxActiveClusters(&fit.n[i][two], select_kernel, &cfg) != cudaSuccess) {
+        cudaGetLastError();  // a size that this device does not take
+        fit.n[i][two] = 0;
+      }
+    }
+  id = cached ? context_id() : 0;  // the calls above made the context current
+  if (id != 0) {
+    fits[dev] = fit;
+    known[dev] = id;
+  }
+  return cudaSuccess;
+}
+
+cudaError_t launch_select(const SelectParams& p, cudaStream_t st) {
+  SelFit fit;
+  cudaError_t e = select_fit(fit);
+  if (e != cudaSuccess) return e;
+  // The longest sequence that there may be (max_len) sets the CTAs of a cluster and their buffers: the lengths are on
+  // the device. In this order:
+  //  - the largest cluster that leaves about kSelSpan slots a CTA, whose ranges' keys fit and of which the device holds
+  //    all at once: two CTAs an SM with up to kSelKeys2 keys each, one with up to kSelKeys1 (32 heads of 128K slots in
+  //    clusters of 4: 54 us, of 8 in several waves 109);
+  //  - a CTA a head with up to kSelKeys1, in several waves (160 heads of 20K slots: 81 us; read again in every pass, by
+  //    two CTAs an SM, 91);
+  //  - two CTAs an SM, in the largest clusters that the device holds at once; what does not fit is read again in every
+  //    pass. 8 heads of 500K slots: 143 us, kept by one CTA an SM in two waves 133; but 16 sequences of 4.1K slots that may
+  //    grow to 128K: 18 us, in two waves 27.
+  const long long pairs = (long long)p.c.num_seqs * p.c.hkv;
+  auto span = [&](int C) { return (((long long)p.c.max_len + C * kSelWarps - 1) / (C * kSelWarps) + 31) / 32 * 32 * kSelWarps; };
+  int top = 0;
+  while (top < 4 && (long long)(1 << top) * kSelSpan < p.c.max_len) ++top;
+  int size = -1;
+  long long keys = 0;
+  for (int i = top; i >= 0 && size < 0; --i) {
+    const long long k = span(1 << i);
+    if (k <= kSelKeys1 && pairs <= fit.n[i][k <= kSelKeys2]) {
+      size = i;
+      keys = k;
+    }
+  }
+  if (size < 0 && span(1) <= kSelKeys1) {
+    size = 0;
+    keys = span(1);
+  }
+  if (size < 0) {
+    for (size = top; size > 0 && pairs > fit.n[size][1];) --size;
+    keys = kSelKeys2;
+  }
+  cudaLaunchAttribute at[2];
+  cudaLaunchConfig_t cfg = select_config(at, (int)(pairs << size), 1 << size, (int)keys, st);
   cfg.numAttrs = 2;
-  return cudaLaunchKernelEx(&cfg, select_kernel, p, cap);
+  return cudaLaunchKernelEx(&cfg, select_kernel, p, (int)keys);
 }
 
 // ------------------------------------------------------------------------ compaction ------------

@@ -83,7 +83,7 @@ cudaError_t set_max_smem_carveout(const void* func, int bytes, unsigned long lon
 
 // Key/value cache (fp_cache.cu, fp_cache_attn.cu).
 cudaError_t launch_append(const AppendParams& p, cudaStream_t st);
-cudaError_t launch_select(const SelectParams& p, int sms, cudaStream_t st);
+cudaError_t launch_select(const SelectParams& p, cudaStream_t st);
 cudaError_t launch_compact(const CompactParams& p, int sms, cudaStream_t st);
 constexpr int kMetaWords = 8;               // ints per CTA that describe the unit its share begins inside of
 // Schedule of the attention call: units of up to 32 rows (fp_cache_attn.cu) or 128-row tiles (fp_cache_tiles.cu).

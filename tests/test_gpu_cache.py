@@ -605,6 +605,42 @@ def test_selection_of_more_slots_than_shared_memory_holds(kind):
         assert torch.equal(mv[:, h:h + 1].cpu(), m) and int(cnt[0, h]) == int(cc)
 
 
+@pytest.mark.parametrize("kind", ["ties", "tail"])
+@pytest.mark.parametrize("S,hkv,n,width,B", [
+    (1, 8, 300000, 0, 4000),       # a cluster a head, a large part of the keys in every CTA
+    (1, 3, 200001, 0, 150000),
+    (1, 8, 800001, 0, 20000),      # clusters that read their slots again in every pass
+    (16, 8, 3000, 131072, 1000),   # short sequences with a block table for long ones
+    (16, 8, 40001, 131072, 5000),
+    (20, 8, 30000, 0, 3000),       # more heads than the GPU holds at once
+    (1, 160, 60001, 0, 4000),      # the same, read again in every pass
+])
+def test_selection_by_what_the_gpu_holds(S, hkv, n, width, B, kind):
+    page, sinks, recent = 256, 4, B // 3
+    need = -(-n // page)
+    g = torch.Generator(device="cuda").manual_seed(n + B)
+    table = torch.full((S, max(need, width // page)), -9, dtype=torch.int32, device="cuda")
+    table[:, :need] = torch.randperm(S * need, generator=g, device="cuda").view(S, need).to(torch.int32)
+    w = torch.rand((S * need, hkv, page), generator=g, device="cuda")
+    w = (w * 50).floor() / 50 if kind == "ties" else torch.exp(8 * w)
+    pos = torch.randint(0, 2 * n, w.shape, generator=g, dtype=torch.int32, device="cuda")
+    k = torch.empty((S * need * page, hkv, D), dtype=torch.bfloat16, device="cuda")  # selection does not read it
+    lens, nxt = (torch.full((S,), v, dtype=torch.int32, device="cuda") for v in (n, 2 * n))
+    p = fp.problem([0] * (S + 1), hkv, hkv)
+    c = fp.kv_cache(p, k, k, lens, table, page, w, pos)
+    mv = torch.empty((S, hkv, B, 2), dtype=torch.int32, device="cuda")
+    cnt, nl = torch.empty((S, hkv), dtype=torch.int32, device="cuda"), torch.empty(S, dtype=torch.int32, device="cuda")
+    st = torch.zeros(1, dtype=torch.int32, device="cuda")
+    fp.cache_select(p, c, B, sinks, recent, nxt, mv, cnt, nl, st)
+    torch.cuda.synchronize()
+    assert int(st.item()) == 0 and nl.tolist() == [B] * S
+    for s, h in {(0, 0), (S - 1, hkv - 1), (S // 2, hkv // 3)}:
+        x = {"lens": [n], "new": [0], "hkv": 1, "page": page, "table": table[s:s + 1].cpu(), "w": w[:, h:h + 1].cpu(),
+             "pos": pos[:, h:h + 1].cpu()}
+        m, cc, _ = oracle_select(x, B, sinks, recent, [2 * n])
+        assert int(cnt[s, h]) == int(cc) and torch.equal(mv[s, h].cpu(), m[0, 0])
+
+
 def test_selection_without_positions_ranks_slots():
     x, _ = select_case(5, [300], [1], 2, 16, "plain")
     d = Dev(x, positions=False)
