@@ -111,9 +111,8 @@ static_assert(kSelBins == 4 * kSelThreads, "a thread sums four bins");
 // slots at or past it) in ascending order.
 // Bound by latency, not by its 8 bytes a slot: of 15 us for 16 sequences of 4.1K slots 4 go to the reads, 2 to 3
 // to each pass, 2 to the list. The loops keep several slots a lane in flight. Clusters of 8 CTAs take 39 us for 128K
-// slots of 8 heads where 16 take 36. Every write is
-// bounded by itself: the passes over a range that is read again would disagree if another stream changed the
-// weights meanwhile.
+// slots of 8 heads where 16 take 36. Every write is bounded by itself: the passes over a range that is read again would
+// disagree if another stream changed the weights meanwhile.
 __global__ void __launch_bounds__(kSelThreads, 2) select_kernel(const __grid_constant__ SelectParams p, const int keys_cap) {
   extern __shared__ uint32_t s_keys[];
   // the list is written once every CTA has added to the first pass's sums and this one has read them; from then on
@@ -472,8 +471,8 @@ cudaError_t launch_select(const SelectParams& p, cudaStream_t st) {
   // The longest sequence that there may be (max_len) sets the CTAs of a cluster and their buffers: the lengths are on
   // the device. In this order:
   //  - the largest cluster that leaves about kSelSpan slots a CTA, whose ranges' keys fit and of which the device holds
-  //    all at once: two CTAs an SM with up to kSelKeys2 keys each, one with up to kSelKeys1 (32 heads of 128K slots in
-  //    clusters of 4: 54 us, of 8 in several waves 109);
+  //    all at once: two CTAs an SM with up to kSelKeys2 keys each, one with up to kSelKeys1 (32 heads of 128K slots, 17K
+  //    a CTA: 54 us by two CTAs an SM, 109 by one in three waves);
   //  - a CTA a head with up to kSelKeys1, in several waves (160 heads of 20K slots: 81 us; read again in every pass, by
   //    two CTAs an SM, 91);
   //  - two CTAs an SM, in the largest clusters that the device holds at once; what does not fit is read again in every
